@@ -14,6 +14,9 @@ Functions with the C names take torch tensors (device buffers) and Python ints:
     dflash_release / dflash_truncate / dflash_context_len / dflash_export_kv / dflash_destroy
 
 `Context` wraps the same calls as methods and allocates outputs when asked to.
+
+Without a context, for a cache that the caller owns (8-bit pages planned, written and read on
+the GPU): page_plan, Rope / rope, KV8Cache, kv8_append, kv8_read, kv8_attention.
 """
 import ctypes
 
@@ -24,7 +27,8 @@ from . import _ffi
 __all__ = ["DFlashError", "Context", "Limits", "dflash_create", "dflash_destroy",
            "dflash_inject_context", "dflash_inject_blocks", "dflash_draft_step", "dflash_verify_greedy",
            "dflash_release", "dflash_truncate", "dflash_context_len", "dflash_export_kv",
-           "dflash_validate_config", "make_config", "library"]
+           "dflash_validate_config", "make_config", "library",
+           "KV8Cache", "Rope", "page_plan", "rope", "kv8_append", "kv8_read", "kv8_attention", "kv8_workspace"]
 
 
 class DFlashError(RuntimeError):
@@ -423,3 +427,7 @@ def dflash_context_len(ctx: Context, req_id):
 
 def dflash_export_kv(ctx: Context, req_id, layer, pos0, n, stream=None):
     return ctx.export_kv(req_id, layer, pos0, n, stream=stream)
+
+
+from .kv8 import (KV8Cache, Rope, kv8_append, kv8_attention, kv8_read, kv8_workspace, page_plan,  # noqa: E402
+                  rope)

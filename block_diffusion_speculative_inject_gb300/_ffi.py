@@ -43,8 +43,32 @@ class DraftOut(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("sel_uniform", "sel_q_tok", "sel_q_p", "sel_q_n")]
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot_dim", "interleaved", "scaling")] + [
+        (n, ctypes.c_float) for n in ("theta", "factor", "original_positions", "beta_fast", "beta_slow")]
+
+
+class RopeTable(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64 * 128), ("magnitude", ctypes.c_float), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class KV8Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_pages", "n_kv_heads", "head_dim")] + [
+        (n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale")]
+
+
+class KV8Attn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_req", "rows", "n_q_heads", "max_blocks", "max_q", "dtype", "mask",
+                                              "tree_words")] + [
+        ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("cu_q", "ctx_len", "block_table", "tree_mask", "out", "lse", "workspace")] + [
+        ("workspace_bytes", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _I32P = ctypes.POINTER(ctypes.c_int32)
 
 SIGNATURES = {
@@ -65,6 +89,14 @@ SIGNATURES = {
     "dflash_verify_sample_q": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dflash_select_sample": (_I32, [_P, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P, _P, _P, _P,
                                     _P, _P, _P, _P, _P]),
+    "dflash_page_plan": (_I32, [_P, _I32, _I32, _I32, _I32] + [_P] * 11),
+    "dflash_rope_init": (_I32, [ctypes.POINTER(RopeParams), ctypes.POINTER(RopeTable)]),
+    "dflash_rope_apply": (_I32, [_P, ctypes.POINTER(RopeTable), _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _I64, _P,
+                                 _I64, _P, _I64, _P, _I64]),
+    "dflash_kv8_append": (_I32, [_P, ctypes.POINTER(KV8Cache), _I32, _I32, _P, _I64, _P, _I64, _P]),
+    "dflash_kv8_read": (_I32, [_P, ctypes.POINTER(KV8Cache), _I32, _P, _P, _P]),
+    "dflash_kv8_attention_workspace": (_I64, [ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Attn)]),
+    "dflash_kv8_attention": (_I32, [_P, ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Attn)]),
     "dflash_release": (_I32, [_P, _I32]),
     "dflash_truncate": (_I32, [_P, _I32, _I32]),
     "dflash_context_len": (_I32, [_P, _I32, _I32P]),

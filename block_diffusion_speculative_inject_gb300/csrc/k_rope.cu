@@ -1,0 +1,218 @@
+// Rotary positions (dflash_rope_init / dflash_rope_apply).
+//
+// Pair i turns by position * f_i. The host keeps F_i = frac(f_i / 2 pi) * 2^64; the 64-bit
+// product position * F_i, whose overflow drops whole turns, is then the angle as a fraction of a
+// turn. Its error is position * 2^-55 turns (F_i comes from a double), below fp32's own for
+// every int32 position, and there is no table: no memory, no position limit.
+//
+// Every element of q and k is read and written once, which bounds it: the sine and cosine of a
+// row's pairs (at most 128) are computed once in shared memory and used by all of its heads.
+#include <cmath>
+
+#include "kv8.cuh"
+
+namespace dflash {
+
+constexpr int ROPE_THREADS = 256;
+
+struct RopeArgs {
+  uint64_t turn[128];
+  float magnitude;
+  int rot, rows, nq, nk, hd, transpose;
+  const int32_t *positions;
+  const void *q, *k;
+  void *qo, *ko;
+  int64_t qs, ks, qos, kos;
+};
+
+// (cos, sin) of a phase in units of 2^-64 turns: the nearest quarter turn is split off exactly,
+// the rest, at most an eighth of a turn, goes to sincospif
+__device__ __forceinline__ float2 phase_cs(uint64_t ph) {
+  const uint32_t quarter = (uint32_t)((ph + (1ull << 61)) >> 62);
+  const int64_t rest = (int64_t)(ph - ((uint64_t)quarter << 62));
+  float s, c;
+  sincospif((float)rest * 0x1p-63f, &s, &c);
+  if (quarter & 1) {
+    const float t = c;
+    c = -s;
+    s = t;
+  }
+  return (quarter & 2) ? make_float2(-c, -s) : make_float2(c, s);
+}
+
+// the turned pair; one contraction for every instance, so that all of them give the same bits
+__device__ __forceinline__ float2 turned(float x, float y, float2 k) {
+  return make_float2(fmaf(x, k.x, -__fmul_rn(y, k.y)), fmaf(y, k.x, __fmul_rn(x, k.y)));
+}
+
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Vec {
+  T v[N];
+};
+
+// ROWS rows of a CTA; V elements per access (16 bytes, or one element where a row, a head or the
+// rotated part does not keep 16-byte alignment).
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ RopeArgs a, int rows_per_cta) {
+  extern __shared__ float2 cs[];                      // [rows][pairs]
+  pdl_trigger();
+  pdl_wait();
+  const int pairs = a.rot / 2;
+  const int r0 = blockIdx.x * rows_per_cta, nr = min(rows_per_cta, a.rows - r0);
+  for (int i = threadIdx.x; i < nr * pairs; i += ROPE_THREADS) {
+    const int r = i / pairs, p = i - r * pairs;
+    float2 t = phase_cs((uint64_t)(int64_t)a.positions[r0 + r] * a.turn[p]);
+    t.x *= a.magnitude;
+    t.y *= a.transpose ? -a.magnitude : a.magnitude;
+    cs[i] = t;
+  }
+  __syncthreads();
+  // Chunks of a head: the half layout takes V dims of the first half with their partners, the
+  // interleaved one V neighbouring dims (V / 2 pairs, one pair where V is 1); then the copied tail.
+  constexpr int IW = INTER && V == 1 ? 2 : V;         // dims of an interleaved chunk
+  const int rot_chunks = INTER ? a.rot / IW : pairs / V;
+  const int chunks = rot_chunks + (a.hd - a.rot) / V;
+  const int per_row = (a.nq + a.nk) * chunks;
+  for (int i = threadIdx.x; i < nr * per_row; i += ROPE_THREADS) {
+    const int r = i / per_row, w = i - r * per_row;
+    int h = w / chunks;
+    const int c = w - h * chunks;
+    const bool isk = h >= a.nq;
+    if (isk) h -= a.nq;
+    const T *src = isk ? (const T *)a.k + (size_t)(r0 + r) * a.ks : (const T *)a.q + (size_t)(r0 + r) * a.qs;
+    T *dst = isk ? (T *)a.ko + (size_t)(r0 + r) * a.kos : (T *)a.qo + (size_t)(r0 + r) * a.qos;
+    src += (size_t)h * a.hd;
+    dst += (size_t)h * a.hd;
+    const float2 *t = cs + r * pairs;
+    typedef Vec<T, V> VT;
+    if (c >= rot_chunks) {
+      const int d = a.rot + (c - rot_chunks) * V;
+      if (src != dst) *(VT *)(dst + d) = *(const VT *)(src + d);
+    } else if (INTER) {
+      const int d = c * IW;
+      if constexpr (V == 1) {
+        const float2 z = turned(to_f(src[d]), to_f(src[d + 1]), t[c]);
+        dst[d] = from_f<T>(z.x);
+        dst[d + 1] = from_f<T>(z.y);
+      } else {
+        VT x = *(const VT *)(src + d);
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+          const float2 z = turned(to_f(x.v[j]), to_f(x.v[j + 1]), t[(d + j) / 2]);
+          x.v[j] = from_f<T>(z.x);
+          x.v[j + 1] = from_f<T>(z.y);
+        }
+        *(VT *)(dst + d) = x;
+      }
+    } else {
+      const int d = c * V;
+      VT x = *(const VT *)(src + d), y = *(const VT *)(src + d + pairs);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 z = turned(to_f(x.v[j]), to_f(y.v[j]), t[d + j]);
+        x.v[j] = from_f<T>(z.x);
+        y.v[j] = from_f<T>(z.y);
+      }
+      *(VT *)(dst + d) = x;
+      *(VT *)(dst + d + pairs) = y;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_rope(const RopeArgs &a, bool inter, bool vec, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int rows_per_cta = 1;
+  const dim3 g((a.rows + rows_per_cta - 1) / rows_per_cta), b(ROPE_THREADS);
+  const size_t sm = (size_t)rows_per_cta * (a.rot / 2) * sizeof(float2);
+  if (vec) return inter ? launch_pdl(k_rope<T, V, true>, g, b, sm, s, a, rows_per_cta)
+                        : launch_pdl(k_rope<T, V, false>, g, b, sm, s, a, rows_per_cta);
+  return inter ? launch_pdl(k_rope<T, 1, true>, g, b, sm, s, a, rows_per_cta)
+               : launch_pdl(k_rope<T, 1, false>, g, b, sm, s, a, rows_per_cta);
+}
+
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" dflash_status dflash_rope_init(const dflash_rope_params *p, dflash_rope *rope) {
+  if (!p || !rope || p->rot_dim < 2 || p->rot_dim > 256 || p->rot_dim % 2 || (p->interleaved & ~1) ||
+      p->scaling < DFLASH_ROPE_NONE || p->scaling > DFLASH_ROPE_YARN || !(p->theta > 1.f) || !std::isfinite(p->theta))
+    return DFLASH_ERR_INVALID_ARG;
+  if (p->scaling != DFLASH_ROPE_NONE && (!(p->factor >= 1.f) || !std::isfinite(p->factor))) return DFLASH_ERR_INVALID_ARG;
+  if (p->scaling == DFLASH_ROPE_YARN &&
+      (!(p->original_positions > 0.f) || !std::isfinite(p->original_positions) || !(p->beta_slow > 0.f) ||
+       !(p->beta_fast > p->beta_slow) || !std::isfinite(p->beta_fast)))
+    return DFLASH_ERR_INVALID_ARG;
+  const double pi = 3.14159265358979323846, rot = p->rot_dim, lt = std::log((double)p->theta);
+  double lo = 0, hi = 0;
+  if (p->scaling == DFLASH_ROPE_YARN) {
+    auto dim = [&](double beta) { return rot * std::log(p->original_positions / (beta * 2 * pi)) / (2 * lt); };
+    lo = std::fmax(std::floor(dim(p->beta_fast)), 0.0);
+    hi = std::fmin(std::ceil(dim(p->beta_slow)), rot - 1);
+  }
+  for (int i = 0; i < 128; ++i) {
+    rope->turn[i] = 0;
+    if (i >= p->rot_dim / 2) continue;
+    double f = std::exp(-2.0 * i / rot * lt);
+    if (p->scaling == DFLASH_ROPE_LINEAR) f /= p->factor;
+    if (p->scaling == DFLASH_ROPE_YARN) {
+      const double g = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      f = f / p->factor * g + f * (1 - g);
+    }
+    // f <= 1, so the fraction of a turn is below 0.16 and fits 64 bits
+    rope->turn[i] = (uint64_t)(f / (2 * pi) * 0x1p64);
+  }
+  rope->magnitude = p->scaling == DFLASH_ROPE_YARN ? (float)(0.1 * std::log((double)p->factor) + 1.0) : 1.f;
+  rope->rot_dim = p->rot_dim;
+  rope->interleaved = p->interleaved;
+  return DFLASH_OK;
+}
+
+extern "C" dflash_status dflash_rope_apply(void *stream, const dflash_rope *rope, int32_t rows, int32_t n_q_heads,
+                                           int32_t n_k_heads, int32_t head_dim, dflash_dtype dtype,
+                                           const int32_t *positions, int32_t transpose, const void *q,
+                                           int64_t q_stride, const void *k, int64_t k_stride, void *q_out,
+                                           int64_t q_out_stride, void *k_out, int64_t k_out_stride) {
+  if (!rope || rows < 0 || n_q_heads < 1 || n_k_heads < 0 || n_q_heads > (1 << 20) || n_k_heads > (1 << 20) ||
+      n_q_heads + n_k_heads > (1 << 20) || (dtype != DFLASH_F32 && dtype != DFLASH_BF16) || (transpose & ~1) ||
+      rope->rot_dim < 2 || rope->rot_dim % 2 || rope->rot_dim > head_dim || head_dim > 256 || (rope->interleaved & ~1))
+    return DFLASH_ERR_INVALID_ARG;
+  const int nk = k ? n_k_heads : 0;
+  const int64_t qw = (int64_t)n_q_heads * head_dim, kw = (int64_t)nk * head_dim;
+  if (q_stride < qw || q_out_stride < qw || (nk && (k_stride < kw || k_out_stride < kw))) return DFLASH_ERR_INVALID_ARG;
+  if (rows == 0) return DFLASH_OK;
+  const unsigned es = dtype_bytes(dtype);
+  if (!positions || !q || !q_out || (nk && !k_out) || !aligned(positions, 4) || !aligned(q, es) || !aligned(q_out, es) ||
+      (nk && (!aligned(k, es) || !aligned(k_out, es))))
+    return DFLASH_ERR_INVALID_ARG;
+  if ((q == q_out && q_stride != q_out_stride) || (nk && k == k_out && k_stride != k_out_stride))
+    return DFLASH_ERR_INVALID_ARG;
+  RopeArgs a;
+  for (int i = 0; i < 128; ++i) a.turn[i] = rope->turn[i];
+  a.magnitude = rope->magnitude;
+  a.rot = rope->rot_dim;
+  a.rows = rows;
+  a.nq = n_q_heads;
+  a.nk = nk;
+  a.hd = head_dim;
+  a.transpose = transpose;
+  a.positions = positions;
+  a.q = q;
+  a.k = k;
+  a.qo = q_out;
+  a.ko = k_out;
+  a.qs = q_stride;
+  a.ks = k_stride;
+  a.qos = q_out_stride;
+  a.kos = k_out_stride;
+  // 16-byte accesses need every row, every head and both rotated halves on 16 bytes
+  const int V = 16 / es;
+  bool vec = aligned(q, 16) && aligned(q_out, 16) && q_stride % V == 0 && q_out_stride % V == 0 && head_dim % V == 0 &&
+             a.rot % (rope->interleaved ? V : 2 * V) == 0;
+  if (nk) vec = vec && aligned(k, 16) && aligned(k_out, 16) && k_stride % V == 0 && k_out_stride % V == 0;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == DFLASH_BF16 ? launch_rope<bf16>(a, rope->interleaved, vec, st)
+                                             : launch_rope<float>(a, rope->interleaved, vec, st);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}

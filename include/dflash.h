@@ -356,6 +356,148 @@ dflash_status dflash_ddtree_walk(void *stream, int32_t n_req, int32_t L, int32_t
                                  const int32_t *n_nodes, const int32_t *target_next,
                                  int32_t *accept_len, int32_t *out_tokens, int32_t *next_anchor);
 
+/* ---- The 8-bit paged cache: caller-owned pages, planned, written and read on the GPU ----
+ * The context above owns its cache and plans its pages on the host. The calls below serve a
+ * cache that the caller owns (a target model's, or a draft's of its own): block tables and slot
+ * maps are made on the GPU from lengths that are on the GPU (the accept lengths of a verify call,
+ * say), so that a round of verification needs no read-back. They need no context, run on the
+ * current device, take DEVICE pointers (16-byte aligned unless said otherwise) and allocate
+ * nothing, so they can be captured into a graph; only dflash_rope_init is a host call.
+ *
+ * dflash_page_plan: n_req requests change their lengths by n_new[b] tokens (negative: the last
+ * -n_new[b] tokens go, all of them at most) and get or give back pages of 64 tokens.
+ *   ctx_len [n_req], n_new [n_req] int32; block_table [n_req, max_blocks] int32, entry i the page
+ *   of tokens 64 i .. 64 i + 63; free_list [n_pages] int32, a stack whose first n_free[0] entries
+ *   are the free pages (n_free [1] int32).
+ * Given back pages (whole pages past the new end) are pushed in request order; then the requests
+ * that grow pop theirs off the top, in request order. A request is refused, and keeps its length,
+ * when its new length needs more than max_blocks pages, when the pages asked for by it and the
+ * requests before it are more than there are, or when their rows are more than max_rows.
+ *   Outputs: new_len [n_req], n_free_out [1], cu_rows [n_req + 1] (prefix sums of the rows that
+ *   were granted), refused [n_req] (1 or 0), and for each new row in request order slot_map
+ *   [max_rows] int64 = page * 64 + offset and positions [max_rows] int32; rows past the last
+ *   one get slot -1 and position 0. block_table and free_list are updated in place: entries of
+ *   new pages and pushed pages are written, every other entry stays as it was.
+ * The outputs must not be the inputs (a call can be repeated on the same inputs).
+ * Limits: 1 <= n_req <= 4096, max_rows >= 0, max_blocks and n_pages in [1, 2^24]. Lengths outside
+ * [0, 64 max_blocks] are read as the nearest end. 4-byte alignment (slot_map: 8). */
+dflash_status dflash_page_plan(void *stream, int32_t n_req, int32_t max_blocks, int32_t n_pages, int32_t max_rows,
+                               const int32_t *ctx_len, const int32_t *n_new, int32_t *block_table,
+                               int32_t *free_list, const int32_t *n_free, int32_t *new_len, int32_t *n_free_out,
+                               int32_t *cu_rows, int32_t *refused, int64_t *slot_map, int32_t *positions);
+
+/* Rotary positions. Pair i < rot_dim / 2 of a head, (x[i], x[i + rot_dim / 2]) in the half layout
+ * or (x[2 i], x[2 i + 1]) interleaved, turns by position * f_i; dims from rot_dim on are copied.
+ * f_i = theta^(-2 i / rot_dim), scaled for contexts longer than those trained on:
+ *   DFLASH_ROPE_LINEAR  f_i / factor (position interpolation);
+ *   DFLASH_ROPE_YARN    f_i ((1 - g_i) + g_i / factor) with the ramp g_i = clamp((i - lo) / (hi - lo))
+ *     between the pairs that make beta_fast and beta_slow turns over original_positions,
+ *     lo = floor(d(beta_fast)) >= 0, hi = ceil(d(beta_slow)) <= rot_dim - 1, d(b) = rot_dim
+ *     ln(original_positions / (2 pi b)) / (2 ln theta); the rotated dims are multiplied by
+ *     0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN", 3.2-3.4).
+ * Angles are kept as 64-bit fixed-point fractions of a turn, so that they are as exact at the
+ * last int32 position as at the first. */
+typedef enum { DFLASH_ROPE_NONE = 0, DFLASH_ROPE_LINEAR = 1, DFLASH_ROPE_YARN = 2 } dflash_rope_scaling;
+typedef struct {
+  int32_t rot_dim;             /* even, 2 .. 256                                          */
+  int32_t interleaved;         /* 0: halves, 1: neighbours                                */
+  int32_t scaling;             /* dflash_rope_scaling                                     */
+  float theta;                 /* > 1                                                     */
+  float factor;                /* >= 1 (read for LINEAR and YARN)                         */
+  float original_positions;    /* > 0; the rest is read for YARN                          */
+  float beta_fast, beta_slow;  /* beta_fast > beta_slow > 0 (commonly 32 and 1)           */
+} dflash_rope_params;
+typedef struct {
+  uint64_t turn[128];          /* f_i / 2 pi modulo 1, times 2^64                         */
+  float magnitude;
+  int32_t rot_dim, interleaved;
+} dflash_rope;
+
+/* Fills *rope (host only; keep it as long as the model). INVALID_ARG: see the fields. */
+dflash_status dflash_rope_init(const dflash_rope_params *params, dflash_rope *rope);
+
+/* Rotates q [rows, n_q_heads, head_dim] into q_out and, if k != NULL, k [rows, n_k_heads, head_dim]
+ * into k_out, row r by positions[r] (int32, any sign). Rows are *_stride elements apart, heads are
+ * contiguous; q_out / k_out may be q / k themselves (with the same stride) but must not overlap
+ * them otherwise. transpose = 1 applies the transposed map, which carries gradients of the
+ * outputs back to the inputs. Any alignment that fits the type; 16-byte aligned rows are faster.
+ * Limits: rot_dim <= head_dim <= 256, strides >= heads * head_dim, n_q_heads + n_k_heads <= 2^20. */
+dflash_status dflash_rope_apply(void *stream, const dflash_rope *rope, int32_t rows, int32_t n_q_heads,
+                                int32_t n_k_heads, int32_t head_dim, dflash_dtype dtype, const int32_t *positions,
+                                int32_t transpose, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride);
+
+/* A cache in 8 bits (e4m3), one scale per page of 64 tokens and kv head for K and for V:
+ *   k_pages [n_pages, n_kv_heads, 64, head_dim], v_pages [n_pages, n_kv_heads, head_dim, 64] (V is
+ *   kept transposed, as in the context's own pool), k_scale / v_scale [n_pages, n_kv_heads] fp32.
+ * A value is byte * scale. Scales are powers of two, 2^-64 or more: scaling is exact, and so is
+ * re-scaling, but for values that fall below the type's range.
+ * Limits: head_dim 64 or 128, n_pages in [1, 2^24], n_kv_heads in [1, 128]. */
+typedef struct {
+  int32_t n_pages, n_kv_heads, head_dim;
+  void *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+} dflash_kv8_cache;
+
+/* Writes rows of k and v [rows, n_kv_heads, head_dim] (row strides in elements, multiples of
+ * 16 bytes) at slot_map [rows] int64; rows whose slot is outside [0, 64 n_pages) are skipped.
+ * A page's rows must be consecutive in slot_map (as dflash_page_plan makes them; skipped rows may
+ * lie between); of rows with the same slot the last one stays. Offset 0 among a page's rows starts
+ * the page afresh: its scale is the smallest power of two s with |x| <= 448 s over its new rows. Else
+ * the scale is the larger of that and the one it has, and where it grows the rows below the last
+ * new one that are not written are rounded anew to it. Infinities are stored as +-448 s and have no say in
+ * the scale, NaN is stored as NaN. */
+dflash_status dflash_kv8_append(void *stream, const dflash_kv8_cache *cache, int32_t rows, dflash_dtype dtype,
+                                const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const int64_t *slot_map);
+
+/* The values at slot_map [rows] as fp32 k_out / v_out [rows, n_kv_heads, head_dim] (inspection);
+ * rows whose slot is outside [0, 64 n_pages) read as zero. */
+dflash_status dflash_kv8_read(void *stream, const dflash_kv8_cache *cache, int32_t rows, const int64_t *slot_map,
+                              float *k_out, float *v_out);
+
+/* Attention of rows cu_q[b] .. cu_q[b+1] - 1 of q (request b) over the first ctx_len[b] cached tokens
+ * of block_table [n_req, max_blocks]; query head h reads kv head h / (n_q_heads / n_kv_heads):
+ *   out = softmax(scale q K^T) V over the visible tokens, lse = ln sum exp(scale q K^T).
+ * Row i of a request with n rows and length len sees token p when
+ *   DFLASH_MASK_NONE    p < len;
+ *   DFLASH_MASK_CAUSAL  p <= len - n + i (its rows are the context's last n tokens);
+ *   DFLASH_MASK_TREE    p < len - n, or bit p - (len - n) of tree_mask row cu_q[b] + i is set
+ *                       ([rows, tree_words] uint32; the masks of dflash_ddtree_build).
+ * A row that sees nothing gets out = 0 and lse = -infinity. What is stored at tokens that a row does
+ * not see, NaN included, does not reach it. A row of q with an infinity or NaN gives NaN. Tokens on a
+ * page outside [0, n_pages) are not seen. Rows past cu_q[n_req] stay as they were.
+ * Sums, maxima and normalisers are fp32. bf16: products of exact 8- or 16-bit operands, softmax weights
+ * rounded to 11 bits, one rounding of the output. fp32: operands split in two 11-bit parts.
+ *   max_q: the most rows of a request as far as the host knows; it only steers the choice of kernel.
+ *   workspace: dflash_kv8_attention_workspace() bytes, 256-byte aligned; contents do not matter
+ *   before or after. Calls that may overlap (two streams, two graphs) need one each.
+ * Limits: n_q_heads a multiple of n_kv_heads, at most 8 per kv head; 1 <= n_req <= 4096; scale
+ * finite and > 0; q_stride >= n_q_heads * head_dim, rows 16-byte aligned; out [rows, n_q_heads,
+ * head_dim] of q's type, lse [rows, n_q_heads] fp32 or NULL. max_blocks in [1, 2^24]; ctx_len is read as at most
+ * 64 max_blocks, cu_q as rising within [0, rows]. */
+typedef enum { DFLASH_MASK_NONE = 0, DFLASH_MASK_CAUSAL = 1, DFLASH_MASK_TREE = 2 } dflash_mask;
+typedef struct {
+  int32_t n_req, rows, n_q_heads, max_blocks, max_q;
+  dflash_dtype dtype;
+  int32_t mask;                /* dflash_mask */
+  int32_t tree_words;
+  float scale;
+  const void *q;
+  int64_t q_stride;
+  const int32_t *cu_q, *ctx_len, *block_table;
+  const uint32_t *tree_mask;
+  void *out;
+  float *lse;
+  void *workspace;
+  int64_t workspace_bytes;
+} dflash_kv8_attn;
+
+/* Bytes of workspace for this cache and these arguments (host only; -1: invalid arguments).
+ * Pointers are not looked at. */
+int64_t dflash_kv8_attention_workspace(const dflash_kv8_cache *cache, const dflash_kv8_attn *args);
+dflash_status dflash_kv8_attention(void *stream, const dflash_kv8_cache *cache, const dflash_kv8_attn *args);
+
 /* Forgets a request and returns its pages to the pool (host only). Work already
  * enqueued that reads those pages must precede any later call in stream order. */
 dflash_status dflash_release(dflash_ctx *ctx, int32_t req_id);

@@ -1,0 +1,637 @@
+"""The 8-bit paged cache on the GPU (page planning, rotary positions, quantised append, attention) against
+64-bit references (kv8_reference.py), alone and run together as a verify loop runs them.
+
+Tolerances (half steps: bf16 2^-8, f16 2^-11, fp32 2^-24, relative to the value):
+  rope      one rounding of the output, plus (|x| + |y|) * magnitude * 8e-7 for fp32: the reduced angle
+            (at most pi/4) is rounded once (2^-24 * 0.79 = 5e-8), sine and cosine are within 2 ulp (2.4e-7),
+            and three fp32 roundings add 1.8e-7; times 2 for the two terms is under 1e-6.
+  append    bytes and scales are equal: scaling by a power of two is exact and there is one rounding.
+  attention per output: its own rounding, plus with A = sum p |v| (p the softmax weights) and
+            D = max sum_d |q_d k_d| scale: the weights' 11-bit (fp32: 22-bit) rounding r = 2^-11 (2^-20),
+            and their error from the scores, 2 (D 2^-19 + 2^-19): fp32 sums over at most 128 terms in
+            pieces that may truncate (16 2^-23 = 2^-19) and exp2's 2^-22 with its argument's rounding.
+  lse       D 2^-19 + |lse| 2^-22 + (L + 32) 2^-24: a positive fp32 sum over at most L terms.
+"""
+import math
+
+import pytest
+import torch
+
+import kv8_reference as R
+
+pytestmark = pytest.mark.gpu
+
+PAGE = 64
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from block_diffusion_speculative_inject_gb300 import build
+    build.build()
+
+
+def _i4(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _cum(v):
+    out = [0]
+    for x in v:
+        out.append(out[-1] + x)
+    return out
+
+
+# ---------------------------------------------------------------- page planning
+def _plan_inputs(seed, n, width, ctx_max, spare):
+    g = torch.Generator().manual_seed(seed)
+    ctx = torch.randint(0, ctx_max + 1, (n,), generator=g).tolist()
+    used = sum(R.pages_of(c) for c in ctx)
+    perm = torch.randperm(used + spare, generator=g).tolist()
+    table, at = [], 0
+    for c in ctx:
+        k = R.pages_of(c)
+        table.append(perm[at:at + k] + [-7] * (width - k))
+        at += k
+    return g, ctx, table, perm[at:], used + spare
+
+
+@pytest.mark.parametrize("n,width,ctx_max,lo,hi,spare,max_rows", [
+    (1, 1, 0, 0, 0, 1, 0), (1, 1, 64, 1, 1, 1, 1), (1, 40, 100, 2000, 2000, 50, 2000), (5, 6, 300, -64, 70, 20, 400),
+    (33, 4, 200, -300, 100, 10, 900), (128, 30, 1536, 1, 8, 200, 1024), (700, 3, 150, -20, 20, 90, 5000),
+    (4096, 2, 100, -5, 9, 500, 9000), (513, 9, 500, -600, 70, 0, 1 << 15), (32, 130, 0, 512, 8192, 4000, 140000),
+    (1025, 5, 300, 1, 64, 300, 20000), (3, 1 << 12, 64, 60, 90, 9, 200)])
+def test_page_plan(n, width, ctx_max, lo, hi, spare, max_rows):
+    """Refusals (too few pages, rows or blocks), releases and grants at once; twice on the same inputs."""
+    from block_diffusion_speculative_inject_gb300 import page_plan
+    g, ctx, table, free, n_pages = _plan_inputs(n * 7 + hi, n, width, min(ctx_max, width * PAGE), spare)
+    add = torch.randint(lo, hi + 1, (n,), generator=g).tolist()
+    t_in, st = _i4(table), _i4(free + [-3] * (n_pages - len(free)))
+    ctx_d, add_d, nf = _i4(ctx), _i4(add), _i4([len(free)])
+    stack = list(free)
+    want_t = [list(r) for r in table]
+    new, cu, slot, pos, refused = R.plan(ctx, add, want_t, stack, max_rows)
+    for _ in range(2):
+        p = page_plan(ctx_d, add_d, t_in, st, nf, max_rows)
+        assert p["new_len"].tolist() == new
+        assert p["refused"].tolist() == refused
+        assert p["cu_rows"].tolist() == cu
+        assert p["n_free"].tolist() == [len(stack)]
+        assert p["slot_map"].tolist() == slot + [-1] * (max_rows - len(slot))
+        assert p["positions"].tolist() == pos + [0] * (max_rows - len(pos))
+        assert t_in.tolist() == want_t
+        assert st[:len(stack)].tolist() == stack
+    gone = sum(max(0, R.pages_of(c) - R.pages_of(x)) for c, x in zip(ctx, new))
+    assert st[len(free) + gone:].tolist() == [-3] * (n_pages - len(free) - gone)     # the rest of the stack stays
+
+
+def test_page_plan_corrupt_lengths_stay_in_bounds():
+    """Lengths and counts outside their range are read as the nearest end."""
+    from block_diffusion_speculative_inject_gb300 import page_plan
+    table = _i4([[0, 1], [2, 3], [4, 5]])
+    p = page_plan(_i4([-5, 1 << 30, 64]), _i4([3, -(1 << 31), (1 << 31) - 1]), table, _i4([6, 7, 8, 9, 10, 11]), _i4([99]), 10)
+    assert p["new_len"].tolist() == [3, 0, 64] and p["refused"].tolist() == [0, 0, 1]
+    assert p["cu_rows"].tolist() == [0, 3, 3, 3]
+    assert p["slot_map"].tolist()[:3] == [11 * 64, 11 * 64 + 1, 11 * 64 + 2]
+
+
+# ---------------------------------------------------------------- rotary positions
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,nq,nk,hd,rot,inter,scaling", [
+    (1, 1, 0, 64, 64, False, "none"), (3, 5, 2, 128, 128, False, "yarn"), (17, 40, 8, 128, 64, True, "linear"),
+    (65, 3, 1, 64, 20, False, "none"), (9, 4, 4, 64, 20, True, "yarn"), (5, 2, 1, 96, 32, False, "none"),
+    (4, 2, 2, 50, 50, True, "none"), (4, 1, 1, 50, 18, False, "linear"), (2, 1, 0, 256, 256, False, "none"),
+    (700, 8, 2, 64, 64, True, "none"), (31, 1, 1, 7, 2, False, "none")])
+def test_rope(dtype, rows, nq, nk, hd, rot, inter, scaling):
+    from block_diffusion_speculative_inject_gb300 import Rope, rope
+    g = torch.Generator().manual_seed(rows * 31 + hd)
+    kw = dict(none={}, linear=dict(factor=2.5), yarn=dict(factor=4.0, original_positions=4096.0))[scaling]
+    t = Rope(hd, rot_dim=rot, theta=1e4, interleaved=inter, scaling=scaling, **kw)
+    rk = {("original" if k == "original_positions" else k): v for k, v in kw.items()}
+    freq, mag = R.rope_freq(rot, 1e4, scaling, **rk)
+    pos = torch.randint(0, 1 << 18, (rows,), generator=g, dtype=torch.int32)
+    pos[0] = 0
+    pos[-1] = (1 << 24) - 1
+    q = torch.randn((rows, nq, hd), generator=g).to(dtype)
+    k = torch.randn((rows, nk, hd), generator=g).to(dtype) if nk else None
+    for transpose in (False, True):
+        got = rope(t, pos.cuda(), q.cuda(), k.cuda() if nk else None, transpose=transpose)
+        for x, y in ((q, got[0]), (k, got[1])):
+            if x is None:
+                assert y is None
+                continue
+            want = R.rope(x.double(), pos.tolist(), rot, freq, mag, inter, transpose)
+            size = R.rope(x.double().abs(), [0] * rows, rot, freq, mag, inter) * 0 + x.double().abs().amax(-1, keepdim=True)
+            tol = want.abs() * HALF[dtype] + 2 * size * mag * 8e-7
+            tol[..., rot:] = 0
+            assert bool(((y.cpu().double() - want).abs() <= tol).all())
+
+
+def test_rope_far_and_negative_positions():
+    """The last and first int32 positions. The frequencies are doubles good to 2^-51: their error times the
+    position, 2 pi * 0.16 * 2^31 * 2^-51 = 1e-6, joins the tolerance."""
+    from block_diffusion_speculative_inject_gb300 import Rope, rope
+    freq, mag = R.rope_freq(128, 1e6)
+    pos = torch.tensor([2 ** 31 - 1, 2 ** 31 - 2, -2 ** 31, -1, -77777, 123456789], dtype=torch.int32)
+    x = torch.randn((6, 2, 128), generator=torch.Generator().manual_seed(1))
+    got, _ = rope(Rope(128, theta=1e6), pos.cuda(), x.cuda())
+    want = R.rope(x.double(), pos.tolist(), 128, freq, mag, False)
+    assert bool(((got.cpu().double() - want).abs() <= 2 * x.double().abs().amax(-1, keepdim=True) * 1.8e-6).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_rope_strided_rows_in_place_and_out(dtype, inter, shift):
+    """q and k as columns of one projection's output (shift: not 16-byte aligned), in place and into another buffer
+    with its own stride; what lies between the rows stays."""
+    from block_diffusion_speculative_inject_gb300 import Rope, rope
+    rows, nq, nk, hd, rot = 11, 3, 2, 64, 32
+    g = torch.Generator().manual_seed(5)
+    pos = torch.randint(0, 9999, (rows,), generator=g, dtype=torch.int32).cuda()
+    width = (nq + 2 * nk) * hd + 8
+    buf = torch.randn((rows, width), generator=g).to(dtype).cuda()
+    q = buf[:, shift:shift + nq * hd].unflatten(1, (nq, hd))
+    k = buf[:, shift + nq * hd:shift + (nq + nk) * hd].unflatten(1, (nk, hd))
+    t = Rope(hd, rot_dim=rot, interleaved=inter)
+    want = rope(t, pos, q.contiguous(), k.contiguous())
+    other = torch.full((rows, width + 24), 7.0, dtype=dtype, device="cuda")
+    qo = other[:, 16:16 + nq * hd].unflatten(1, (nq, hd))
+    rope(t, pos, q, k, q_out=qo)
+    assert torch.equal(qo, want[0]) and bool((other[:, :16] == 7).all()) and bool((other[:, 16 + nq * hd:] == 7).all())
+    before = buf.clone()
+    rope(t, pos, q, k, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(buf[:, shift + (nq + nk) * hd:], before[:, shift + (nq + nk) * hd:])
+    assert torch.equal(buf[:, :shift], before[:, :shift])
+
+
+def test_rope_transpose_is_the_gradient():
+    """<R x, y> = <x, R^T y> in fp32, and the transposed call against differences of the forward one
+    (the map is linear, so the difference over any step is the derivative)."""
+    from block_diffusion_speculative_inject_gb300 import Rope, rope
+    g = torch.Generator().manual_seed(2)
+    pos = torch.randint(0, 99999, (5,), generator=g, dtype=torch.int32).cuda()
+    t = Rope(64, rot_dim=48, interleaved=True, scaling="yarn", factor=4.0, original_positions=2048.0)
+    x, y = torch.randn((5, 2, 64), generator=g).cuda(), torch.randn((5, 2, 64), generator=g).cuda()
+    fx, grad = rope(t, pos, x)[0].double(), rope(t, pos, y, transpose=True)[0].double()
+    # fp32 outputs of size up to 1.14 |x|: each within 2e-6 of its value, summed over 640 terms
+    assert abs(float((fx * y.double()).sum() - (x.double() * grad).sum())) < 2e-6 * 640
+    for at in ((0, 0, 0), (4, 1, 47), (2, 0, 63), (3, 1, 20)):
+        d = torch.zeros_like(x)
+        d[at] = 1.0
+        diff = rope(t, pos, x + d)[0].double() - fx
+        assert abs(float((diff * y.double()).sum()) - float(grad[at])) < 1e-4      # 128 outputs, 2 * 4e-7 * |y| each
+
+
+# ---------------------------------------------------------------- quantised append
+def _cache_cpu(seed, n_pages, nkv, hd, poison=True):
+    """A pool with finite random bytes in every page, scales 2^-8 .. 2^-4."""
+    g = torch.Generator().manual_seed(seed)
+    c = {}
+    for name, shape in (("k_pages", (n_pages, nkv, PAGE, hd)), ("v_pages", (n_pages, nkv, hd, PAGE))):
+        c[name] = (torch.randn(shape, generator=g) * 80).clamp(-448, 448).to(R.E4M3)
+    for name in ("k_scale", "v_scale"):
+        c[name] = torch.exp2(torch.randint(-8, -3, (n_pages, nkv), generator=g).float())
+    return c
+
+
+def _to_gpu(c):
+    from block_diffusion_speculative_inject_gb300 import KV8Cache
+    return KV8Cache(*(c[n].cuda().contiguous() for n in ("k_pages", "v_pages", "k_scale", "v_scale")))
+
+
+def _same_cache(gpu, want):
+    for n in ("k_scale", "v_scale"):
+        assert torch.equal(getattr(gpu, n).cpu(), want[n]), n
+    for n in ("k_pages", "v_pages"):
+        a, b = getattr(gpu, n).cpu().float(), want[n].float()
+        assert bool(((a == b) | (a.isnan() & b.isnan())).all()), n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("nkv,spans", [
+    (1, [(0, 0, 1)]), (2, [(3, 63, 1)]), (3, [(1, 17, 16), (2, 0, 64)]), (8, [(0, 1, 63), (5, 0, 30), (4, 40, 5)]),
+    (1, [(i, i % 64, 1 + i % 3) for i in range(60)])])
+def test_append(dtype, hd, nkv, spans):
+    """Spans (page, first offset, rows) in one call: started and fresh pages, grown and unchanged scales; rows of
+    sizes over forty powers of two; skipped rows between."""
+    from block_diffusion_speculative_inject_gb300 import kv8_append
+    n_pages = 64
+    spans = [(p, o, min(n, PAGE - o)) for p, o, n in spans]
+    slots = []
+    for p, o, n in spans:
+        slots += [p * PAGE + o + i for i in range(n)] + ([-1] if p % 2 else []) + ([n_pages * PAGE] if p % 3 == 2 else [])
+    g = torch.Generator().manual_seed(len(slots) + hd)
+    size = torch.exp2(torch.randint(-20, 21, (len(slots), nkv, 1), generator=g).float())
+    k = (torch.randn((len(slots), nkv, hd), generator=g) * size).to(dtype)
+    v = torch.randn((len(slots), nkv, hd), generator=g).to(dtype)
+    want = _cache_cpu(9, n_pages, nkv, hd)
+    gpu = _to_gpu(want)
+    kv8_append(gpu, k.cuda(), v.cuda(), torch.tensor(slots, device="cuda"))
+    R.append(want, k, v, slots)
+    _same_cache(gpu, want)
+
+
+def test_append_long_runs_and_windows():
+    """A prompt over many windows of rows, starting in the middle of a page, then one row at a time."""
+    from block_diffusion_speculative_inject_gb300 import kv8_append
+    n_pages, nkv, hd = 130, 2, 64
+    g = torch.Generator().manual_seed(3)
+    order = torch.randperm(n_pages, generator=g).tolist()
+    slots = [order[p // PAGE] * PAGE + p % PAGE for p in range(29, 29 + 8000)]
+    k, v = (torch.randn((8000, nkv, hd), generator=g).bfloat16() for _ in range(2))
+    want = _cache_cpu(1, n_pages, nkv, hd)
+    gpu = _to_gpu(want)
+    kv8_append(gpu, k.cuda(), v.cuda(), torch.tensor(slots, device="cuda"))
+    R.append(want, k, v, slots)
+    _same_cache(gpu, want)
+    nxt = order[8029 // PAGE] * PAGE + 8029 % PAGE
+    for i in range(4):
+        x = (torch.randn((1, nkv, hd), generator=g) * 4.0 ** i).bfloat16()
+        kv8_append(gpu, x.cuda(), x.cuda(), torch.tensor([nxt + i], device="cuda"))
+        R.append(want, x, x, [nxt + i])
+    _same_cache(gpu, want)
+
+
+def test_append_special_values():
+    """Zeros (scale 2^-64), infinities (saturate, no say in the scale), NaN (kept), the largest and smallest
+    fp32 values, amax on and just above a scale's edge; the last of two rows with one slot stays."""
+    from block_diffusion_speculative_inject_gb300 import kv8_append, kv8_read
+    n_pages, nkv, hd = 8, 1, 64
+    k = torch.zeros((9, nkv, hd))
+    k[1, 0, 3], k[1, 0, 4], k[1, 0, 5], k[1, 0, 6] = math.inf, -math.inf, math.nan, 1.0
+    k[2, 0, 0], k[2, 0, 1] = 3.4e38, 1.0
+    k[3, 0, 0] = 1e-42
+    k[4, 0, 0] = 448.0
+    k[5, 0, 0] = float(torch.nextafter(torch.tensor(448.0), torch.tensor(500.0)))
+    k[6, 0, :] = torch.linspace(-5, 5, hd)
+    k[7, 0, :] = 2.5
+    k[8, 0, :] = 900.0
+    slots = [0, 64, 128, 192, 256, 320, 384 + 5, 384 + 5, 384 + 6]
+    want = _cache_cpu(4, n_pages, nkv, hd)
+    gpu = _to_gpu(want)
+    s = torch.tensor(slots, device="cuda")
+    kv8_append(gpu, k.cuda(), (k * -1).cuda(), s)
+    R.append(want, k, -k, slots)
+    _same_cache(gpu, want)
+    assert gpu.k_scale[0, 0] == 2.0 ** -64 and gpu.k_scale[4, 0] == 1.0 and gpu.k_scale[5, 0] == 2.0
+    rk, rv = kv8_read(gpu, torch.tensor(slots + [-1, n_pages * PAGE], device="cuda"))
+    assert rk[1, 0, 5].isnan() and rk[1, 0, 3] == 448 * gpu.k_scale[1, 0] and bool((rk[9:] == 0).all())
+    for x, name in ((rk, "k"), (rv, "v")):
+        pages = want["k_pages"] if name == "k" else want["v_pages"].transpose(2, 3)
+        for r, sl in enumerate(slots):
+            y = pages[sl // PAGE, 0, sl % PAGE].float() * want[name + "_scale"][sl // PAGE, 0]
+            assert torch.equal(torch.nan_to_num(x[r, 0].cpu(), nan=-9), torch.nan_to_num(y, nan=-9))
+
+
+def test_append_strided_rows_and_padding_tail():
+    """k and v as columns of one buffer; a long tail of skipped rows; pages that are not named stay."""
+    from block_diffusion_speculative_inject_gb300 import kv8_append
+    nkv, hd, rows = 2, 64, 20000
+    buf = torch.randn((rows, 5 * hd), generator=torch.Generator().manual_seed(8)).bfloat16()
+    k, v = buf[:, :2 * hd].unflatten(1, (2, hd)), buf[:, 3 * hd:].unflatten(1, (2, hd))
+    slots = [70 + i for i in range(50)] + [-1] * (rows - 50)
+    want = _cache_cpu(2, 6, nkv, hd)
+    gpu = _to_gpu(want)
+    b = buf.cuda()
+    kv8_append(gpu, b[:, :2 * hd].unflatten(1, (2, hd)), b[:, 3 * hd:].unflatten(1, (2, hd)), torch.tensor(slots, device="cuda"))
+    R.append(want, k, v, slots)
+    _same_cache(gpu, want)
+
+
+# ---------------------------------------------------------------- attention
+NAN_BYTE = 0x7F
+
+
+def _attn_case(seed, ctx, n_q, nkv, hd, nq, mask, dtype, spread=1.5, extra=3):
+    """Inputs with NaN in every place no row may read: unused pages, page tails, unused scales."""
+    g = torch.Generator().manual_seed(seed)
+    n = len(ctx)
+    blocks = [R.pages_of(c) for c in ctx]
+    n_pages = sum(blocks) + extra
+    c = _cache_cpu(seed + 1, n_pages, nkv, hd)
+    perm = torch.randperm(n_pages, generator=g).tolist()
+    width = max(1, max(blocks)) + 1
+    table = torch.full((n, width), -1, dtype=torch.int32)
+    at = 0
+    used = set()
+    for b, k in enumerate(blocks):
+        table[b, :k] = torch.tensor(perm[at:at + k], dtype=torch.int32)
+        used |= set(perm[at:at + k])
+        at += k
+        if ctx[b] % PAGE:
+            p, o = perm[at - 1], ctx[b] % PAGE
+            c["k_pages"].view(torch.uint8)[p, :, o:] = NAN_BYTE
+            c["v_pages"].view(torch.uint8)[p, :, :, o:] = NAN_BYTE
+    for p in range(n_pages):
+        if p not in used:
+            c["k_pages"].view(torch.uint8)[p] = NAN_BYTE
+            c["v_pages"].view(torch.uint8)[p] = NAN_BYTE
+            c["k_scale"][p], c["v_scale"][p] = math.nan, math.nan
+    rows = sum(n_q)
+    q = (torch.randn((rows, nq, hd), generator=g) * spread).to(dtype)
+    tree = None
+    if mask == "tree":
+        words = max(1, -(-max(n_q) // 32))
+        tree = torch.randint(-2 ** 31, 2 ** 31, (rows, words), generator=g).to(torch.int32)
+    return c, table, q, _cum(n_q), tree
+
+
+def _check_attn(c, table, q, cu, ctx, mask, tree, dtype, scale=None, cache=None, max_q=None, **kw):
+    from block_diffusion_speculative_inject_gb300 import kv8_attention
+    gpu = cache or _to_gpu(c)
+    pad = 3                                            # rows past the last request's stay as they were
+    rows, nq, hd = q.shape
+    qg = torch.cat([q, torch.ones((pad, nq, hd), dtype=dtype)]).cuda()
+    out = torch.full((rows + pad, nq, hd), 77.0, dtype=dtype, device="cuda")
+    lse = torch.full((rows + pad, nq), 77.0, device="cuda")
+    tg = torch.cat([tree, torch.zeros((pad, tree.shape[1]), dtype=torch.int32)]).cuda() if tree is not None else None
+    kv8_attention(gpu, qg, _i4(cu), _i4(ctx), table.cuda(), mask=mask, tree_mask=tg, scale=scale, out=out, lse=lse,
+                  max_q=max_q, **kw)
+    out, lse = out.cpu(), lse.cpu()
+    assert bool((out[rows:] == 77).all()) and bool((lse[rows:] == 77).all())
+    want, wl, absv, top = R.attention(c, q, cu, ctx, table, mask, tree, scale)
+    r = 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -20
+    delta = 2 * (top * 2.0 ** -19 + 2.0 ** -19)
+    tol = want.abs() * HALF[dtype] + absv * (r + delta[..., None])
+    err = (out[:rows].double() - want).abs()
+    assert torch.equal(out[:rows].isnan(), want.isnan())
+    bad = ~((err <= tol) | want.isnan())
+    assert not bool(bad.any()), f"{int(bad.sum())} outputs off, worst {float((err / tol.clamp(min=1e-30))[bad].max()):.3g} x"
+    fin = wl.isfinite()
+    assert torch.equal(lse[:rows][~fin].nan_to_num(9.0), wl[~fin].float().nan_to_num(9.0))
+    big = max([1] + list(ctx))
+    ltol = (top * 2.0 ** -19 + wl.abs() * 2.0 ** -22 + (big + 32) * 2.0 ** -24)[fin]
+    assert bool(((lse[:rows].double() - wl).abs()[fin] <= ltol).all())
+    return out[:rows], lse[:rows]
+
+
+RAGGED = [0, 1, 63, 64, 65, 127, 128, 129, 300, 517]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hd,nkv,group", [(128, 2, 4), (64, 1, 1), (128, 1, 5), (64, 2, 8), (128, 1, 7)])
+@pytest.mark.parametrize("mask", ["none", "causal", "tree"])
+@pytest.mark.parametrize("rows", ["one", "block", "many"])
+def test_attention(dtype, hd, nkv, group, mask, rows):
+    """Ragged contexts and row counts (none for some requests, more rows than tokens for others)."""
+    n_q = dict(one=[1] * 10, block=[1, 3, 0, 16, 2, 7, 16, 5, 16, 9], many=[40, 2, 70, 1, 0, 33, 150, 64, 31, 90])[rows]
+    if rows == "many" and (dtype == torch.float32 or group in (1, 7)):
+        n_q = [min(x, 37) for x in n_q]
+    c, table, q, cu, tree = _attn_case(hd + group, RAGGED, n_q, nkv, hd, nkv * group, mask, dtype)
+    _check_attn(c, table, q, cu, RAGGED, mask, tree, dtype, max_q=max(n_q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_q", [[1], [16], [50]])
+def test_attention_one_long_context(dtype, n_q):
+    """One request whose context is split over many workers and merged."""
+    ctx = [9001]
+    c, table, q, cu, tree = _attn_case(77, ctx, n_q, 1, 128, 2, "causal", dtype)
+    _check_attn(c, table, q, cu, ctx, "causal", tree, dtype, max_q=n_q[0])
+
+
+@pytest.mark.parametrize("n_q", [1, 20])
+def test_attention_many_requests(n_q):
+    """More requests than workers, most of them short."""
+    ctx = [(i * 37) % 200 for i in range(400)]
+    c, table, q, cu, tree = _attn_case(5, ctx, [n_q if i % 5 else 0 for i in range(400)], 1, 64, 2, "none", torch.bfloat16)
+    _check_attn(c, table, q, cu, ctx, "none", tree, torch.bfloat16, max_q=n_q)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_q", [3, 40])
+def test_attention_nan_and_infinity_in_hidden_places(dtype, n_q):
+    """Later rows' K and V hold NaN, and one row of q an infinity: rows that do not see them are untouched, a
+    row that sees a NaN in one value dimension has NaN there alone, one that sees a NaN key is NaN."""
+    from block_diffusion_speculative_inject_gb300 import kv8_attention
+    ctx = [100 + n_q, 64 + n_q]
+    c, table, q, cu, _ = _attn_case(3, ctx, [n_q, n_q], 1, 128, 4, "causal", dtype)
+    for b in range(2):
+        pv, pk = 100 + n_q - 2 if b == 0 else 64 + n_q - 1, ctx[b] - 1
+        page, off = int(table[b, pv // PAGE]), pv % PAGE
+        c["v_pages"].view(torch.uint8)[page, 0, 5, off] = NAN_BYTE
+        page, off = int(table[b, pk // PAGE]), pk % PAGE
+        c["k_pages"].view(torch.uint8)[page, 0, off, 9] = 0xFF
+    q[cu[1]] = math.inf
+    gpu = _to_gpu(c)
+    out, lse = kv8_attention(gpu, q.cuda(), _i4(cu), _i4(ctx), table.cuda(), mask="causal", want_lse=True, max_q=n_q)
+    out, lse = out.cpu(), lse.cpu()
+    last = cu[1] - 1
+    assert bool(out[:last - 1].isfinite().all()) and bool(lse[:last].isfinite().all())
+    nan = out[last - 1].isnan()
+    assert bool(nan[:, 5].all()) and int(nan.sum()) == nan.shape[0]
+    assert bool(out[last].isnan().all()) and bool(lse[last].isnan().all())
+    assert bool(out[cu[1]].isnan().all()) and bool(out[cu[1] + 1:-1].isfinite().all()) and bool(out[-1].isnan().all())
+
+
+def test_attention_tree_bits_beyond_the_words_and_pages_out_of_range():
+    """Rows past the mask's words are not seen; tokens on a page outside the pool are not seen."""
+    ctx, n_q = [150, 90], [40, 5]
+    c, table, q, cu, tree = _attn_case(6, ctx, n_q, 1, 64, 2, "tree", torch.bfloat16)
+    table[0, 0], table[1, 1] = 1 << 20, -5
+    _check_attn(c, table, q, cu, ctx, "tree", tree[:, :1].contiguous(), torch.bfloat16, max_q=40)
+    _check_attn(c, table, q, cu, ctx, "none", None, torch.bfloat16, max_q=40)
+
+
+@pytest.mark.parametrize("n_q", [2, 24])
+def test_attention_rows_that_see_nothing(n_q):
+    """A tree whose rows' bits are clear over a context of the rows alone, and an empty context."""
+    ctx = [n_q, 0, 70]
+    c, table, q, cu, tree = _attn_case(6, ctx, [n_q] * 3, 2, 64, 4, "tree", torch.bfloat16)
+    tree[:n_q] = 0
+    out, lse = _check_attn(c, table, q, cu, ctx, "tree", tree, torch.bfloat16, max_q=n_q)
+    assert bool((out[:2 * n_q] == 0).all()) and bool((lse[:2 * n_q] == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_q", [1, 20])
+def test_attention_scales_and_scores_of_very_different_size(dtype, n_q):
+    """Page scales over 2^-64 .. 2^60, peaked and flat scores, one dominant token among thousands of small ones."""
+    ctx = [1500, 400, 2000]
+    c, table, q, cu, tree = _attn_case(12, ctx, [n_q] * 3, 1, 128, 4, "none", dtype)
+    g = torch.Generator().manual_seed(1)
+    fin = c["v_scale"].isfinite()
+    c["v_scale"][fin] = torch.exp2(torch.randint(-64, 61, (int(fin.sum()),), generator=g).float())
+    _check_attn(c, table, q, cu, ctx, "none", tree, dtype, max_q=n_q)
+    c, table, q, cu, tree = _attn_case(13, ctx, [n_q] * 3, 1, 128, 4, "none", dtype, spread=30.0)
+    _check_attn(c, table, q, cu, ctx, "none", tree, dtype, max_q=n_q)
+    c, table, q, cu, tree = _attn_case(14, ctx, [n_q] * 3, 1, 128, 4, "none", dtype, spread=1e-3)
+    for b in range(3):                                 # a token 14 nats above the rest
+        p = int(table[b, 3])
+        c["k_scale"][p], c["k_scale"][int(table[b, 0])] = 1.0, 1.0
+        qm = q[cu[b]:cu[b] + 1, :1].float()
+        c["k_pages"][p, 0, 7] = (qm[0, 0] / qm.norm() * 400).to(R.E4M3)
+        q[cu[b]:cu[b + 1]] = (qm / qm.norm() * 0.4).to(dtype)
+    _check_attn(c, table, q, cu, ctx, "none", tree, dtype, max_q=n_q)
+    _check_attn(c, table, q, cu, ctx, "none", tree, dtype, scale=3.0, max_q=n_q)
+
+
+@pytest.mark.parametrize("hint", [0, 1, 16, 17, 10 ** 6])
+def test_attention_max_q_only_steers(hint):
+    """Any max_q gives the rows of every request."""
+    c, table, q, cu, tree = _attn_case(21, [200, 333], [1, 45], 2, 128, 8, "causal", torch.bfloat16)
+    _check_attn(c, table, q, cu, [200, 333], "causal", tree, torch.bfloat16, max_q=hint)
+
+
+def test_attention_strided_queries():
+    """q as columns of a projection's output."""
+    from block_diffusion_speculative_inject_gb300 import kv8_attention
+    for n_q in (2, 30):
+        c, table, q, cu, _ = _attn_case(4, [90, 140], [n_q, n_q], 2, 64, 4, "causal", torch.bfloat16)
+        gpu = _to_gpu(c)
+        args = (_i4(cu), _i4([90, 140]), table.cuda())
+        want = kv8_attention(gpu, q.cuda(), *args, max_q=n_q)
+        buf = torch.full((2 * n_q, 8 * 64 + 8), math.nan, dtype=torch.bfloat16, device="cuda")
+        view = buf[:, 128:128 + 4 * 64].unflatten(1, (4, 64))
+        view.copy_(q)
+        assert torch.equal(kv8_attention(gpu, view, *args, max_q=n_q), want)
+
+
+def test_far_pages_of_a_large_pool():
+    """Pages whose bytes lie beyond 2^32: append, read and both attention kernels."""
+    from block_diffusion_speculative_inject_gb300 import KV8Cache, kv8_append, kv8_attention, kv8_read
+    n_pages, nkv, hd = 1_100_000, 1, 64
+    cache = KV8Cache.empty(n_pages, nkv, hd)
+    g = torch.Generator().manual_seed(1)
+    pages = [n_pages - 1, 5, 1_048_577]
+    slots = torch.tensor([pages[p // PAGE] * PAGE + p % PAGE for p in range(150)])
+    k, v = (torch.randn((150, nkv, hd), generator=g).bfloat16() for _ in range(2))
+    kv8_append(cache, k.cuda(), v.cuda(), slots.cuda())
+    small = _cache_cpu(0, 3, nkv, hd)
+    local = [p // PAGE * PAGE + p % PAGE for p in range(150)]
+    R.append(small, k, v, local)
+    rk, rv = kv8_read(cache, slots.cuda())
+    idx = torch.tensor(local)
+    assert torch.equal(rk.cpu()[:, 0], small["k_pages"].float()[idx // PAGE, 0, idx % PAGE] * small["k_scale"][idx // PAGE])
+    for n_q in (1, 40):
+        q = torch.randn((n_q, 2, hd), generator=g).bfloat16()
+        got = kv8_attention(cache, q.cuda(), _i4([0, n_q]), _i4([150]), _i4([pages]), max_q=n_q)
+        want, _, absv, top = R.attention(small, q, [0, n_q], [150], torch.tensor([[0, 1, 2]]), "causal")
+        tol = want.abs() * 2.0 ** -8 + absv * (2.0 ** -11 + 2 * (top * 2.0 ** -19 + 2.0 ** -19))[..., None]
+        assert bool(((got.cpu().double() - want).abs() <= tol).all())
+
+
+# ---------------------------------------------------------------- together
+class _Loop:
+    """Verify rounds over an 8-bit cache, and the same rounds on the reference's cache."""
+
+    def __init__(self, n, nkv, group, hd, n_pages, width, dtype, seed=0):
+        from block_diffusion_speculative_inject_gb300 import KV8Cache, Rope
+        self.n, self.nkv, self.nq, self.hd, self.dtype = n, nkv, nkv * group, hd, dtype
+        self.g = torch.Generator().manual_seed(seed)
+        self.rope = Rope(hd, theta=1e4)
+        self.freq, self.mag = R.rope_freq(hd, 1e4)
+        self.cache = KV8Cache.empty(n_pages, nkv, hd)
+        self.ref = {k: getattr(self.cache, k).cpu().clone() for k in ("k_pages", "v_pages", "k_scale", "v_scale")}
+        self.len = _i4([0] * n)
+        self.table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+        self.stack = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+        self.free = _i4([n_pages])
+
+    def draw(self, rows):
+        f = lambda h: torch.randn((rows, h, self.hd), generator=self.g).to(self.dtype)  # noqa: E731
+        return f(self.nq), f(self.nkv), f(self.nkv)
+
+    def device_round(self, n_new, rows, q, k, v, max_q):
+        from block_diffusion_speculative_inject_gb300 import kv8_append, kv8_attention, page_plan, rope
+        p = page_plan(self.len, n_new, self.table, self.stack, self.free, rows)
+        q, k = rope(self.rope, p["positions"], q, k)
+        kv8_append(self.cache, k, v, p["slot_map"])
+        out = kv8_attention(self.cache, q, p["cu_rows"], p["new_len"], self.table, mask="causal", max_q=max_q)
+        return p, q, k, out
+
+    def check_round(self, p, k, q, v, out):
+        """The call's own rotated rows through the reference's cache and attention."""
+        R.append(self.ref, k.cpu(), v, p["slot_map"].tolist())
+        used = sorted({s // PAGE for s in p["slot_map"].tolist() if s >= 0})
+        for name in ("k_pages", "v_pages"):
+            a = getattr(self.cache, name).view(torch.uint8)[used].cpu()
+            assert torch.equal(a, self.ref[name].view(torch.uint8)[used])
+        cu, ctx = p["cu_rows"].tolist(), p["new_len"].tolist()
+        want, _, absv, top = R.attention(self.ref, q.cpu(), cu, ctx, self.table.cpu(), "causal")
+        r = 2.0 ** -11 if self.dtype == torch.bfloat16 else 2.0 ** -20
+        tol = want.abs() * HALF[self.dtype] + absv * (r + 2 * (top * 2.0 ** -19 + 2.0 ** -19))[..., None]
+        n = cu[-1]
+        assert bool(((out.cpu().double()[:n] - want[:n]).abs() <= tol[:n]).all())
+
+
+@pytest.mark.parametrize("dtype,group,hd", [(torch.bfloat16, 4, 128), (torch.float32, 2, 64)])
+def test_verify_loop(dtype, group, hd):
+    """Prompts, then rounds of a block of rows per request whose rejected part is dropped by the next plan;
+    the accept lengths never leave the GPU."""
+    from block_diffusion_speculative_inject_gb300 import page_plan
+    n, blk = 5, 8
+    lp = _Loop(n, 2, group, hd, 64, 8, dtype)
+    prompt = [70, 1, 128, 33, 200]
+    rows = sum(prompt)
+    q, k, v = lp.draw(rows)
+    p, qr, kr, out = lp.device_round(_i4(prompt), rows, q.cuda(), k.cuda(), v.cuda(), max(prompt))
+    assert p["refused"].sum() == 0
+    lp.check_round(p, kr, qr, v, out)
+    lp.len, lp.free = p["new_len"], p["n_free"]
+    for step in range(4):
+        q, k, v = lp.draw(n * blk)
+        p, qr, kr, out = lp.device_round(_i4([blk] * n), n * blk, q.cuda(), k.cuda(), v.cuda(), blk)
+        lp.check_round(p, kr, qr, v, out)
+        accept = torch.randint(0, blk, (n,), generator=lp.g, dtype=torch.int32).cuda()
+        drop = page_plan(p["new_len"], accept + 1 - blk, lp.table, lp.stack, p["n_free"], 0)
+        assert torch.equal(drop["new_len"], lp.len + accept + 1)
+        held = sum(R.pages_of(x) for x in drop["new_len"].tolist())
+        assert drop["n_free"].tolist() == [64 - held]
+        lp.len, lp.free = drop["new_len"], drop["n_free"]
+    got = [x for b in range(n) for x in lp.table[b, :R.pages_of(int(lp.len[b]))].tolist()]
+    assert sorted(got + lp.stack[:int(lp.free)].tolist()) == list(range(64))      # no page lost, none twice
+
+
+def test_round_in_a_graph_and_on_another_stream():
+    """A whole round captured once and replayed on new inputs equals the eager round; two graphs with their own
+    workspaces run at once on two streams."""
+    n, blk = 3, 6
+    eager, captured = (_Loop(n, 2, 4, 128, 32, 6, torch.bfloat16) for _ in range(2))
+    q, k, v = (x.cuda() for x in eager.draw(n * blk))
+    add = _i4([blk] * n)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        captured.device_round(add, n * blk, q, k, v, blk)        # warm up
+    torch.cuda.current_stream().wait_stream(side)
+    captured.len, captured.free = _i4([0] * n), _i4([32])
+    captured.stack.copy_(torch.arange(32, dtype=torch.int32))
+    graph = torch.cuda.CUDAGraph()
+    sq, sk, sv = q.clone(), k.clone(), v.clone()
+    with torch.cuda.graph(graph):
+        p, _, _, out = captured.device_round(add, n * blk, sq, sk, sv, blk)
+    for step in range(3):
+        for s, x in ((sq, q), (sk, k), (sv, v)):
+            s.copy_(x)
+        graph.replay()
+        pe, _, _, oe = eager.device_round(add, n * blk, q, k, v, blk)
+        assert torch.equal(out, oe) and torch.equal(p["slot_map"], pe["slot_map"])
+        captured.len.copy_(p["new_len"])
+        captured.free.copy_(p["n_free"])
+        eager.len, eager.free = pe["new_len"], pe["n_free"]
+        q, k, v = (x.cuda() for x in eager.draw(n * blk))
+
+
+@pytest.mark.parametrize("n_q", [1, 20])
+def test_two_calls_at_once(n_q):
+    """Two streams, their own workspaces, split contexts: each equals its call alone, bit for bit, many times."""
+    from block_diffusion_speculative_inject_gb300 import kv8_attention, kv8_workspace
+    sets = []
+    for seed in (1, 2):
+        c, table, q, cu, _ = _attn_case(seed, [6000, 900], [n_q, n_q], 2, 128, 8, "causal", torch.bfloat16)
+        a = (_to_gpu(c), q.cuda(), _i4(cu), _i4([6000, 900]), table.cuda())
+        ws = torch.empty(kv8_workspace(*a, max_q=n_q), dtype=torch.uint8, device="cuda")
+        sets.append((a, ws, kv8_attention(*a, max_q=n_q)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(10):
+        for i, (a, ws, _) in enumerate(sets):
+            got[i].append(kv8_attention(*a, max_q=n_q, workspace=ws, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, (_, _, want) in enumerate(sets):
+        assert all(torch.equal(x, want) for x in got[i])
