@@ -1,94 +1,537 @@
-// Attention over the 8-bit paged cache (dflash_kv8_attention): one warp per query row and head,
-// lanes over 32 keys at a time, a running maximum and sum, everything in fp32.
+// Attention over the 8-bit paged cache (dflash_kv8_attention): the entry point, the kernel for few
+// query rows per kv head (and for fp32), and the merge of split contexts.
+//
+// Few rows (a decoding step, a short block): the cache's bytes bound it, each read once. A worker is
+// a warp with its own ring of K and V pages in shared memory, filled by bulk copies that it issues
+// itself, so that warps never wait for one another; 16 query rows (tokens x heads of a kv head)
+// are the M of mma.m16n8k16. Per page of 64 tokens:
+//   S[16, 64] = Q . K^T      K bytes go from shared memory to f16 B fragments in registers (exact)
+//   P = 2^(S c + log2 s_v - m), S = sum in log2 units, c = scale log2(e) s_k 2^row exponent
+//   O[16, hd] += P . V       V bytes likewise: both contractions run along 16 contiguous bytes
+// The contraction indices are permuted so that no fragment needs a shuffle: lane (g, t) of a B fragment
+// holds dims 32 t .. 32 t + 31 of token 16 (g >> 1) + 2 j + (g & 1) for K, and tokens 16 t .. 16 t + 15 of
+// a value dim for V, which makes the S accumulators of a lane exactly its part of the P fragments.
+// V's page scale goes into the exponent (P carries s_v, the row sum divides it out again), so that
+// O of pages of very different scale adds up in one accumulator. f16 holds q exactly (bf16 times a
+// power of two per row) and P to 11 bits with its largest at 2^14, so P is normal down to 2^-28. For
+// fp32, q and P are pairs of f16 (22 bits) and every product is two.
 #include <cmath>
 
-#include "kv8.cuh"
+#include "kv8_sched.cuh"
+#include "tc_ptx.cuh"
 
 namespace dflash {
 
-struct Kv8AttnArgs {
-  int n_req, rows, nq, nkv, width, mask, words, n_pages;
-  float scale;
-  const void *q;
-  int64_t q_stride;
-  const int32_t *cu_q, *ctx_len, *table;
-  const uint32_t *tree;
-  void *out;
-  float *lse;
-  const uint8_t *kp, *vp;
-  const float *ks, *vs;
+constexpr int KM_WARPS = 8;
+constexpr int KM_THREADS = 32 * KM_WARPS;
+constexpr int KM_ROWS = 16;
+constexpr float KM_BIAS = 14.f;                        // P's largest value is 2^14
+constexpr float LN2 = 0.693147180559945309f;
+
+template <int HD>
+struct KmLayout {
+  static constexpr int SLOT = KV_PAGE * HD;            // bytes of a K or V page of one head
+  static constexpr int SLOTS = HD == 128 ? 3 : 6;      // 24 KB per warp
+  static constexpr int RING = SLOT * SLOTS;
+  static constexpr int SIDE = 4;                       // units whose page and scales are kept
+  static constexpr size_t SMEM = 128 + (size_t)KM_WARPS * (RING + SLOTS * 8 + SIDE * 16);
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// a (low half) and b as f16, to nearest even
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t h) {
+  float2 v;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n" : "=f"(v.x), "=f"(v.y) : "r"(h));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+// bytes 0x7f / 0xff (e4m3 NaN) of a word, as 0x80 in each
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t byte_mask(uint32_t high_bits) { return (high_bits >> 7) * 0xffu; }
+
+// The warp's copies: pages of its units in order, K then V, each into the next slot of its ring.
+template <int HD>
+struct KmFeed {
+  Kv8Piece p;                                          // piece of the next copy
+  int u, tab_u, tab;                                   // next unit; the 32 table entries from tab_u on
+  uint32_t seq;                                        // copies issued
+  bool v, done;
 };
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(128) k_kv8_attn_rows(const Kv8AttnArgs a) {
+__global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnArgs a) {
+  typedef KmLayout<HD> Lay;
+  typedef Kv8Tiles<KV_PAGE, KM_ROWS> Tiles;
+  constexpr int KS = HD / 16;                          // k steps of S
+  constexpr int NT = HD / 8;                           // n tiles of O
+  constexpr int PL = sizeof(T) == 4 ? 2 : 1;           // f16 planes of q and P
+  extern __shared__ __align__(128) uint8_t km_smem[];
+  __shared__ long long s_grp[KV8_GROUPS + 1];
+  __shared__ int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t *base = km_smem;
+  const uint32_t ring = smem_u32(base) + warp * Lay::RING;
+  uint64_t *bars = (uint64_t *)(base + KM_WARPS * Lay::RING) + warp * Lay::SLOTS;
+  const uint32_t bar0 = smem_u32(bars);
+  // per unit: page id (-1: not in the pool) and the two scales
+  struct Side { int page; float ks, vs, pad; };
+  Side *side = (Side *)(base + KM_WARPS * (Lay::RING + Lay::SLOTS * 8)) + warp * Lay::SIDE;
+  pdl_trigger();
+  if (lane < Lay::SLOTS) mbar_init(bar0 + 8 * lane, 1);
+  if (threadIdx.x == 0) s_abort = 0;
+  fence_mbar_init();
+  pdl_wait();
+  kv8_group_sums<KV_PAGE, KM_ROWS>(a, s_grp);
+
+  const long long total = s_grp[(a.n_req + 31) / 32];
+  const int workers = gridDim.x * KM_WARPS, me = warp * gridDim.x + blockIdx.x;
+  const long long chunk = (total + workers - 1) / workers;
+  const long long pos = (long long)me * chunk;
+  if (pos >= total) {
+    if (lane == 0) a.desc[me].units = 0;
+    return;                                            // (no barrier of the whole CTA follows)
+  }
+  long long item_begin;
+  Kv8Piece pc = kv8_first_piece<KV_PAGE, KM_ROWS>(a, s_grp, pos, min(chunk, total - pos), item_begin);
+  if (lane == 0) a.desc[me] = Kv8Desc{item_begin, chunk, pc.units, pc.b, pc.qt, pc.h};
+  bool first = true;
+
+  KmFeed<HD> f;
+  f.p = pc;
+  f.u = pc.u0;
+  f.tab_u = -32;
+  f.tab = 0;
+  f.seq = 0;
+  f.v = f.done = false;
+  auto feed = [&]() {
+    if (!f.done) {
+      if (f.u >= f.tab_u + 32 || f.tab_u < 0) {        // the next 32 table entries of this piece
+        f.tab_u = f.u;
+        f.tab = f.u + lane < f.p.u1 ? a.table[(size_t)f.p.b * a.width + f.u + lane] : -1;
+        if (f.p.r.len == 0) f.tab = -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, f.tab, f.u - f.tab_u);
+      const bool in = page >= 0 && page < a.n_pages;
+      const uint32_t unit = f.seq >> 1;
+      Side *sd = side + unit % Lay::SIDE;
+      const uint32_t slot = f.seq % Lay::SLOTS;
+      if (lane == 0) {
+        // a page outside the pool is not copied; its arrival is a plain one
+        if (in) {
+          mbar_expect_tx(bar0 + 8 * slot, Lay::SLOT);
+          bulk_load(ring + slot * Lay::SLOT, (f.v ? a.vp : a.kp) + kv8_block(page, f.p.h, a.nkv, HD), Lay::SLOT, bar0 + 8 * slot);
+        } else {
+          mbar_arrive(bar0 + 8 * slot);
+        }
+        if (!f.v) sd->page = in ? page : -1;
+      }
+      if (!f.v && in && lane < 2) {
+        const float *src = (lane ? a.vs : a.ks) + (size_t)page * a.nkv + f.p.h;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sd->ks + lane)), "l"(src) : "memory");
+      }
+      ++f.seq;
+      f.v = !f.v;
+      if (!f.v && ++f.u == f.p.u1) {
+        if (f.p.left > 0) {
+          kv8_next_piece<KV_PAGE, KM_ROWS>(a, f.p);
+          f.u = f.p.u0;
+          f.tab_u = -32;
+        } else {
+          f.done = true;
+        }
+      }
+      if (f.v) asm volatile("cp.async.commit_group;" ::: "memory");   // one group per unit, with its K page
+    } else {
+      // keep one group per unit ahead of the reader
+      if (f.v ^= true) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < Lay::SLOTS; ++i) feed();
+
+  const int group = a.nq / a.nkv, tpt = KM_ROWS / group;
+  uint32_t take = 0;                                   // pages taken from the ring
+  bool ok = true;
+  auto wait = [&]() {                                  // the slot of the next page
+    const uint32_t slot = take % Lay::SLOTS;
+    ok = ok && mbar_wait(bar0 + 8 * slot, take / Lay::SLOTS & 1, (volatile int *)&s_abort, nullptr, 0);
+    ok = __all_sync(0xffffffffu, ok);
+    return ring + slot * Lay::SLOT;
+  };
+
+  for (;;) {
+    // ---------------- this piece's query rows, as f16 fragments
+    // row g (and g + 8) of the tile: token row / group, head row % group
+    uint32_t qf[PL][KS][4];
+    float rs[2];                                       // scale log2(e) 2^(row exponent)
+    bool bad[2];
+    int tok[2];
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      const int row = g + 8 * rr, tk = pc.qt * tpt + row / group;
+      const bool live = row < tpt * group && tk < pc.r.n;
+      tok[rr] = live ? tk : -1;
+      float x[HD / 4];                                 // dims (HD / 4) t .. + HD / 4 - 1
+      float big = 0.f;
+      bool fin = true;
+      if (live) {
+        const T *src = (const T *)a.q + (int64_t)(pc.r.row0 + tk) * a.q_stride + (int64_t)(pc.h * group + row % group) * HD + t * (HD / 4);
+#pragma unroll
+        for (int i = 0; i < HD / 4; i += 16 / sizeof(T)) {
+          const uint4 w = *(const uint4 *)(src + i);
+          const T *e = (const T *)&w;
+#pragma unroll
+          for (int j = 0; j < 16 / (int)sizeof(T); ++j) x[i + j] = to_f(e[j]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 4; ++i) {
+        big = fmaxf(big, fabsf(x[i]));
+        fin = fin && fabsf(x[i]) <= 3.402823466e38f;
+      }
+      big = quad_max(big);
+      const unsigned fb = __ballot_sync(0xffffffffu, fin);
+      bad[rr] = (fb >> (lane & ~3) & 15) != 15;
+      // q * 2^(14 - e): the largest is in [2^14, 2^15)
+      const int e = bad[rr] ? 0 : max(-100, (int)(__float_as_uint(big) >> 23) - 127);
+      const float up = exp2f((float)(14 - e));
+      rs[rr] = a.scale * 1.44269504088896341f * exp2f((float)(e - 14));
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = bad[rr] ? 0.f : x[4 * k + j] * up;
+        qf[0][k][rr] = pack_f16(y[0], y[1]);
+        qf[0][k][2 + rr] = pack_f16(y[2], y[3]);
+        if constexpr (PL == 2) {
+          const float2 h0 = unpack_f16(qf[0][k][rr]), h1 = unpack_f16(qf[0][k][2 + rr]);
+          qf[PL - 1][k][rr] = pack_f16(y[0] - h0.x, y[1] - h0.y);
+          qf[PL - 1][k][2 + rr] = pack_f16(y[2] - h1.x, y[3] - h1.y);
+        }
+      }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // tokens from `open` on are hidden from some row of the request
+    const int open = a.mask == DFLASH_MASK_NONE ? pc.r.len : max(0, pc.r.len - pc.r.n);
+
+#pragma unroll 1
+    for (int u = pc.u0; u < pc.u1; ++u) {
+      const uint32_t kslot = wait();
+      asm volatile("cp.async.wait_group %0;" ::"n"(Lay::SLOTS / 2 - (Lay::SLOTS == 3 ? 0 : 1)) : "memory");
+      __syncwarp();
+      const Side sd = side[take / 2 % Lay::SIDE];
+      if (!ok) break;
+      ++take;
+      if (sd.page < 0) {                               // not in the pool: nothing is seen
+        wait();
+        ++take;
+        __syncwarp();
+        feed();
+        feed();
+        continue;
+      }
+      float s[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        const int key = 16 * (g >> 1) + 2 * j + (g & 1);
+        uint32_t w[HD / 16];
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c) {
+          const uint4 v = lds128(kslot + key * HD + t * (HD / 4) + 16 * c);
+          w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t b0 = e4m3x2_to_f16x2(w[k]), b1 = e4m3x2_to_f16x2(w[k] >> 16);
+#pragma unroll
+          for (int pl = 0; pl < PL; ++pl) mma_f16(s[j], qf[pl][k], b0, b1);
+        }
+      }
+      __syncwarp();                                    // every lane has read the K page
+      feed();
+      // a lane's tokens: 16 t + 2 j + {0, 1} for n tile j
+      const bool partial = (u + 1) * KV_PAGE > open;
+      const float ev = log2f(sd.vs), iv = 1.f / sd.vs;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const float c = rs[rr] * sd.ks;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s[j][2 * rr + e] = fmaf(s[j][2 * rr + e], c, ev);
+      }
+      if (partial) {
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          const uint32_t hidden = tok[rr] < 0 ? ~0u : ~(uint32_t)(kv8_visible(a, pc.r, tok[rr], u) >> (16 * t));
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (hidden >> (2 * j + e) & 1) s[j][2 * rr + e] = -INFINITY;
+            }
+        }
+      }
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx[rr] = fmaxf(mx[rr], fmaxf(s[j][2 * rr], s[j][2 * rr + 1]));
+        mx[rr] = fmaxf(quad_max(mx[rr]), m[rr]);
+      }
+      float alpha[2], ref[2];
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const float top = mx[rr] == -INFINITY ? 0.f : mx[rr];
+        ref[rr] = top - KM_BIAS;
+        alpha[rr] = ex2(m[rr] - top);
+        m[rr] = mx[rr];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float &x = s[j][2 * rr + e];
+            x = ex2(x - ref[rr]);
+            sum += x;
+          }
+        l[rr] = fmaf(l[rr], alpha[rr], sum * iv);
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          o[i][0] *= alpha[0], o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1], o[i][3] *= alpha[1];
+        }
+      }
+      uint32_t pf[PL][4][4];                           // P fragments of 16 tokens each
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 2 * k + (i >> 1), rr = i & 1;
+          const float x0 = s[j][2 * rr], x1 = s[j][2 * rr + 1];
+          pf[0][k][i] = pack_f16(x0, x1);
+          if constexpr (PL == 2) {
+            const float2 h = unpack_f16(pf[0][k][i]);
+            pf[PL - 1][k][i] = pack_f16(x0 - h.x, x1 - h.y);
+          }
+        }
+      const uint32_t vslot = wait();
+      if (!ok) break;
+      ++take;
+      bool nan = false;
+      // bytes of tokens that no row sees (a page's tail) may be anything
+      const int tail = min(16, max(0, pc.r.len - u * KV_PAGE - 16 * t));
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint4 v = lds128(vslot + (8 * i + g) * KV_PAGE + 16 * t);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (partial) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int n = tail - 4 * k;
+            w[k] = n >= 4 ? w[k] : n <= 0 ? 0u : w[k] & ((1u << 8 * n) - 1);
+            const uint32_t nb = nan_bytes(w[k]);       // a NaN must not meet the zero weight of a row that does not see it
+            nan |= nb != 0;
+            w[k] &= ~byte_mask(nb);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t b0 = e4m3x2_to_f16x2(w[k]), b1 = e4m3x2_to_f16x2(w[k] >> 16);
+#pragma unroll
+          for (int pl = 0; pl < PL; ++pl) mma_f16(o[i], pf[pl][k], b0, b1);
+        }
+      }
+      if (partial && __any_sync(0xffffffffu, nan)) {   // rows that see a NaN value get it (rare)
+        const uint64_t vis0 = tok[0] < 0 ? 0 : kv8_visible(a, pc.r, tok[0], u);
+        const uint64_t vis1 = tok[1] < 0 ? 0 : kv8_visible(a, pc.r, tok[1], u);
+        uint32_t hit0 = 0, hit1 = 0;                   // bit 2 i + e: dim 8 i + 2 t + e holds one
+#pragma unroll 1
+        for (int d = 0; d < 2 * NT; ++d) {
+          uint64_t at = 0;                             // tokens whose value is NaN in that dim
+#pragma unroll 1
+          for (int k = 0; k < KV_PAGE; ++k) {
+            uint32_t byte;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(vslot + (8 * (d >> 1) + 2 * t + (d & 1)) * KV_PAGE + k));
+            at |= (uint64_t)((byte & 0x7f) == 0x7f) << k;
+          }
+          hit0 |= (uint32_t)((at & vis0) != 0) << d;
+          hit1 |= (uint32_t)((at & vis1) != 0) << d;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // adding 0 or NaN, so that no lane branches
+            o[i][e] += __uint_as_float((uint32_t)((int)(hit0 << (31 - 2 * i - e)) >> 31) & 0x7fc00000u);
+            o[i][2 + e] += __uint_as_float((uint32_t)((int)(hit1 << (31 - 2 * i - e)) >> 31) & 0x7fc00000u);
+          }
+      }
+      __syncwarp();                                    // every lane has read the V page
+      feed();
+    }
+    if (!ok) break;
+
+    // ---------------- the piece's result
+    l[0] = quad_sum(l[0]);
+    l[1] = quad_sum(l[1]);
+    const bool whole = pc.u1 - pc.u0 == pc.units;
+    const int slot = 2 * me + (first ? 0 : 1);
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      if (tok[rr] < 0) continue;
+      const int row = g + 8 * rr;
+      if (bad[rr]) l[rr] = NAN;
+      if (whole) {
+        const size_t at = (size_t)(pc.r.row0 + tok[rr]) * a.nq + pc.h * group + row % group;
+        const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
+        T *out = (T *)a.out + at * HD + 2 * t;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          if constexpr (PL == 1) *(__nv_bfloat162 *)(out + 8 * i) = __floats2bfloat162_rn(o[i][2 * rr] * inv, o[i][2 * rr + 1] * inv);
+          else *(float2 *)(out + 8 * i) = make_float2(o[i][2 * rr] * inv, o[i][2 * rr + 1] * inv);
+        }
+        if (a.lse && t == 0) a.lse[at] = l[rr] == 0.f ? -INFINITY : (m[rr] - KM_BIAS + log2f(l[rr])) * LN2;
+      } else {
+        float *po = a.part_o + ((size_t)slot * KM_ROWS + row) * HD + 2 * t;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) *(float2 *)(po + 8 * i) = make_float2(o[i][2 * rr], o[i][2 * rr + 1]);
+        if (t == 0) *(float2 *)(a.part_ml + ((size_t)slot * KM_ROWS + row) * 2) = make_float2(m[rr] - KM_BIAS, l[rr]);
+      }
+    }
+    if (pc.left <= 0) break;
+    kv8_next_piece<KV_PAGE, KM_ROWS>(a, pc);
+    first = false;
+  }
+  if (!ok) {
+    // A wait ran out of time: the rows that this worker still owes become NaN, and its copies in
+    // flight are waited for, with a limit.
+    for (;;) {
+      const int slot = 2 * me + (first ? 0 : 1);
+      for (int row = 0; row < tpt * group; ++row) {
+        const int tk = pc.qt * tpt + row / group;
+        if (tk >= pc.r.n) break;
+        const size_t at = (size_t)(pc.r.row0 + tk) * a.nq + pc.h * group + row % group;
+        if (pc.u1 - pc.u0 == pc.units) {
+          for (int d = lane; d < HD; d += 32) ((T *)a.out)[at * HD + d] = from_f<T>(NAN);
+          if (a.lse && lane == 0) a.lse[at] = NAN;
+        } else if (lane == 0) {
+          *(float2 *)(a.part_ml + ((size_t)slot * KM_ROWS + row) * 2) = make_float2(0.f, NAN);
+        }
+      }
+      if (pc.left <= 0) break;
+      kv8_next_piece<KV_PAGE, KM_ROWS>(a, pc);
+      first = false;
+    }
+    const unsigned long long t0 = global_ns();
+    for (; take < f.seq; ++take)
+      while (!mbar_try_wait(bar0 + 8 * (take % Lay::SLOTS), take / Lay::SLOTS & 1) && global_ns() - t0 < TC_WAIT_NS) {
+      }
+  }
+}
+
+// ---------------------------------------------------------------- merge of split items
+// CTA w looks at the descriptor of worker w: if its first piece continues an item that worker w - 1 began,
+// the CTA merges that item: partial (m, l, O) of worker w - 1's last piece and of the first pieces of w,
+// w + 1, .. up to the item's end. A thread owns one row and four dims.
+template <typename T, int HD, int U, int M>
+__global__ void __launch_bounds__(128) k_kv8_combine(const Kv8AttnArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float sq[4][HD];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long id = (long)blockIdx.x * 4 + w;
-  if (id >= (long)a.rows * a.nq) return;
-  const int row = (int)(id / a.nq), h = (int)(id % a.nq), kvh = h / (a.nq / a.nkv);
-  int lo = 0, hi = a.n_req;                            // first b with cu_q[b + 1] > row
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (a.cu_q[m + 1] > row) hi = m;
-    else lo = m + 1;
-  }
-  if (lo == a.n_req || a.cu_q[lo] > row) return;
-  const int b = lo, i = row - a.cu_q[b], n = min(a.cu_q[b + 1], a.rows) - a.cu_q[b];
-  const int len = max(0, (int)min((long)a.ctx_len[b], (long)a.width * KV_PAGE));
-  const int first = len - n;                           // position of the request's first row
-  const T *q = (const T *)a.q + row * a.q_stride + (int64_t)h * HD;
-  bool bad = false;
-  for (int d = lane; d < HD; d += 32) {
-    const float x = to_f(q[d]);
-    bad |= !(fabsf(x) <= 3.402823466e38f);
-    sq[w][d] = x;
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[HD / 32] = {};
-  for (int p0 = 0; p0 < len; p0 += 32) {
-    const int p = p0 + lane, page = a.table[(size_t)b * a.width + p / KV_PAGE];
-    bool see = p < len && page >= 0 && page < a.n_pages;
-    if (a.mask == DFLASH_MASK_CAUSAL) see = see && p <= first + i;
-    if (a.mask == DFLASH_MASK_TREE && p >= first && see) {
-      const int j = p - first;
-      see = j < 32 * a.words && (a.tree[(size_t)row * a.words + j / 32] >> (j % 32) & 1);
+  const int w = blockIdx.x + 1;
+  const Kv8Desc d = a.desc[w];
+  if (d.units == 0) return;
+  const long long pos = (long long)w * d.chunk;
+  if (d.begin == pos || d.begin < pos - d.chunk) return;     // starts here, or begun before worker w - 1
+  const Kv8Tiles<U, M> tl(a);
+  const int group = a.nq / a.nkv;
+  const Kv8Req r = kv8_req(a, d.b);
+  const int last = (int)((d.begin + d.units - 1) / d.chunk);  // the worker of the item's last unit
+  const int slot0 = 2 * (w - 1) + (d.begin == pos - d.chunk ? 0 : 1);
+  const int rows = min(tl.tpt, r.n - d.qt * tl.tpt) * group;
+  for (int i = blockIdx.y * 128 + threadIdx.x; i < rows * (HD / 4); i += gridDim.y * 128) {
+    const int row = i / (HD / 4), c = i % (HD / 4) * 4;
+    auto slot_of = [&](int x) { return x == w - 1 ? slot0 : 2 * x; };
+    float m = -INFINITY;
+    for (int x = w - 1; x <= last; ++x) m = fmaxf(m, a.part_ml[((size_t)slot_of(x) * M + row) * 2]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = w - 1; x <= last; ++x) {
+      const size_t s = (size_t)slot_of(x) * M + row;
+      const float2 ml = *(const float2 *)(a.part_ml + s * 2);
+      const float4 v = *(const float4 *)(a.part_o + s * HD + c);
+      const float e = exp2f(ml.x - ref);
+      l = fmaf(ml.y, e, l);
+      o.x = fmaf(v.x, e, o.x);
+      o.y = fmaf(v.y, e, o.y);
+      o.z = fmaf(v.z, e, o.z);
+      o.w = fmaf(v.w, e, o.w);
     }
-    const size_t blk = see ? kv8_block(page, kvh, a.nkv, HD) : 0;
-    float s = -INFINITY;
-    if (see) {
-      const uint8_t *k = a.kp + blk + (size_t)(p % KV_PAGE) * HD;
-      s = 0.f;
-      for (int d = 0; d < HD; d += 4) {
-        const uint32_t u = *(const uint32_t *)(k + d);
-        const float2 x = e4m3x2_to_f32(u & 0xffff), y = e4m3x2_to_f32(u >> 16);
-        s += sq[w][d] * x.x + sq[w][d + 1] * x.y + sq[w][d + 2] * y.x + sq[w][d + 3] * y.y;
-      }
-      s *= a.scale * a.ks[(size_t)page * a.nkv + kvh];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t at = (size_t)(r.row0 + d.qt * tl.tpt + row / group) * a.nq + d.h * group + row % group;
+    T *out = (T *)a.out + at * HD + c;
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+      *(uint2 *)out = *(const uint2 *)h;
+    } else {
+      *(float4 *)out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
-    const float top = fmaxf(m, warp_max(s));
-    if (top == -INFINITY && !__any_sync(0xffffffffu, see)) continue;
-    const float base = top == -INFINITY ? 0.f : top;
-    const float pr = see ? expf(s - base) : 0.f, c = expf(m - base);
-    const float pv = see ? pr * a.vs[(size_t)page * a.nkv + kvh] : 0.f;
-    l = l * c + warp_sum(pr);
-    m = top;
-    for (int d = 0; d < HD / 32; ++d) o[d] *= c;
-    for (int j = 0; j < 32; ++j) {
-      const float pj = __shfl_sync(0xffffffffu, pv, j);
-      const bool sj = __shfl_sync(0xffffffffu, (int)see, j);
-      const size_t bj = __shfl_sync(0xffffffffu, blk, j);
-      if (!sj) continue;
-      for (int d = 0; d < HD / 32; ++d)
-        o[d] = fmaf(pj, e4m3x2_to_f32(a.vp[bj + (size_t)(lane + 32 * d) * KV_PAGE + (p0 + j) % KV_PAGE]).x, o[d]);
-    }
+    if (a.lse && c == 0) a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * LN2;
   }
-  const float inv = bad ? NAN : l == 0.f ? 0.f : 1.f / l;
-  T *out = (T *)a.out + ((size_t)row * a.nq + h) * HD;
-  for (int d = 0; d < HD / 32; ++d) out[lane + 32 * d] = from_f<T>(bad ? NAN : o[d] * inv);
-  if (a.lse && lane == 0) a.lse[(size_t)row * a.nq + h] = bad ? NAN : m + logf(l);
+}
+
+constexpr int KM_CTAS = 152;                           // one per SM
+
+template <typename T, int HD>
+cudaError_t launch_rows(const Kv8AttnArgs &a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_rows<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)KmLayout<HD>::SMEM);
+  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD>, dim3(KM_CTAS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
+  if (e == cudaSuccess)
+    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, KM_ROWS>, dim3(KM_CTAS * KM_WARPS - 1, 1), dim3(128), 0, s, a);
+  return e;
 }
 
 }  // namespace dflash
@@ -110,25 +553,39 @@ bool attn_ok(const dflash_kv8_cache *c, const dflash_kv8_attn *x, bool pointers)
          aligned(x->cu_q, 4) && aligned(x->ctx_len, 4) && aligned(x->block_table, 4) && aligned(x->lse, 4) &&
          (x->mask != DFLASH_MASK_TREE || (x->tree_mask && aligned(x->tree_mask, 4)));
 }
+
+// Workspace: descriptors, then partial maxima and sums, then partial outputs.
+struct Space {
+  int64_t desc, ml, o, bytes;
+};
+Space space_of(int hd) {
+  const int64_t workers = KM_CTAS * KM_WARPS, m = KM_ROWS;
+  Space s;
+  s.desc = 0;
+  s.ml = (workers * (int64_t)sizeof(Kv8Desc) + 255) / 256 * 256;
+  s.o = s.ml + workers * 2 * m * 8;
+  s.bytes = s.o + workers * 2 * m * hd * 4;
+  return s;
+}
 }  // namespace
 
 extern "C" int64_t dflash_kv8_attention_workspace(const dflash_kv8_cache *cache, const dflash_kv8_attn *args) {
   if (!attn_ok(cache, args, false)) return -1;
-  return 256;
+  return space_of(cache->head_dim).bytes;
 }
 
 extern "C" dflash_status dflash_kv8_attention(void *stream, const dflash_kv8_cache *c, const dflash_kv8_attn *x) {
   if (!attn_ok(c, x, true)) return DFLASH_ERR_INVALID_ARG;
   if (x->rows == 0) return DFLASH_OK;
-  if (!x->workspace || !aligned(x->workspace, 256) || x->workspace_bytes < dflash_kv8_attention_workspace(c, x))
-    return DFLASH_ERR_INVALID_ARG;
+  const Space sp = space_of(c->head_dim);
+  if (!x->workspace || !aligned(x->workspace, 256) || x->workspace_bytes < sp.bytes) return DFLASH_ERR_INVALID_ARG;
+  uint8_t *ws = (uint8_t *)x->workspace;
   const Kv8AttnArgs a{x->n_req, x->rows, x->n_q_heads, c->n_kv_heads, x->max_blocks, x->mask, x->tree_words, c->n_pages,
                       x->scale, x->q, x->q_stride, x->cu_q, x->ctx_len, x->block_table, x->tree_mask, x->out, x->lse,
-                      (const uint8_t *)c->k_pages, (const uint8_t *)c->v_pages, c->k_scale, c->v_scale};
+                      (const uint8_t *)c->k_pages, (const uint8_t *)c->v_pages, c->k_scale, c->v_scale,
+                      (Kv8Desc *)(ws + sp.desc), (float *)(ws + sp.o), (float *)(ws + sp.ml)};
   const cudaStream_t s = (cudaStream_t)stream;
-  const dim3 g((unsigned)(((long)x->rows * x->n_q_heads + 3) / 4)), b(128);
-  const cudaError_t e = x->dtype == DFLASH_BF16
-      ? (c->head_dim == 128 ? launch_pdl(k_kv8_attn_rows<bf16, 128>, g, b, 0, s, a) : launch_pdl(k_kv8_attn_rows<bf16, 64>, g, b, 0, s, a))
-      : (c->head_dim == 128 ? launch_pdl(k_kv8_attn_rows<float, 128>, g, b, 0, s, a) : launch_pdl(k_kv8_attn_rows<float, 64>, g, b, 0, s, a));
+  const cudaError_t e = x->dtype == DFLASH_BF16 ? (c->head_dim == 128 ? launch_rows<bf16, 128>(a, s) : launch_rows<bf16, 64>(a, s))
+                                                : (c->head_dim == 128 ? launch_rows<float, 128>(a, s) : launch_rows<float, 64>(a, s));
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }

@@ -1,0 +1,233 @@
+// The work of one attention call over the 8-bit cache, cut into equal pieces on the GPU.
+//
+// An item is (request, tile of query tokens, kv head); its units are the U-token stretches of the
+// context that its rows may see. All units, in the order requests > tiles > heads > units, form
+// one line that is cut into equal chunks, one per worker; a worker thus owns at most two
+// pieces of items that others also work on (its first and its last), whose partial results go to
+// the workspace and are merged by k_kv8_combine. Every worker finds its start by itself from the
+// lengths on the GPU: unit counts of 32 requests are summed by a warp, the sums of those
+// groups sit in shared memory, and the unit counts inside a request have a closed form.
+#pragma once
+#include "kv8.cuh"
+
+namespace dflash {
+
+constexpr int KV8_GROUPS = KV8_MAX_REQ / 32;
+
+struct Kv8AttnArgs {
+  int n_req, rows, nq, nkv, width, mask, words, n_pages;
+  float scale;
+  const void *q;
+  int64_t q_stride;
+  const int32_t *cu_q, *ctx_len, *table;
+  const uint32_t *tree;
+  void *out;
+  float *lse;
+  const uint8_t *kp, *vp;
+  const float *ks, *vs;
+  // workspace: one descriptor per worker, then two partial results per worker
+  struct Kv8Desc *desc;
+  float *part_o, *part_ml;     // [2 workers][M][hd], [2 workers][M][2] (max in log2 units, sum)
+};
+
+// What the merge needs to know of a worker's first piece.
+struct Kv8Desc {
+  long long begin, chunk;      // first unit of the item, units per worker
+  int units;                   // of the item; 0: the worker has nothing to do
+  int b, qt, h;
+};
+
+// sum over i < n of floor((a i + b) / m), for a, b >= 0
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    if (a >= m) s += (n - 1) * n / 2 * (a / m), a %= m;
+    if (b >= m) s += n * (b / m), b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+struct Kv8Req {
+  int n, len, row0;            // rows, context length, first row
+};
+__device__ __forceinline__ Kv8Req kv8_req(const Kv8AttnArgs &a, int b) {
+  Kv8Req r;
+  r.row0 = max(0, min(a.cu_q[b], a.rows));
+  r.n = max(r.row0, min(a.cu_q[b + 1], a.rows)) - r.row0;
+  r.len = (int)max(0ll, min((long long)a.ctx_len[b], (long long)a.width * KV_PAGE));
+  return r;
+}
+
+// Tokens of a tile, tokens it may see, units: M rows of a tile hold M / group tokens.
+template <int U, int M>
+struct Kv8Tiles {
+  int tpt, nkv, causal;
+  __device__ __forceinline__ Kv8Tiles(const Kv8AttnArgs &a)
+      : tpt(M / (a.nq / a.nkv)), nkv(a.nkv), causal(a.mask == DFLASH_MASK_CAUSAL) {}
+  __device__ __forceinline__ int tiles(const Kv8Req &r) const { return (r.n + tpt - 1) / tpt; }
+  // the tokens [0, limit) hold all that some row of the tile sees
+  __device__ __forceinline__ int limit(const Kv8Req &r, int qt) const {
+    return causal ? max(0, (int)min((long long)r.len, (long long)r.len - r.n + min((long long)(qt + 1) * tpt, (long long)r.n)))
+                  : r.len;
+  }
+  __device__ __forceinline__ int units(const Kv8Req &r, int qt) const { return max(1, (limit(r, qt) + U - 1) / U); }
+  // units of one head's tiles before qt, for qt < tiles
+  __device__ __forceinline__ long long before(const Kv8Req &r, int qt) const {
+    if (!causal) return (long long)qt * units(r, 0);
+    if (qt == 0) return 0;
+    const long long A = (long long)r.len - r.n;                // the row before the first one's position + 1
+    const int t0 = (int)min((long long)qt, A < 0 ? -A / tpt : 0ll);   // tiles that see nothing have one unit
+    return t0 + floor_sum(qt - t0, U, tpt, A + (long long)(t0 + 1) * tpt + U - 1);
+  }
+  __device__ __forceinline__ long long total(const Kv8Req &r) const {
+    const int nt = tiles(r);
+    return nt ? nkv * (before(r, nt - 1) + units(r, nt - 1)) : 0;
+  }
+};
+
+// A worker's place on the line: the item, its unit range for this worker.
+struct Kv8Piece {
+  Kv8Req r;
+  int b, qt, h;
+  int u0, u1, units;           // [u0, u1) of the item's units
+  long long left;              // units of the worker after this piece
+};
+
+// Sums of units per group of 32 requests as a prefix in s_grp[0 .. groups]; whole CTA, ends in a barrier.
+template <int U, int M>
+__device__ __forceinline__ void kv8_group_sums(const Kv8AttnArgs &a, long long *s_grp) {
+  const Kv8Tiles<U, M> tl(a);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int groups = (a.n_req + 31) / 32;
+  for (int g = warp; g < groups; g += warps) {
+    const int b = g * 32 + lane;
+    long long t = b < a.n_req ? tl.total(kv8_req(a, b)) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) s_grp[g + 1] = t;
+  }
+  if (threadIdx.x == 0) s_grp[0] = 0;
+  __syncthreads();
+  if (groups > 1 && warp == 0) {
+    long long base = 0;
+    for (int g0 = 1; g0 <= groups; g0 += 32) {
+      long long x = g0 + lane <= groups ? s_grp[g0 + lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += t;
+      }
+      if (g0 + lane <= groups) s_grp[g0 + lane] = base + x;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// First piece of the worker that owns units [pos, pos + count), pos < s_grp[groups] (one warp, all lanes).
+template <int U, int M>
+__device__ __forceinline__ Kv8Piece kv8_first_piece(const Kv8AttnArgs &a, const long long *s_grp, long long pos,
+                                                    long long count, long long &item_begin) {
+  const Kv8Tiles<U, M> tl(a);
+  const int lane = threadIdx.x & 31, groups = (a.n_req + 31) / 32;
+  int lo = 0, hi = groups - 1;                         // last group with s_grp <= pos
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (s_grp[m] <= pos) lo = m;
+    else hi = m - 1;
+  }
+  const int b0 = lo * 32;
+  Kv8Req r{0, 0, 0};
+  long long mine = 0;
+  if (b0 + lane < a.n_req) {
+    r = kv8_req(a, b0 + lane);
+    mine = tl.total(r);
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  const unsigned past = __ballot_sync(0xffffffffu, s_grp[lo] + inc > pos);
+  const int who = __ffs(past) - 1;                     // the request that holds pos
+  Kv8Piece p;
+  p.b = b0 + who;
+  p.r.n = __shfl_sync(0xffffffffu, r.n, who);
+  p.r.len = __shfl_sync(0xffffffffu, r.len, who);
+  p.r.row0 = __shfl_sync(0xffffffffu, r.row0, who);
+  const long long start = s_grp[lo] + __shfl_sync(0xffffffffu, inc - mine, who);
+  const long long off = pos - start;
+  if (tl.causal) {
+    int l = 0, h = tl.tiles(p.r) - 1;
+    while (l < h) {
+      const int m = (l + h + 1) >> 1;
+      if (tl.before(p.r, m) * a.nkv <= off) l = m;
+      else h = m - 1;
+    }
+    p.qt = l;
+  } else {
+    p.qt = (int)(off / ((long long)tl.units(p.r, 0) * a.nkv));
+  }
+  p.units = tl.units(p.r, p.qt);
+  const long long in_tile = off - tl.before(p.r, p.qt) * a.nkv;
+  p.h = (int)(in_tile / p.units);
+  p.u0 = (int)(in_tile % p.units);
+  p.u1 = (int)min((long long)p.units, p.u0 + count);
+  p.left = count - (p.u1 - p.u0);
+  item_begin = pos - p.u0;
+  return p;
+}
+
+// The next piece of the same worker; p.left > 0.
+template <int U, int M>
+__device__ __forceinline__ void kv8_next_piece(const Kv8AttnArgs &a, Kv8Piece &p) {
+  const Kv8Tiles<U, M> tl(a);
+  if (++p.h == a.nkv) {
+    p.h = 0;
+    if (++p.qt == tl.tiles(p.r)) {
+      p.qt = 0;
+      do {
+        if (++p.b >= a.n_req) {                        // (not reached: left counts what there is)
+          p.u0 = p.u1 = 0;
+          p.left = 0;
+          return;
+        }
+        p.r = kv8_req(a, p.b);
+      } while (p.r.n == 0);
+    }
+    p.units = tl.units(p.r, p.qt);
+  }
+  p.u0 = 0;
+  p.u1 = (int)min((long long)p.units, p.left);
+  p.left -= p.u1;
+}
+
+// Which of the 64 tokens of page `page_no` the row of `token` (index among the request's rows) sees,
+// apart from whether the page is in the pool.
+__device__ __forceinline__ uint64_t kv8_visible(const Kv8AttnArgs &a, const Kv8Req &r, int token, int page_no) {
+  const int p0 = page_no * KV_PAGE;
+  auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };   // tokens 0 .. n - 1
+  const uint64_t in = below(r.len - p0);
+  const int first = r.len - r.n;
+  if (a.mask == DFLASH_MASK_NONE) return in;
+  if (a.mask == DFLASH_MASK_CAUSAL) return in & below(first + token + 1 - p0);
+  // tree: bit i of the page is token p0 + i, bit p0 + i - first of the row's mask
+  uint64_t bits = below(first - p0);                   // the context before the rows
+  const uint32_t *w = a.tree + (size_t)(r.row0 + token) * a.words;
+  const int j0 = p0 - first;                           // mask bit of the page's first token
+  const int wd = j0 >> 5, sh = j0 & 31;                // floor division: j0 may be negative
+  auto word = [&](int i) { return i >= 0 && i < a.words ? w[i] : 0u; };
+  const uint32_t x0 = word(wd), x1 = word(wd + 1), x2 = word(wd + 2);
+  bits |= (uint64_t)__funnelshift_r(x0, x1, sh) | (uint64_t)__funnelshift_r(x1, x2, sh) << 32;
+  return in & bits;
+}
+
+}  // namespace dflash
