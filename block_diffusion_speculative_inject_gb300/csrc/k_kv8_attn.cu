@@ -17,8 +17,7 @@
 // fp32, q and P are pairs of f16 (22 bits) and every product is two.
 #include <cmath>
 
-#include "kv8_sched.cuh"
-#include "tc_ptx.cuh"
+#include "kv8_attn.cuh"
 
 namespace dflash {
 
@@ -26,7 +25,6 @@ constexpr int KM_WARPS = 8;
 constexpr int KM_THREADS = 32 * KM_WARPS;
 constexpr int KM_ROWS = 16;
 constexpr float KM_BIAS = 14.f;                        // P's largest value is 2^14
-constexpr float LN2 = 0.693147180559945309f;
 
 template <int HD>
 struct KmLayout {
@@ -43,31 +41,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// a (low half) and b as f16, to nearest even
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t h) {
-  float2 v;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n" : "=f"(v.x), "=f"(v.y) : "r"(h));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(mbar) : "memory");
-}
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
@@ -76,10 +49,6 @@ __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
-// bytes 0x7f / 0xff (e4m3 NaN) of a word, as 0x80 in each
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ uint32_t byte_mask(uint32_t high_bits) { return (high_bits >> 7) * 0xffu; }
-
 // The warp's copies: pages of its units in order, K then V, each into the next slot of its ring.
 template <int HD>
 struct KmFeed {
@@ -470,67 +439,13 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   }
 }
 
-// ---------------------------------------------------------------- merge of split items
-// CTA w looks at the descriptor of worker w: if its first piece continues an item that worker w - 1 began,
-// the CTA merges that item: partial (m, l, O) of worker w - 1's last piece and of the first pieces of w,
-// w + 1, .. up to the item's end. A thread owns one row and four dims.
-template <typename T, int HD, int U, int M>
-__global__ void __launch_bounds__(128) k_kv8_combine(const Kv8AttnArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  const int w = blockIdx.x + 1;
-  const Kv8Desc d = a.desc[w];
-  if (d.units == 0) return;
-  const long long pos = (long long)w * d.chunk;
-  if (d.begin == pos || d.begin < pos - d.chunk) return;     // starts here, or begun before worker w - 1
-  const Kv8Tiles<U, M> tl(a);
-  const int group = a.nq / a.nkv;
-  const Kv8Req r = kv8_req(a, d.b);
-  const int last = (int)((d.begin + d.units - 1) / d.chunk);  // the worker of the item's last unit
-  const int slot0 = 2 * (w - 1) + (d.begin == pos - d.chunk ? 0 : 1);
-  const int rows = min(tl.tpt, r.n - d.qt * tl.tpt) * group;
-  for (int i = blockIdx.y * 128 + threadIdx.x; i < rows * (HD / 4); i += gridDim.y * 128) {
-    const int row = i / (HD / 4), c = i % (HD / 4) * 4;
-    auto slot_of = [&](int x) { return x == w - 1 ? slot0 : 2 * x; };
-    float m = -INFINITY;
-    for (int x = w - 1; x <= last; ++x) m = fmaxf(m, a.part_ml[((size_t)slot_of(x) * M + row) * 2]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = w - 1; x <= last; ++x) {
-      const size_t s = (size_t)slot_of(x) * M + row;
-      const float2 ml = *(const float2 *)(a.part_ml + s * 2);
-      const float4 v = *(const float4 *)(a.part_o + s * HD + c);
-      const float e = exp2f(ml.x - ref);
-      l = fmaf(ml.y, e, l);
-      o.x = fmaf(v.x, e, o.x);
-      o.y = fmaf(v.y, e, o.y);
-      o.z = fmaf(v.z, e, o.z);
-      o.w = fmaf(v.w, e, o.w);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const size_t at = (size_t)(r.row0 + d.qt * tl.tpt + row / group) * a.nq + d.h * group + row % group;
-    T *out = (T *)a.out + at * HD + c;
-    if constexpr (sizeof(T) == 2) {
-      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
-      *(uint2 *)out = *(const uint2 *)h;
-    } else {
-      *(float4 *)out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    }
-    if (a.lse && c == 0) a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * LN2;
-  }
-}
-
-constexpr int KM_CTAS = 152;                           // one per SM
-
 template <typename T, int HD>
 cudaError_t launch_rows(const Kv8AttnArgs &a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_rows<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)KmLayout<HD>::SMEM);
-  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD>, dim3(KM_CTAS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
+  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD>, dim3(KV8_SMS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
   if (e == cudaSuccess)
-    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, KM_ROWS>, dim3(KM_CTAS * KM_WARPS - 1, 1), dim3(128), 0, s, a);
+    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, KM_ROWS>, dim3(KV8_SMS * KM_WARPS - 1, 1), dim3(128), 0, s, a);
   return e;
 }
 
@@ -559,7 +474,7 @@ struct Space {
   int64_t desc, ml, o, bytes;
 };
 Space space_of(int hd) {
-  const int64_t workers = KM_CTAS * KM_WARPS, m = KM_ROWS;
+  const int64_t workers = KV8_SMS * KM_WARPS, m = KM_ROWS;
   Space s;
   s.desc = 0;
   s.ml = (workers * (int64_t)sizeof(Kv8Desc) + 255) / 256 * 256;
@@ -585,7 +500,9 @@ extern "C" dflash_status dflash_kv8_attention(void *stream, const dflash_kv8_cac
                       (const uint8_t *)c->k_pages, (const uint8_t *)c->v_pages, c->k_scale, c->v_scale,
                       (Kv8Desc *)(ws + sp.desc), (float *)(ws + sp.o), (float *)(ws + sp.ml)};
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = x->dtype == DFLASH_BF16 ? (c->head_dim == 128 ? launch_rows<bf16, 128>(a, s) : launch_rows<bf16, 64>(a, s))
+  const bool tiles = x->dtype == DFLASH_BF16 && (int64_t)x->max_q * (x->n_q_heads / c->n_kv_heads) > KM_ROWS;
+  const cudaError_t e = tiles ? launch_kv8_tiles(a, c->head_dim, s)
+                      : x->dtype == DFLASH_BF16 ? (c->head_dim == 128 ? launch_rows<bf16, 128>(a, s) : launch_rows<bf16, 64>(a, s))
                                                 : (c->head_dim == 128 ? launch_rows<float, 128>(a, s) : launch_rows<float, 64>(a, s));
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }

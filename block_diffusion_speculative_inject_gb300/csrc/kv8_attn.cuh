@@ -1,0 +1,97 @@
+// Shared by the two attention kernels over the 8-bit cache: small device helpers and the merge of the
+// partial results of split items.
+#pragma once
+#include "kv8_sched.cuh"
+#include "tc_ptx.cuh"
+
+namespace dflash {
+
+constexpr int KV8_SMS = 152;                           // one CTA per SM
+constexpr float LN2 = 0.693147180559945309f;
+
+// a (low half) and b as f16, to nearest even
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t h) {
+  float2 v;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n" : "=f"(v.x), "=f"(v.y) : "r"(h));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(mbar) : "memory");
+}
+// bytes 0x7f / 0xff (e4m3 NaN) of a word, as 0x80 in each
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t byte_mask(uint32_t high_bits) { return (high_bits >> 7) * 0xffu; }
+
+// ---------------------------------------------------------------- merge of split items
+// CTA w looks at the descriptor of worker w: if its first piece continues an item that worker w - 1 began,
+// the CTA merges that item: partial (m, l, O) of worker w - 1's last piece and of the first pieces of w,
+// w + 1, .. up to the item's end. A thread owns one row and four dims.
+template <typename T, int HD, int U, int M>
+__global__ void __launch_bounds__(128) k_kv8_combine(const Kv8AttnArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int w = blockIdx.x + 1;
+  const Kv8Desc d = a.desc[w];
+  if (d.units == 0) return;
+  const long long pos = (long long)w * d.chunk;
+  if (d.begin == pos || d.begin < pos - d.chunk) return;     // starts here, or begun before worker w - 1
+  const Kv8Tiles<U, M> tl(a);
+  const int group = a.nq / a.nkv;
+  const Kv8Req r = kv8_req(a, d.b);
+  const int last = (int)((d.begin + d.units - 1) / d.chunk);  // the worker of the item's last unit
+  const int slot0 = 2 * (w - 1) + (d.begin == pos - d.chunk ? 0 : 1);
+  const int rows = min(tl.tpt, r.n - d.qt * tl.tpt) * group;
+  for (int i = blockIdx.y * 128 + threadIdx.x; i < rows * (HD / 4); i += gridDim.y * 128) {
+    const int row = i / (HD / 4), c = i % (HD / 4) * 4;
+    auto slot_of = [&](int x) { return x == w - 1 ? slot0 : 2 * x; };
+    float m = -INFINITY;
+    for (int x = w - 1; x <= last; ++x) m = fmaxf(m, a.part_ml[((size_t)slot_of(x) * M + row) * 2]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = w - 1; x <= last; ++x) {
+      const size_t s = (size_t)slot_of(x) * M + row;
+      const float2 ml = *(const float2 *)(a.part_ml + s * 2);
+      const float4 v = *(const float4 *)(a.part_o + s * HD + c);
+      const float e = exp2f(ml.x - ref);
+      l = fmaf(ml.y, e, l);
+      o.x = fmaf(v.x, e, o.x);
+      o.y = fmaf(v.y, e, o.y);
+      o.z = fmaf(v.z, e, o.z);
+      o.w = fmaf(v.w, e, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t at = (size_t)(r.row0 + d.qt * tl.tpt + row / group) * a.nq + d.h * group + row % group;
+    T *out = (T *)a.out + at * HD + c;
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+      *(uint2 *)out = *(const uint2 *)h;
+    } else {
+      *(float4 *)out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+    if (a.lse && c == 0) a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * LN2;
+  }
+}
+
+// The kernel for many query rows (bf16): tiles of 128 rows and 128 tokens, one worker per SM.
+constexpr int KT_ROWS = 128, KT_TOKENS = 128;
+cudaError_t launch_kv8_tiles(const Kv8AttnArgs &a, int hd, cudaStream_t s);
+
+}  // namespace dflash

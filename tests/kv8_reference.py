@@ -109,7 +109,9 @@ def append(cache, k, v, slots):
 
 
 def attention(cache, q, cu, ctx, table, mask, tree=None, scale=None):
-    """(out, lse, weight of |v|, largest sum |q k| scale) in float64; cache tensors on the CPU."""
+    """(out, lse, weight of |v|, D) in float64; cache tensors on the CPU. D bounds the scores' terms: over a row's
+    tokens the largest sum |q_d k_d| scale, plus a quarter of the largest |q| times sum |k_d| scale (what a q
+    that is kept to 2^-21 of its row's largest entry, 2^-19 / 4, can be off by)."""
     rows, nq, hd = q.shape
     n_pages, nkv = cache["k_scale"].shape
     scale = 1 / math.sqrt(hd) if scale is None else scale
@@ -155,5 +157,5 @@ def attention(cache, q, cu, ctx, table, mask, tree=None, scale=None):
                     lse[row, hq] = z
                     out[row, hq] = w @ v[s]
                     absv[row, hq] = w @ v[s].abs()
-                    top[row, hq] = (k[s].abs() @ q[row, hq].abs()).max() * scale
+                    top[row, hq] = ((k[s].abs() @ q[row, hq].abs()).max() + q[row, hq].abs().max() * k[s].abs().sum(1).max() / 4) * scale
     return out, lse, absv, top

@@ -7,7 +7,8 @@ Tolerances (half steps: bf16 2^-8, f16 2^-11, fp32 2^-24, relative to the value)
             and three fp32 roundings add 1.8e-7; times 2 for the two terms is under 1e-6.
   append    bytes and scales are equal: scaling by a power of two is exact and there is one rounding.
   attention per output: its own rounding, plus with A = sum p |v| (p the softmax weights) and
-            D = max sum_d |q_d k_d| scale: the weights' 11-bit (fp32: 22-bit) rounding r = 2^-11 (2^-20),
+            D = max sum_d |q_d k_d| scale (and a part for small entries of q, see the reference):
+            the weights' 11-bit (fp32: 22-bit) rounding r = 2^-11 (2^-20),
             and their error from the scores, 2 (D 2^-19 + 2^-19): fp32 sums over at most 128 terms in
             pieces that may truncate (16 2^-23 = 2^-19) and exp2's 2^-22 with its argument's rounding.
   lse       D 2^-19 + |lse| 2^-22 + (L + 32) 2^-24: a positive fp32 sum over at most L terms.
@@ -391,6 +392,14 @@ def test_attention_one_long_context(dtype, n_q):
     ctx = [9001]
     c, table, q, cu, tree = _attn_case(77, ctx, n_q, 1, 128, 2, "causal", dtype)
     _check_attn(c, table, q, cu, ctx, "causal", tree, dtype, max_q=n_q[0])
+
+
+@pytest.mark.parametrize("hd,n_q", [(64, 17), (128, 40), (128, 2)])
+def test_attention_long_pieces(hd, n_q):
+    """Several items and many tiles per worker: every ring wraps a few times within a piece."""
+    ctx = [3000, 2600, 4100, 2049, 2048, 3333, 64, 2500]
+    c, table, q, cu, tree = _attn_case(31, ctx, [n_q] * 8, 8, hd, 8, "causal", torch.bfloat16)
+    _check_attn(c, table, q, cu, ctx, "causal", tree, torch.bfloat16, max_q=n_q)
 
 
 @pytest.mark.parametrize("n_q", [1, 20])
