@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   bool ok = true;
   auto wait = [&]() {                                  // the slot of the next page
     const uint32_t slot = take % Lay::SLOTS;
-    ok = ok && mbar_wait(bar0 + 8 * slot, take / Lay::SLOTS & 1, (volatile int *)&s_abort, nullptr, 0);
+    ok = ok && kv8_wait(bar0 + 8 * slot, take / Lay::SLOTS & 1, (volatile int *)&s_abort);
     ok = __all_sync(0xffffffffu, ok);
     return ring + slot * Lay::SLOT;
   };

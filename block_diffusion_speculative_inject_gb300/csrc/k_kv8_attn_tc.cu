@@ -2,7 +2,7 @@
 // trees, prompt chunks. One persistent CTA per SM walks its share of the work (kv8_sched.cuh) in tiles
 // of 128 rows (tokens x query heads of the kv head) and 128 tokens (two pages):
 //   S[128, 128] = Q . K^T        kind::f8f6f4, A = Q in tensor memory, B = the K pages as they are
-//   P = 2^(S c + log2 s_v - m)   two threads per row, one page each; f16, written over S
+//   P = 2^(S c + log2 s_v - m)   f16, written over S
 //   O[128, hd] += P . V          kind::f16, A = P in tensor memory, B = V pages widened to f16
 // Q's row, scaled by a power of two so that its largest entry is in [128, 256), is the sum of an e4m3 and
 // an e5m2 part: bf16 has 8 significant bits, e4m3 takes 4, and what rounding to nearest leaves is at
@@ -17,19 +17,23 @@
 // pages' scales enter as in the few-row kernel: s_k in c, s_v in the exponent of P.
 //
 // Tensor memory (512 columns): S/P at 0 and 128 (tile parity), O at 256, Q at 384 and 448 (piece
-// parity: 32 columns of the e4m3 part, then 32 of the e5m2 part). P of the 64 tokens of a half row lies in
-// the first 32 of their own 64 columns of S.
+// parity: 32 columns of the e4m3 part, then 32 of the e5m2 part). P of a page's 64 tokens lies in the first 32
+// of their own 64 columns of S.
 //
-// Roles (384 threads): warp 0 copies K (TMA, 128- or 64-byte swizzle) and V (bulk, as stored) into
-// rings of 4 tiles; warp 1 issues the MMAs, S of the next tile ahead of P.V of this one, across
-// piece borders; warps 2-9 load Q (of the next piece, ahead), run the softmax and write
-// results; warps 10-11 widen V. All waits are bounded; rows whose wait ran out become NaN.
+// Roles (384 threads, 168 registers): warp 0 copies K (TMA, 128- or 64-byte swizzle) and V (bulk, as stored)
+// into rings of 4 tiles; warp 1 issues the MMAs, S of the next tile ahead of P.V of this one, across
+// piece borders; it runs converged, with the MMAs themselves predicated on one lane, which leaves the
+// descriptors to the uniform datapath (a lone lane took over twice as long to issue a tile as the
+// tensor cores take to do it). Warps 2-9 run the softmax, two threads per row, one page each: warps w
+// and w + 4 share the rows of lane quarter w % 4 and trade their maxima. They also load Q (of the next
+// piece, ahead) and write results, half of the dims each. Warps 10-11 widen V. All walk the
+// same pieces on their own. All waits are bounded; rows whose wait ran out become NaN.
 #include "kv8_attn.cuh"
 
 namespace dflash {
 
 constexpr int KT_THREADS = 384;
-constexpr int KT_WIDEN = 64;                            // threads that widen V
+constexpr int KT_WIDEN = 64;                             // threads that widen V
 constexpr int KT_STAGES = 4;
 constexpr int KT_SIDE = 2 * KT_STAGES;                 // tiles whose page ids and scales are kept
 constexpr float KT_BIAS = 7.f;
@@ -50,15 +54,17 @@ struct KtLayout {
 
 struct KtSide {
   int page[2];                                         // -1: not there, nothing of it is seen
-  float ks[2], vs[2];
+  float ks[2], ev[2], iv[2];                           // K's scale, log2 of V's and 1 over it
 };
 
 struct KtShared {
   uint64_t kfull[KT_STAGES], kempty[KT_STAGES], vfull[KT_STAGES], vempty[KT_STAGES];
-  uint64_t s_full[2], p_full[2], w_full[2], w_empty[2], q_full[2], o_full, o_empty, pv_done, drain;
+  uint64_t s_full[2], p_full[2], w_full[2], pv_done[2], q_full[2], o_full, o_empty, drain[1];
+  uint64_t x_ready[2][4];                              // maxima traded: per tile parity and lane quarter
+  uint64_t l_ready[2][2][4];                           // row sums: per piece parity, half and lane quarter
   KtSide side[KT_SIDE];
-  float xmax[2][2][128], xsum[2][128];
-  int xok[2][2][4];
+  float xmax[2][2][128], lsum[2][2][128];              // per tile (piece) parity, half and row
+  int xgrow[2][2][4];                                  // a row of the warp outgrew its reference
   int nan_piece[4];                                    // per piece ordinal mod 4 (two are ahead): ordinal + 1 if V held a NaN
   int abort;
   uint32_t tmem;
@@ -73,10 +79,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(c2), "r"(mbar) : "memory");
 }
-__device__ __forceinline__ void umma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-               " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-               "r"(acc) : "memory");
+// MMAs and commits of the one thread with `lead` set; the whole warp runs them. hi: the descriptors' upper word
+__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 b, {%2, %3};\n"
+               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi),
+               "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 b, {%2, %3};\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi),
+               "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint32_t lead, uint32_t mbar) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+               " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(mbar), "r"(lead) : "memory");
 }
 // K-major descriptor of rows of 64 bytes in the 64-byte swizzle: 8-row atoms of 512 bytes
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
@@ -95,7 +111,31 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// 32 columns of this thread's lane, without the wait
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
+  uint32_t *u = (uint32_t *)r;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
+        "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]),
+        "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]),
+        "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+// (a.x * b + c, a.y * b + c) and a + b in one paired instruction each
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n fma.rn.f32x2 x, x, y, z;\n"
+      " mov.b64 {%0, %1}, x;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t *w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
@@ -122,13 +162,17 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       mbar_init(bar(sh.s_full[i]), 2);                 // the MMAs, and their issuer for the side words that it has seen
       mbar_init(bar(sh.p_full[i]), 8);
       mbar_init(bar(sh.w_full[i]), KT_WIDEN / 32);
-      mbar_init(bar(sh.w_empty[i]), 1);
+      mbar_init(bar(sh.pv_done[i]), 1);
       mbar_init(bar(sh.q_full[i]), 8);
+      for (int j = 0; j < 4; ++j) {
+        mbar_init(bar(sh.x_ready[i][j]), 2);
+        mbar_init(bar(sh.l_ready[i][0][j]), 1);
+        mbar_init(bar(sh.l_ready[i][1][j]), 1);
+      }
     }
     mbar_init(bar(sh.o_full), 1);
+    mbar_init(bar(sh.drain[0]), 1);
     mbar_init(bar(sh.o_empty), 8);
-    mbar_init(bar(sh.pv_done), 1);
-    mbar_init(bar(sh.drain), 1);
     sh.abort = 0;
     for (int i = 0; i < 4; ++i) sh.nan_piece[i] = 0;
     fence_mbar_init();
@@ -153,7 +197,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   volatile int *abort_flag = (volatile int *)&sh.abort;
-  auto wait = [&](uint64_t &b, uint32_t parity) { return mbar_wait(bar(b), parity & 1, abort_flag, nullptr, 0); };
+  auto wait = [&](uint64_t &b, uint32_t parity) { return kv8_wait(bar(b), parity & 1, abort_flag); };
 
   if (warp == 0) {
     // ---------------- copies
@@ -161,179 +205,186 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     uint32_t i = 0;
     bool go = true;
     for (;;) {
+      // lane x: page x (and its scales) of the 16 tiles of this piece from tab_u on, and of the 16 after
+      // them, whose table entries and then scales are fetched while these are used
       const int limit = Tiles(a).limit(pc.r, pc.qt);
-      int tab_u = -32, page = -1;                      // lane x: page x of the 16 tiles from tab_u on
-      float ks = 1.f, vs = 1.f;
+      int tab_u = pc.u0, next_page = -1;
+      auto table = [&](int from) {
+        const int x = 2 * from + lane;
+        return (long long)x * KV_PAGE < limit && x < 2 * pc.u1 ? a.table[(size_t)pc.b * a.width + x] : -1;
+      };
+      auto scales = [&](int &pg, float &k, float &v) {
+        if (pg < 0 || pg >= a.n_pages) pg = -1;
+        k = v = 1.f;
+        if (pg >= 0) {
+          k = a.ks[(size_t)pg * a.nkv + pc.h];
+          v = a.vs[(size_t)pg * a.nkv + pc.h];
+        }
+      };
+      float ks, vs, next_ks = 1.f, next_vs = 1.f;
+      int page = table(tab_u);
+      scales(page, ks, vs);
+      float ev = log2f(vs), iv = 1.f / vs;
       for (int u = pc.u0; u < pc.u1 && go; ++u, ++i) {
-        if (tab_u < 0 || u >= tab_u + 16) {
+        if (u == tab_u + 16) {
           tab_u = u;
-          const int x = 2 * u + lane;
-          page = (long long)x * KV_PAGE < limit && x < 2 * pc.u1 ? a.table[(size_t)pc.b * a.width + x] : -1;
-          if (page < 0 || page >= a.n_pages) page = -1;
-          ks = vs = 1.f;
-          if (page >= 0) {
-            ks = a.ks[(size_t)page * a.nkv + pc.h];
-            vs = a.vs[(size_t)page * a.nkv + pc.h];
-          }
+          page = next_page;
+          ks = next_ks;
+          ev = log2f(next_vs);
+          iv = 1.f / next_vs;
         }
-        const int at = 2 * (u - tab_u);
-        const int stg = i % KT_STAGES;
+        if (u == tab_u + 4) next_page = table(tab_u + 16);
+        if (u == tab_u + 10) scales(next_page, next_ks, next_vs);
+        const int at = 2 * (u - tab_u), stg = i % KT_STAGES;
         const uint32_t use = i / KT_STAGES;
-        KtSide sd;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          sd.page[x] = __shfl_sync(0xffffffffu, page, at + x);
-          sd.ks[x] = __shfl_sync(0xffffffffu, ks, at + x);
-          sd.vs[x] = __shfl_sync(0xffffffffu, vs, at + x);
+        go = use == 0 || (wait(sh.kempty[stg], use - 1) && wait(sh.vempty[stg], use - 1));
+        go = __all_sync(0xffffffffu, go);
+        if (!go) break;
+        const int x = lane - at;                       // the two lanes that hold the tile's pages write and copy them
+        const unsigned there = __popc(__ballot_sync(0xffffffffu, (x == 0 || x == 1) && page >= 0));
+        if (x == 0 || x == 1) {
+          KtSide &sd = sh.side[i % KT_SIDE];
+          sd.page[x] = page;
+          sd.ks[x] = ks;
+          sd.ev[x] = ev;
+          sd.iv[x] = iv;
         }
+        __syncwarp();
         if (lane == 0) {
-          if (use > 0) go = wait(sh.kempty[stg], use - 1) && wait(sh.vempty[stg], use - 1);
-          if (go) {
-            sh.side[i % KT_SIDE] = sd;
-            const uint32_t there = (sd.page[0] >= 0) + (sd.page[1] >= 0);
-            if (there) {
-              mbar_expect_tx(bar(sh.kfull[stg]), there * Lay::PAGE8);
-              mbar_expect_tx(bar(sh.vfull[stg]), there * Lay::PAGE8);
-            } else {
-              mbar_arrive(bar(sh.kfull[stg]));
-              mbar_arrive(bar(sh.vfull[stg]));
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (sd.page[x] >= 0) {
-                tma_load_3d(base + Lay::K0 + (2 * stg + x) * Lay::PAGE8, &p.kmap, 0, 0, sd.page[x] * a.nkv + pc.h, bar(sh.kfull[stg]));
-                bulk_load(base + Lay::V0 + (2 * stg + x) * Lay::PAGE8, a.vp + kv8_block(sd.page[x], pc.h, a.nkv, HD), Lay::PAGE8,
-                          bar(sh.vfull[stg]));
-              }
+          if (there) {
+            mbar_expect_tx(bar(sh.kfull[stg]), there * Lay::PAGE8);
+            mbar_expect_tx(bar(sh.vfull[stg]), there * Lay::PAGE8);
+          } else {
+            mbar_arrive(bar(sh.kfull[stg]));
+            mbar_arrive(bar(sh.vfull[stg]));
           }
         }
-        go = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
-        if (!go) break;
+        __syncwarp();
+        if ((x == 0 || x == 1) && page >= 0) {
+          tma_load_3d(base + Lay::K0 + (2 * stg + x) * Lay::PAGE8, &p.kmap, 0, 0, page * a.nkv + pc.h, bar(sh.kfull[stg]));
+          bulk_load(base + Lay::V0 + (2 * stg + x) * Lay::PAGE8, a.vp + kv8_block(page, pc.h, a.nkv, HD), Lay::PAGE8, bar(sh.vfull[stg]));
+        }
       }
       if (!go || pc.left <= 0) break;
       kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
     }
-    if (lane == 0) {
-      // copies in flight end before the CTA does (bounded; at once unless a wait ran out)
-      const unsigned long long t0 = global_ns();
-      for (uint32_t j = i > KT_STAGES ? i - KT_STAGES : 0; j < i; ++j)
-        while (!(mbar_try_wait(bar(sh.kfull[j % KT_STAGES]), j / KT_STAGES & 1) &&
-                 mbar_try_wait(bar(sh.vfull[j % KT_STAGES]), j / KT_STAGES & 1)) && global_ns() - t0 < TC_WAIT_NS) {
-        }
-    }
+    // copies in flight end before the CTA does (bounded; at once unless a wait ran out)
+    const unsigned long long t0 = global_ns();
+    for (uint32_t j = i > KT_STAGES ? i - KT_STAGES : 0; j < i; ++j)
+      while (!(mbar_try_wait(bar(sh.kfull[j % KT_STAGES]), j / KT_STAGES & 1) &&
+               mbar_try_wait(bar(sh.vfull[j % KT_STAGES]), j / KT_STAGES & 1)) && global_ns() - t0 < TC_WAIT_NS) {
+      }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMAs
-      constexpr uint32_t idS0 = idesc_of(0, 0, KT_TOKENS), idS1 = idesc_of(1, 0, KT_TOKENS), idO = idesc_of(0, 0, HD);
-      Kv8Piece sp = pc;                                // the piece whose S is issued next
-      int su = sp.u0;
-      uint32_t si = 0, spn = 0;                        // its tile and piece ordinals
-      bool more = true;
-      auto issue_s = [&]() {
-        if (su == sp.u0 && !wait(sh.q_full[spn & 1], spn >> 1)) return false;
-        const int stg = si % KT_STAGES;
-        if (!wait(sh.kfull[stg], si / KT_STAGES)) return false;
+    // ---------------- MMAs
+    constexpr uint32_t idS0 = idesc_of(0, 0, KT_TOKENS), idS1 = idesc_of(1, 0, KT_TOKENS), idO = idesc_of(0, 0, HD);
+    const uint32_t lead = lane == 0;
+    auto wait_all = [&](uint64_t &b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+    const uint64_t k0 = HD == 128 ? sw128_desc(base + Lay::K0) : sw64_desc(base + Lay::K0), w0 = sw128_desc(base + Lay::W0);
+    const uint32_t k_hi = (uint32_t)(k0 >> 32), w_hi = (uint32_t)(w0 >> 32);
+    Kv8Piece sp = pc;                                  // the piece whose S is issued next
+    int s_left = sp.u1 - sp.u0;                        // its tiles without S
+    uint32_t si = 0, spn = 0;                          // tile and piece ordinals of S
+    bool new_q = true, more = true;
+    auto issue_s = [&]() {
+      if (new_q && !wait_all(sh.q_full[spn & 1], spn >> 1)) return false;
+      new_q = false;
+      const uint32_t stg = si % KT_STAGES, par = si & 1;
+      if (!wait_all(sh.kfull[stg], si / KT_STAGES)) return false;
+      tc_fence_after();
+      const uint32_t kd = (uint32_t)k0 + stg * (2 * Lay::PAGE8 >> 4), d = tmem + par * 128, q = tmem + TM_Q + (spn & 1) * 64;
+#pragma unroll
+      for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) mma_f8(lead, d, q + 32 * pl + 8 * k, kd + 2 * k, k_hi, pl ? idS1 : idS0, (pl | k) ? 1u : 0u);
+      commit_lead(lead, bar(sh.s_full[par]));
+      commit_lead(lead, bar(sh.kempty[stg]));
+      if (lead) mbar_arrive(bar(sh.s_full[par]));
+      ++si;
+      if (--s_left == 0) {
+        more = sp.left > 0;
+        if (more) {
+          kv8_next_piece<KT_TOKENS, KT_ROWS>(a, sp);
+          s_left = sp.u1 - sp.u0;
+          ++spn;
+          new_q = true;
+        }
+      }
+      return true;
+    };
+    bool go = issue_s();
+    uint32_t i = 0;
+    for (uint32_t pn = 0; go; ++pn) {
+      const int n = pc.u1 - pc.u0;
+      for (int x = 0; x < n; ++x, ++i) {
+        if (more && !(go = issue_s())) break;
+        const uint32_t par = i & 1;
+        if (!(go = wait_all(sh.w_full[par], i >> 1))) break;
+        if (x == 0 && pn > 0 && !(go = wait_all(sh.o_empty, pn - 1))) break;
+        if (!(go = wait_all(sh.p_full[par], i >> 1))) break;
         tc_fence_after();
-        const uint32_t ks = base + Lay::K0 + 2 * stg * Lay::PAGE8, d = tmem + (si & 1) * 128, q = tmem + TM_Q + (spn & 1) * 64;
+        const uint32_t wd = (uint32_t)w0 + par * (2 * Lay::PAGE16 >> 4), pa = tmem + par * 128;
 #pragma unroll
-        for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-          for (int k = 0; k < HD / 32; ++k)
-            umma_f8_ts(d, q + 32 * pl + 8 * k, HD == 128 ? sw128_desc(ks + 32 * k) : sw64_desc(ks + 32 * k), pl ? idS1 : idS0,
-                       (pl | k) ? 1u : 0u);
-        umma_commit(bar(sh.kempty[stg]));
-        mbar_arrive(bar(sh.s_full[si & 1]));
-        umma_commit(bar(sh.s_full[si & 1]));
-        ++si;
-        if (++su == sp.u1) {
-          if (sp.left > 0) {
-            kv8_next_piece<KT_TOKENS, KT_ROWS>(a, sp);
-            su = sp.u0;
-            ++spn;
-          } else {
-            more = false;
-          }
-        }
-        return true;
-      };
-      bool go = issue_s();
-      uint32_t i = 0;
-      for (uint32_t pn = 0; go; ++pn) {
-        for (int u = pc.u0; go && u < pc.u1; ++u, ++i) {
-          if (more && !(go = issue_s())) break;
-          const int par = i & 1;
-          if (!(go = wait(sh.p_full[par], i >> 1))) break;
-          if (!(go = wait(sh.w_full[par], i >> 1))) break;
-          if (u == pc.u0 && pn > 0 && !(go = wait(sh.o_empty, pn - 1))) break;
-          tc_fence_after();
-          const uint32_t w = base + Lay::W0 + 2 * par * Lay::PAGE16;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)                  // 16 tokens each; k >> 2: the page
-            umma_bf16_ts(tmem + TM_O, tmem + par * 128 + 64 * (k >> 2) + 8 * (k & 3),
-                         sw128_desc(w + (k >> 2) * Lay::PAGE16 + (k & 3) * 32), idO, (u > pc.u0 || k) ? 1u : 0u);
-          umma_commit(bar(sh.w_empty[par]));
-          umma_commit(bar(sh.pv_done));
-        }
-        if (!go) break;
-        umma_commit(bar(sh.o_full));
-        if (pc.left <= 0) break;
-        kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
+        for (int k = 0; k < 8; ++k)                    // 16 tokens each; k >> 2: the page
+          mma_f16(lead, tmem + TM_O, pa + 64 * (k >> 2) + 8 * (k & 3), wd + (k >> 2) * (Lay::PAGE16 >> 4) + (k & 3) * 2, w_hi, idO,
+                  k ? 1u : (uint32_t)(x > 0));
+        commit_lead(lead, bar(sh.pv_done[par]));
       }
-      // MMAs in flight end before the tensor memory is given back
-      umma_commit(bar(sh.drain));
-      const unsigned long long t0 = global_ns();
-      while (!mbar_try_wait(bar(sh.drain), 0) && global_ns() - t0 < TC_WAIT_NS) {
-      }
+      if (!go) break;
+      commit_lead(lead, bar(sh.o_full));
+      if (pc.left <= 0) break;
+      kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
+    }
+    // MMAs in flight end before the tensor memory is given back
+    __syncwarp();
+    commit_lead(lead, bar(sh.drain[0]));
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(bar(sh.drain[0]), 0) && global_ns() - t0 < TC_WAIT_NS) {
     }
   } else if (warp < 10) {
-    // ---------------- Q, softmax, results: warps w and w + 4 share the rows of lane quarter w % 4
+    // ---------------- Q, softmax, results: row r, page `half` of each tile
     const int q = warp & 3, half = (warp - 2) >> 2, r = q * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     const int group = a.nq / a.nkv, tpt = Tiles(a).tpt;
     bool ok = true;
-    // writes Q of a piece; returns the row's factor (NaN: the row holds an infinity or NaN)
+    // writes this half of the dims of Q of a piece; returns the row's factor (NaN: the row holds
+    // an infinity or NaN)
     auto load_q = [&](const Kv8Piece &x, uint32_t pn) {
       const int tk = x.qt * tpt + r / group;
       const bool live = r < tpt * group && tk < x.r.n;
-      constexpr int N = HD / 2;                        // this half's dims
-      float v[N];
+      constexpr int N = HD / 2;                        // dims of a half
       float big = 0.f;
       bool fin = true;
-      const bf16 *src = (const bf16 *)a.q + (int64_t)(x.r.row0 + tk) * a.q_stride + (int64_t)(x.h * group + r % group) * HD + N * half;
+      const bf16 *src = (const bf16 *)a.q + (int64_t)(x.r.row0 + tk) * a.q_stride + (int64_t)(x.h * group + r % group) * HD;
       uint4 w[N / 8];
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i) w[i] = live ? *(const uint4 *)(src + 8 * i) : make_uint4(0, 0, 0, 0);
+      for (int hf = 1; hf >= 0; --hf) {                // the other half for the row's maximum, then this one
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i) {
-        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int i = 0; i < N / 8; ++i) w[i] = live ? *(const uint4 *)(src + N * (half ^ hf) + 8 * i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = __uint_as_float(e[j] << 16);
-          v[8 * i + 2 * j + 1] = __uint_as_float(e[j] & 0xffff0000u);
+        for (int i = 0; i < N / 8; ++i) {
+          const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float v0 = __uint_as_float(e[j] << 16), v1 = __uint_as_float(e[j] & 0xffff0000u);
+            big = fmaxf(big, fmaxf(fabsf(v0), fabsf(v1)));
+            fin = fin && fabsf(v0) <= 3.402823466e38f && fabsf(v1) <= 3.402823466e38f;
+          }
         }
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        big = fmaxf(big, fabsf(v[i]));
-        fin = fin && fabsf(v[i]) <= 3.402823466e38f;
-      }
-      if (!fin) big = INFINITY;
-      sh.xsum[half][r] = big;
-      pair_sync(1 + q);
-      big = fmaxf(big, sh.xsum[half ^ 1][r]);
-      pair_sync(1 + q);                                // (the row sums reuse the words)
-      const bool bad = !(big <= 3.402823466e38f);
-      const int e = bad ? 0 : max(-100, (int)(__float_as_uint(big) >> 23) - 127);
-      const float up = bad ? 0.f : exp2f((float)(7 - e));
+      const int e = fin ? max(-100, (int)(__float_as_uint(big) >> 23) - 127) : 0;
+      const float up = exp2f((float)(7 - e));
       const uint32_t dst = lane_base + TM_Q + (pn & 1) * 64 + half * (N / 4);
 #pragma unroll
       for (int c = 0; c < N / 4; c += 8) {
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float y[4];
+          const uint4 &b = w[(c + j) / 2];
+          const uint32_t e0 = j & 1 ? b.z : b.x, e1 = j & 1 ? b.w : b.y;
+          float y[4] = {__uint_as_float(e0 << 16), __uint_as_float(e0 & 0xffff0000u), __uint_as_float(e1 << 16),
+                        __uint_as_float(e1 & 0xffff0000u)};
 #pragma unroll
-          for (int z = 0; z < 4; ++z) y[z] = bad ? 0.f : v[4 * (c + j) + z] * up;
+          for (int z = 0; z < 4; ++z) y[z] = fin ? y[z] * up : 0.f;
           const uint32_t h0 = f32_to_e4m3x2(y[0], y[1]), h1 = f32_to_e4m3x2(y[2], y[3]);
           const float2 f0 = e4m3x2_to_f32(h0), f1 = e4m3x2_to_f32(h1);
           hi[j] = h0 | h1 << 16;
@@ -346,15 +397,15 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.q_full[pn & 1]));
-      return bad ? NAN : a.scale * 1.44269504088896341f * exp2f((float)(e - 7));
+      return fin ? a.scale * 1.44269504088896341f * exp2f((float)(e - 7)) : NAN;
     };
     float rs_next = load_q(pc, 0);
-    uint32_t i = 0, pn = 0;
+    uint32_t i = 0, pn = 0;                            // tile and piece ordinals
     bool first = true;
     for (;; ++pn) {
       const float rs = rs_next;
-      Kv8Piece nx = pc;
       if (pc.left > 0) {
+        Kv8Piece nx = pc;
         kv8_next_piece<KT_TOKENS, KT_ROWS>(a, nx);
         rs_next = load_q(nx, pn + 1);
       }
@@ -366,29 +417,19 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       float m_used = -INFINITY, l = 0.f;
       for (int u = pc.u0; u < pc.u1; ++u, ++i) {
         const int par = i & 1;
-        const bool got = __all_sync(0xffffffffu, ok && wait(sh.s_full[par], i >> 1));
-        const uint32_t sa = lane_base + par * 128 + half * 64;   // my 64 tokens: page 2 u + half
-        float sc[64];
-        float mt = -INFINITY;
+        ok = __all_sync(0xffffffffu, ok && wait(sh.s_full[par], i >> 1));
+        if (!ok) break;
+        const uint32_t sa = lane_base + par * 128 + half * 64;   // my 64 tokens
         const KtSide &sd = sh.side[i % KT_SIDE];
-        float c = 0.f, ev = 0.f, iv = 1.f;
-        if (got && !quiet) {
-          const int page = sd.page[half];
-          c = fac * sd.ks[half];
-          ev = log2f(sd.vs[half]);
-          iv = 1.f / sd.vs[half];
-          tc_fence_after();
-#pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            uint32_t t[16];
-            tmem_ld16(sa + c0, t);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sc[c0 + j] = __uint_as_float(t[j]);
-          }
-          const int pgn = 2 * u + half;
-          if (page < 0 || (pgn + 1) * KV_PAGE > open) {
-            const uint64_t see = page < 0 || !live ? 0 : kv8_visible(a, pc.r, tk, pgn);
+        const float c = fac * sd.ks[half], ev = sd.ev[half];
+        const bool partial = sd.page[half] < 0 || (long long)(2 * u + half + 1) * KV_PAGE > open;
+        // S of my tokens, without what the row does not see
+        auto load_s = [&](float *sc) {
+          tmem_ld32(sa, sc);
+          tmem_ld32(sa + 32, sc + 32);
+          tmem_ld_wait();
+          if (partial) {
+            const uint64_t see = live && sd.page[half] >= 0 ? kv8_visible(a, pc.r, tk, 2 * u + half) : 0;
             const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -396,71 +437,92 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
               if (!(s1 >> j & 1)) sc[32 + j] = -INFINITY;
             }
           }
+        };
+        // P of 32 tokens for the present reference, as f16 pairs; returns their sum
+        // (a factor of zero may meet the -infinity of a hidden token: such rows are not written)
+        auto exps = [&](const float *v, uint32_t *pw) {
+          const float off = ev + KT_BIAS - (m_used == -INFINITY ? 0.f : m_used);
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-          for (int j = 0; j < 64; ++j) mt = fmaxf(mt, sc[j]);
+          for (int j = 0; j < 16; ++j) {
+            float2 e = fma2(make_float2(v[2 * j], v[2 * j + 1]), c, off);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[j & 1] = add2(sum[j & 1], e);
+            pw[j] = pack_f16(e.x, e.y);
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          return sum[0].x + sum[0].y;
+        };
+        float sc[64];
+        uint32_t pw[16];
+        float mt = -INFINITY, sum = 0.f;
+        if (!quiet) {
+          tc_fence_after();
+          load_s(sc);
+          float mx[4];                                 // four chains, three values a step
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(sc[16 * j], sc[16 * j + 1]);
+#pragma unroll
+          for (int k = 2; k < 16; k += 2)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], sc[16 * j + k]), sc[16 * j + k + 1]);
+          mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           mt = mt == -INFINITY ? mt : fmaf(mt, c, ev);
         }
+        // The maxima are traded with the other half's warp. A first tile waits for them; any other keeps the
+        // reference and makes half of its P meanwhile, in vain only if some row of the pair outgrew
+        // its reference by 2^8.
+        bool grow = u == pc.u0 || __any_sync(0xffffffffu, mt > m_used + 8.f);
         sh.xmax[par][half][r] = mt;
-        if (lane == 0) sh.xok[par][half][q] = got;
-        pair_sync(1 + q);
-        const float mp = sh.xmax[par][half ^ 1][r];
-        ok = got && *(volatile int *)&sh.xok[par][half ^ 1][q] != 0;
+        if (lane == 0) sh.xgrow[par][half][q] = grow;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.x_ready[par][q]));
+        if (!grow && !quiet) sum = exps(sc, pw);
+        ok = __all_sync(0xffffffffu, wait(sh.x_ready[par][q], i >> 1));
         if (!ok) break;
-        mt = fmaxf(mt, mp);
-        if (u == pc.u0) {
-          m_used = mt;
-        } else if (__any_sync(0xffffffffu, mt > m_used + 8.f)) {
-          const float m_new = fmaxf(m_used, mt);
+        grow = grow || *(volatile int *)&sh.xgrow[par][half ^ 1][q] != 0;
+        if (grow) {
+          const float m_new = fmaxf(m_used, fmaxf(mt, sh.xmax[par][half ^ 1][r]));
           const float corr = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
           m_used = m_new;
-          // P.V of the previous tile must have retired (the one before it has: its end preceded this S)
-          if (!__all_sync(0xffffffffu, wait(sh.pv_done, i - 1))) {
-            ok = false;                                // the partner learns of it at the next exchange
-            continue;
-          }
-          tc_fence_after();
+          if (u > pc.u0) {
+            // O so far is scaled down (P.V of the tile before must be done; this one's waits for this warp)
+            l *= corr;
+            ok = __all_sync(0xffffffffu, wait(sh.pv_done[par ^ 1], (i - 1) >> 1));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < HD / 2; c0 += 16) {
-            uint32_t t[16];
-            const uint32_t oa = lane_base + TM_O + (HD / 2) * half + c0;
-            tmem_ld16(oa, t);
-            tmem_ld_wait();
+            for (int c0 = 0; c0 < HD / 2; c0 += 16) {
+              const uint32_t oa = lane_base + TM_O + (HD / 2) * half + c0;
+              tmem_ld16(oa, pw);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) t[j] = __float_as_uint(__uint_as_float(t[j]) * corr);
-            tmem_st16(oa, t);
+              for (int j = 0; j < 16; ++j) pw[j] = __float_as_uint(__uint_as_float(pw[j]) * corr);
+              tmem_st16(oa, pw);
+            }
           }
-          l *= corr;
+          if (!quiet) sum = exps(sc, pw);
         }
         if (!quiet) {
-          const float off = ev - (m_used == -INFINITY ? 0.f : m_used) + KT_BIAS;
-          float sum = 0.f;
-#pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 32) {
-            uint32_t pw[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float s0 = sc[c0 + 2 * j], s1 = sc[c0 + 2 * j + 1];
-              // (a factor of zero must not meet the -infinity of a hidden token: such rows are not written)
-              const float e0 = ex2(fmaf(s0, c, off)), e1 = ex2(fmaf(s1, c, off));
-              sum += e0 + e1;
-              pw[j] = pack_f16(e0, e1);
-            }
-            tmem_st16(sa + c0 / 2, pw);
-          }
-          l = fmaf(sum, iv, l);
+          tmem_st16(sa, pw);
+          sum += exps(sc + 32, pw);
+          tmem_st16(sa + 16, pw);
+          l = fmaf(sum, sd.iv[half], l);
           tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.p_full[par]));
       }
-      // the row's sum over both halves (run by both warps of the pair)
-      sh.xsum[half][r] = l;
-      if (lane == 0) sh.xok[0][half][q] = ok;
-      pair_sync(1 + q);
-      float l_row = l + sh.xsum[half ^ 1][r];
-      ok = ok && *(volatile int *)&sh.xok[0][half ^ 1][q] != 0;
-      pair_sync(1 + q);
+      // the row's sum over both halves (by piece parity: the other warp may be a piece ahead)
+      float l_row = 0.f;
+      const int pp = pn & 1;
+      sh.lsum[pp][half][r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.l_ready[pp][half][q]));
+      ok = __all_sync(0xffffffffu, ok && wait(sh.l_ready[pp][half ^ 1][q], pn >> 1));
+      if (ok) l_row = sh.lsum[pp][0][r] + sh.lsum[pp][1][r];
       ok = __all_sync(0xffffffffu, ok && wait(sh.o_full, pn));
       tc_fence_after();
       const bool whole = pc.u1 - pc.u0 == pc.units;
@@ -476,15 +538,15 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
 #pragma unroll 1
       for (int c0 = 0; c0 < HD / 2; c0 += 16) {
         uint32_t t[16];
-        if (ok) {
-          tmem_ld16(lane_base + TM_O + (HD / 2) * half + c0, t);
+        const int d0 = (HD / 2) * half + c0;
+        if (ok && !quiet) {
+          tmem_ld16(lane_base + TM_O + d0, t);
           tmem_ld_wait();
         }
         if (!live) continue;
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = ok ? __uint_as_float(t[j]) : NAN;
-        const int d0 = (HD / 2) * half + c0;
         if (nan_v) {                                   // rows that see a NaN value get it (rare)
           uint32_t hit = 0;
           const int lim = Tiles(a).limit(pc.r, pc.qt);
@@ -522,7 +584,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.o_empty));
       if (pc.left <= 0) break;
-      pc = nx;
+      kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
       first = false;
     }
   } else {
@@ -534,44 +596,57 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       const int open = a.mask == DFLASH_MASK_NONE ? pc.r.len : max(0, pc.r.len - pc.r.n);
       for (int u = pc.u0; u < pc.u1; ++u, ++i) {
         const int stg = i % KT_STAGES, par = i & 1;
-        go = wait(sh.vfull[stg], i / KT_STAGES) && (i < 2 || wait(sh.w_empty[par], (i >> 1) - 1));
+        go = wait(sh.vfull[stg], i / KT_STAGES) && (i < 2 || wait(sh.pv_done[par], (i >> 1) - 1));
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
+        constexpr int N = HD * 4 / KT_WIDEN;           // pieces of 16 tokens of one dim: all loads first
+        uint4 v[2][N];
+        const uint32_t src = base + Lay::V0 + 2 * stg * Lay::PAGE8 + tid * 16;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const bool there = sh.side[i % KT_SIDE].page[x] >= 0;
-          const int p0 = (2 * u + x) * KV_PAGE;        // the page's first token
-          const bool partial = p0 + KV_PAGE > open;
-          const uint32_t src = base + Lay::V0 + (2 * stg + x) * Lay::PAGE8, dst = base + Lay::W0 + (2 * par + x) * Lay::PAGE16;
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[x][j] = lds128(src + x * Lay::PAGE8 + KT_WIDEN * 16 * j);
+        const KtSide &sd = sh.side[i % KT_SIDE];
+        if (sd.page[0] < 0 || sd.page[1] < 0 || (long long)(u + 1) * KT_TOKENS > open) {
           bool nan = false;
 #pragma unroll
-          for (int j = 0; j < HD * 4 / KT_WIDEN; ++j) {   // 16 tokens of one dim at a time
-            const int it = tid + KT_WIDEN * j, d = it >> 2, c = it & 3;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (there) v = lds128(src + it * 16);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            if (partial) {
-              const int tail = pc.r.len - p0 - 16 * c;
+          for (int x = 0; x < 2; ++x) {
+            // tokens that exist, from this thread's 16: the rest may be anything
+            const int tail = sd.page[x] < 0 ? 0 : pc.r.len - (2 * u + x) * KV_PAGE - 16 * (tid & 3);
+            const bool hidden = (long long)(2 * u + x + 1) * KV_PAGE > open;   // some row does not see some token
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+              uint32_t *w = (uint32_t *)&v[x][j];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const int n = tail - 4 * k;            // tokens that exist: the rest may be anything
+                const int n = tail - 4 * k;
                 w[k] = n >= 4 ? w[k] : n <= 0 ? 0u : w[k] & ((1u << 8 * n) - 1);
-                const uint32_t nb = nan_bytes(w[k]);   // must not meet the zero weight of a row that does not see it
+                const uint32_t nb = hidden ? nan_bytes(w[k]) : 0u;   // must not meet a hidden token's zero weight
                 nan |= nb != 0;
                 w[k] &= ~byte_mask(nb);
               }
             }
+          }
+          if (nan) *(volatile int *)&sh.nan_piece[pn & 3] = (int)pn + 1;
+        }
+        // row d of V^T in 128-byte rows, its 16-byte chunk c at c ^ (d & 7); d & 7 is the same for all j
+        const uint32_t dst = base + Lay::W0 + 2 * par * Lay::PAGE16 + (tid >> 2) * 128;
+        const uint32_t c0 = (2 * (tid & 3)) ^ (tid >> 2 & 7), c1 = c0 ^ 1;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const uint32_t w[4] = {v[x][j].x, v[x][j].y, v[x][j].z, v[x][j].w};
             uint32_t f[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               f[2 * k] = e4m3x2_to_f16x2(w[k]);
               f[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
             }
-            sts128(dst + d * 128 + (((2 * c) ^ (d & 7)) << 4), f);
-            sts128(dst + d * 128 + (((2 * c + 1) ^ (d & 7)) << 4), f + 4);
+            const uint32_t at = dst + x * Lay::PAGE16 + j * (KT_WIDEN / 4 * 128);
+            sts128(at + 16 * c0, f);
+            sts128(at + 16 * c1, f + 4);
           }
-          if (nan) *(volatile int *)&sh.nan_piece[pn & 3] = (int)pn + 1;
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

@@ -38,7 +38,7 @@ struct Kv8Desc {
 };
 
 // sum over i < n of floor((a i + b) / m), for a, b >= 0
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   while (n > 0) {
     if (a >= m) s += (n - 1) * n / 2 * (a / m), a %= m;
