@@ -178,11 +178,17 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
 
 // ---------------------------------------------------------------- quantised append
 // One CTA of (window of rows, kv head, K or V) walks the runs that begin in its window: a run is the
-// consecutive rows of one page, so a page has one writer. Per run: the largest finite |x| gives
-// the scale 2^e; the rows are read once into registers, scaled (exact), rounded to e4m3 once and
-// stored. A page that grows its scale has its kept rows rounded again. V goes through a shared
-// tile, since its pages are transposed.
+// consecutive rows of one page, so a page has one writer. Per run: the rows are read once into
+// registers; the largest finite |x| gives the scale 2^e; the values are scaled (exact), rounded to e4m3
+// once and stored. A page that grows its scale has its kept rows rounded again. V goes through a
+// shared tile, since its pages are transposed: a thread holds neighbouring tokens of its dims, so that
+// the tile is written in words of four tokens.
+//
+// Bound by latency for a few rows (scale, rows and slots are dependent loads) and by memory for many.
+// The slots of a run are found by every warp for itself (a run whose slots rise by one, which is what a
+// plan makes, needs no barrier); only two barriers are left, around the CTA's maximum and V's tile.
 constexpr int KA_THREADS = 256;
+constexpr int KV8_CTAS = 152 * 8;                     // CTAs of KA_THREADS that the GPU holds at once
 
 template <typename T>
 struct AppendArgs {
@@ -217,140 +223,137 @@ template <typename T, int HD>
 __global__ void __launch_bounds__(KA_THREADS) k_kv8_append(const AppendArgs<T> a) {
   constexpr int V = 16 / sizeof(T);                   // values of a 16-byte load
   constexpr int TPR = HD / V;                         // threads of a row
-  constexpr int RPP = KA_THREADS / TPR;               // rows of a pass
-  constexpr int NP = KV_PAGE / RPP;                   // passes of a page
+  constexpr int NP = KV_PAGE * TPR / KA_THREADS;      // neighbouring rows of a thread
   __shared__ int owner[KV_PAGE];                      // row that stays at each offset, -1: none
   __shared__ int s_end;
   __shared__ float s_max[KA_THREADS / 32];
-  __shared__ __align__(16) uint8_t tile[HD][KV_PAGE + 4];
+  __shared__ __align__(16) uint32_t tile[HD * (KV_PAGE / 4)];   // word w of dim d at w ^ (d / 8 & 15)
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, h = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, h = blockIdx.y;
   const bool isv = blockIdx.z != 0;
   const T *src = isv ? a.v : a.k;
   const int64_t stride = isv ? a.vs : a.ks;
   const int64_t n_slots = (int64_t)a.n_pages * KV_PAGE;
-  auto page_of = [&](int r) {                         // -1: a skipped row
-    const int64_t s = a.slot[r];
-    return s < 0 || s >= n_slots ? -1 : (int)(s / KV_PAGE);
+  auto slot_of = [&](int r) {                         // -1: a skipped row, or none
+    const int64_t s = r >= 0 && r < a.rows ? a.slot[r] : -1;
+    return s < n_slots && s >= 0 ? s : -1;
   };
   const int w0 = blockIdx.x * a.window, w1 = min(w0 + a.window, a.rows);
-  int i = w0, before = -2;                            // page of the last row that was not skipped
-  while (i < w1) {
-    const int page = page_of(i);                      // uniform: all threads read the same slot
-    if (page < 0) {
+  int i = w0;
+  while (i < w1) {                                    // uniform: all threads read the same slots
+    const int64_t s0 = slot_of(i), before = slot_of(i - 1);
+    const int page = (int)(s0 / KV_PAGE);
+    if (s0 < 0 || (before >= 0 && (int)(before / KV_PAGE) == page)) {   // skipped, or of a run begun before
       ++i;
       continue;
     }
-    if (before == -2) {                               // the window's first row: look back past its start
-      before = -1;
-      for (int r = i - 1; r >= 0 && before < 0; --r) before = page_of(r);
-    }
-    if (page == before) {                             // a run that an earlier row began
-      ++i;
-      continue;
-    }
-    before = page;
-    // the run's rows, and the row that stays at each offset
-    __syncthreads();
-    if (tid < KV_PAGE) owner[tid] = -1;
-    if (tid == 0) s_end = a.rows;
-    __syncthreads();
-    int end = a.rows;
-    for (int r = i; r < end; r += KA_THREADS) {
-      const int rr = r + tid;
-      if (rr < a.rows) {
-        const int p = page_of(rr);
-        if (p >= 0 && p != page) atomicMin(&s_end, rr);
+    // the run: slots s0, s0 + 1, .. as a rule
+    const int64_t s1 = slot_of(i + lane), s2 = slot_of(i + 32 + lane);
+    const uint64_t rising = (uint64_t)__ballot_sync(0xffffffffu, s2 == s0 + 32 + lane && s2 / KV_PAGE == page) << 32 |
+                            __ballot_sync(0xffffffffu, s1 == s0 + lane && s1 / KV_PAGE == page);
+    const int first = (int)(s0 % KV_PAGE), len = ~rising ? __ffsll(~rising) - 1 : 64;
+    const int64_t after = slot_of(i + len);
+    const bool plain = after < 0 || (int)(after / KV_PAGE) != page;
+    int end = i + len;
+    uint64_t owned;
+    if (plain) {
+      owned = (len == 64 ? ~0ull : (1ull << len) - 1) << first;
+    } else {                                          // slots in any order, some of them twice: the last row stays
+      __syncthreads();
+      if (tid < KV_PAGE) owner[tid] = -1;
+      if (tid == 0) s_end = a.rows;
+      end = a.rows;
+      __syncthreads();
+      for (int r = i; r < end; r += KA_THREADS) {
+        const int rr = r + tid;
+        const int64_t s = slot_of(rr);
+        const bool in = s >= 0 && (int)(s / KV_PAGE) == page;
+        if (rr < a.rows && !in) atomicMin(&s_end, rr);
+        __syncthreads();
+        end = s_end;
+        if (rr < end) atomicMax(&owner[(int)(s % KV_PAGE)], rr);
+        __syncthreads();
       }
-      __syncthreads();
-      end = s_end;
-      if (rr < end && page_of(rr) == page) atomicMax(&owner[(int)(a.slot[rr] % KV_PAGE)], rr);
-      __syncthreads();
+      owned = (uint64_t)__ballot_sync(0xffffffffu, owner[32 + lane] >= 0) << 32 |
+              __ballot_sync(0xffffffffu, owner[lane] >= 0);
     }
-    uint64_t owned = 0;
-    {
-      const uint32_t lo = __ballot_sync(0xffffffffu, owner[tid & 31] >= 0);
-      const uint32_t hi = __ballot_sync(0xffffffffu, owner[32 + (tid & 31)] >= 0);
-      owned = (uint64_t)hi << 32 | lo;
-    }
-    // rows of the page, one 16-byte piece per thread and pass
-    const int c = tid % TPR, rp = tid / TPR;
-    float x[NP][V];
+    // the CTA's rows of the page, one 16-byte piece per thread and row
+    const int c = tid % TPR, off0 = tid / TPR * NP;
+    uint4 q[NP];
     float big = 0.f;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      const int row = owner[p * RPP + rp];
-      if (row >= 0) {
-        const T *g = src + (int64_t)row * stride + (int64_t)h * HD + c * V;
-        const uint4 q = *(const uint4 *)g;
-        const T *t = (const T *)&q;
+      const int off = off0 + p, row = plain ? i + off - first : owner[off];
+      q[p] = owned >> off & 1 ? *(const uint4 *)(src + (int64_t)row * stride + (int64_t)h * HD + c * V) : make_uint4(0, 0, 0, 0);
+    }
+    float *sp = (isv ? a.vscale : a.kscale) + (size_t)page * a.nkv + h;
+    const bool fresh = owned & 1;
+    const float old = fresh ? 0.f : *sp;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[p][j] = to_f(t[j]);
-          big = fmaxf(big, finite_abs(x[p][j]));
-        }
-      }
+    for (int p = 0; p < NP; ++p) {
+      const T *t = (const T *)&q[p];
+#pragma unroll
+      for (int j = 0; j < V; ++j) big = fmaxf(big, finite_abs(to_f(t[j])));
     }
     big = warp_max(big);
-    if ((tid & 31) == 0) s_max[tid >> 5] = big;
-    __syncthreads();
+    if (lane == 0) s_max[tid >> 5] = big;
+    __syncthreads();                                  // (and every thread has read *sp)
 #pragma unroll
     for (int j = 0; j < KA_THREADS / 32; ++j) big = fmaxf(big, s_max[j]);
-    float *sp = (isv ? a.vscale : a.kscale) + (size_t)page * a.nkv + h;
     float scale = pow2f(scale_exp(big)), again = 1.f;
-    const bool fresh = owned & 1;
-    if (!fresh) {
-      const float old = *sp;
-      if (old >= scale) scale = old;
-      else again = old / scale;                       // powers of two: exact
-    }
+    if (old >= scale) scale = old;
+    else if (!fresh) again = old / scale;             // powers of two: exact
     const int last = 63 - __clzll(owned);
-    const uint64_t below = last == 63 ? ~0ull : (2ull << last) - 1;
-    const uint64_t kept = fresh || again == 1.f ? 0 : below & ~owned;
+    const uint64_t kept = fresh || again == 1.f ? 0 : (last == 63 ? ~0ull : (2ull << last) - 1) & ~owned;
     const float inv = 1.f / scale;                    // exact
-    __syncthreads();                                  // every thread has read *sp
     if (tid == 0) *sp = scale;
     uint8_t *blk = (isv ? a.vp : a.kp) + kv8_block(page, h, a.nkv, HD);
+    uint32_t w[NP][V / 4];                            // four dims of a row each
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const T *t = (const T *)&q[p];
+#pragma unroll
+      for (int j = 0; j < V; j += 4)
+        w[p][j / 4] = f32_to_e4m3x2(to_f(t[j]) * inv, to_f(t[j + 1]) * inv) |
+                      f32_to_e4m3x2(to_f(t[j + 2]) * inv, to_f(t[j + 3]) * inv) << 16;
+    }
     if (!isv) {
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const int off = p * RPP + rp;
+        const int off = off0 + p;
         uint8_t *dst = blk + off * HD + c * V;
-        uint32_t w[V / 4];
-        if (owned >> off & 1) {
+        if (kept >> off & 1) {
 #pragma unroll
-          for (int j = 0; j < V; j += 4)
-            w[j / 4] = f32_to_e4m3x2(x[p][j] * inv, x[p][j + 1] * inv) |
-                       f32_to_e4m3x2(x[p][j + 2] * inv, x[p][j + 3] * inv) << 16;
-        } else if (kept >> off & 1) {
-#pragma unroll
-          for (int j = 0; j < V; j += 4) w[j / 4] = rescale4(*(const uint32_t *)(dst + j), again);
-        } else {
+          for (int j = 0; j < V / 4; ++j) w[p][j] = rescale4(*(const uint32_t *)(dst + 4 * j), again);
+        } else if (!(owned >> off & 1)) {
           continue;
         }
-        if constexpr (V == 8) *(uint2 *)dst = make_uint2(w[0], w[1]);
-        else *(uint32_t *)dst = w[0];
+        if constexpr (V == 8) *(uint2 *)dst = make_uint2(w[p][0], w[p][1]);
+        else *(uint32_t *)dst = w[p][0];
       }
+      __syncthreads();                                // s_max and owner are free again
     } else {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int off = p * RPP + rp;
-        if (!(owned >> off & 1)) continue;
+      for (int j = 0; j < V; ++j) {
+        const int d = c * V + j;
+        auto byte = [&](int p) { return w[p][j / 4] >> (8 * (j & 3)) & 0xff; };
+        auto at = [&](int off) { return (uint8_t *)&tile[d * (KV_PAGE / 4) + ((off >> 2) ^ (d >> 3 & 15))] + (off & 3); };
+        if constexpr (NP >= 4) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          const uint32_t w = f32_to_e4m3x2(x[p][j] * inv, x[p][j + 1] * inv);
-          tile[c * V + j][off] = (uint8_t)w;
-          tile[c * V + j + 1][off] = (uint8_t)(w >> 8);
+          for (int p = 0; p < NP; p += 4) *(uint32_t *)at(off0 + p) = byte(p) | byte(p + 1) << 8 | byte(p + 2) << 16 | byte(p + 3) << 24;
+        } else {
+          *(uint16_t *)at(off0) = (uint16_t)(byte(0) | byte(1) << 8);
         }
       }
       __syncthreads();
+#pragma unroll 4
       for (int t = tid; t < HD * (KV_PAGE / 4); t += KA_THREADS) {
-        const int d = t / (KV_PAGE / 4), o4 = t % (KV_PAGE / 4) * 4;
-        const uint32_t mo = (uint32_t)(owned >> o4) & 15, mk = (uint32_t)(kept >> o4) & 15;
+        const int d = t / (KV_PAGE / 4), o = t % (KV_PAGE / 4);
+        const uint32_t mo = (uint32_t)(owned >> (4 * o)) & 15, mk = (uint32_t)(kept >> (4 * o)) & 15;
         if (!(mo | mk)) continue;
-        uint32_t *dst = (uint32_t *)(blk + d * KV_PAGE + o4);
-        uint32_t w = *(const uint32_t *)&tile[d][o4];
+        uint32_t *dst = (uint32_t *)(blk + 4 * t);
+        uint32_t x = tile[d * (KV_PAGE / 4) + (o ^ (d >> 3 & 15))];
         if (mo != 15) {                               // keep or round anew the word's other bytes
           const uint32_t was = *dst, re = mk ? rescale4(was, again) : was;
           uint32_t bo = 0, bk = 0;
@@ -359,10 +362,11 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv8_append(const AppendArgs<T> a
             bo |= (mo >> j & 1) ? 0xffu << 8 * j : 0;
             bk |= (mk >> j & 1) ? 0xffu << 8 * j : 0;
           }
-          w = (w & bo) | (re & bk) | (was & ~(bo | bk));
+          x = (x & bo) | (re & bk) | (was & ~(bo | bk));
         }
-        *dst = w;
+        *dst = x;
       }
+      __syncthreads();                                // the tile, s_max and owner are free again
     }
     i = min(end, w1);
   }
@@ -376,7 +380,7 @@ cudaError_t launch_append(const dflash_kv8_cache *c, int rows, const void *k, in
   // Rows of a window: one, so that every row of a few may start a page of its own at once, up to a
   // page's worth when there are CTAs enough for about two waves of 8 per SM without.
   const long ctas = (long)rows * c->n_kv_heads * 2;
-  a.window = (int)(ctas / (152 * 8 * 2));
+  a.window = (int)(ctas / (KV8_CTAS * 2));
   a.window = a.window < 1 ? 1 : a.window > KV_PAGE ? KV_PAGE : a.window;
   const dim3 g((rows + a.window - 1) / a.window, c->n_kv_heads, 2), b(KA_THREADS);
   return c->head_dim == 128 ? launch_pdl(k_kv8_append<T, 128>, g, b, 0, s, a)

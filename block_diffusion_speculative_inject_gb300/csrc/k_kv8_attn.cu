@@ -5,16 +5,18 @@
 // a warp with its own ring of K and V pages in shared memory, filled by bulk copies that it issues
 // itself, so that warps never wait for one another; 16 query rows (tokens x heads of a kv head)
 // are the M of mma.m16n8k16. Per page of 64 tokens:
-//   S[16, 64] = Q . K^T      K bytes go from shared memory to f16 B fragments in registers (exact)
+//   S[16, 64] = Q . K^T      K bytes widened to f16 in registers (exact)
 //   P = 2^(S c + log2 s_v - m), S = sum in log2 units, c = scale log2(e) s_k 2^row exponent
-//   O[16, hd] += P . V       V bytes likewise: both contractions run along 16 contiguous bytes
-// The contraction indices are permuted so that no fragment needs a shuffle: lane (g, t) of a B fragment
-// holds dims 32 t .. 32 t + 31 of token 16 (g >> 1) + 2 j + (g & 1) for K, and tokens 16 t .. 16 t + 15 of
-// a value dim for V, which makes the S accumulators of a lane exactly its part of the P fragments.
+//   O[16, hd] += P . V       V bytes likewise, P in f16
+// (m16n8k32 on the bytes themselves, with q in two 8-bit parts, was slower: 157 against 129 us.)
+// The contraction indices are permuted so that no fragment needs a shuffle and both contractions run
+// along 16 contiguous bytes: lane (g, t) of a B fragment holds dims 32 t .. 32 t + 31 of token
+// 16 (g >> 1) + 2 j + (g & 1) for K, and tokens 16 t .. 16 t + 15 of a value dim for V, which makes the S
+// accumulators of a lane exactly its part of the P fragments.
 // V's page scale goes into the exponent (P carries s_v, the row sum divides it out again), so that
 // O of pages of very different scale adds up in one accumulator. f16 holds q exactly (bf16 times a
-// power of two per row) and P to 11 bits with its largest at 2^14, so P is normal down to 2^-28. For
-// fp32, q and P are pairs of f16 (22 bits) and every product is two.
+// power of two per row) and P to 11 bits with its largest at 2^14, so P is normal down to 2^-28 of
+// that. For fp32, q and P are pairs of f16 (22 bits) and every product is two.
 #include <cmath>
 
 #include "kv8_attn.cuh"
@@ -36,8 +38,7 @@ struct KmLayout {
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -70,7 +71,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t *base = km_smem;
-  const uint32_t ring = smem_u32(base) + warp * Lay::RING;
+  uint8_t *my_ring = base + warp * Lay::RING;
+  const uint32_t ring = smem_u32(my_ring);
   uint64_t *bars = (uint64_t *)(base + KM_WARPS * Lay::RING) + warp * Lay::SLOTS;
   const uint32_t bar0 = smem_u32(bars);
   // per unit: page id (-1: not in the pool) and the two scales
@@ -81,18 +83,13 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   if (threadIdx.x == 0) s_abort = 0;
   fence_mbar_init();
   pdl_wait();
-  kv8_group_sums<KV_PAGE, KM_ROWS>(a, s_grp);
-
-  const long long total = s_grp[(a.n_req + 31) / 32];
-  const int workers = gridDim.x * KM_WARPS, me = warp * gridDim.x + blockIdx.x;
-  const long long chunk = (total + workers - 1) / workers;
-  const long long pos = (long long)me * chunk;
-  if (pos >= total) {
+  const int me = warp * gridDim.x + blockIdx.x;        // few workers spread over all SMs
+  long long chunk, item_begin;
+  Kv8Piece pc;
+  if (!kv8_start<KV_PAGE, KM_ROWS>(a, s_grp, me, gridDim.x * KM_WARPS, pc, chunk, item_begin)) {
     if (lane == 0) a.desc[me].units = 0;
     return;                                            // (no barrier of the whole CTA follows)
   }
-  long long item_begin;
-  Kv8Piece pc = kv8_first_piece<KV_PAGE, KM_ROWS>(a, s_grp, pos, min(chunk, total - pos), item_begin);
   if (lane == 0) a.desc[me] = Kv8Desc{item_begin, chunk, pc.units, pc.b, pc.qt, pc.h};
   bool first = true;
 
@@ -156,7 +153,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
     const uint32_t slot = take % Lay::SLOTS;
     ok = ok && kv8_wait(bar0 + 8 * slot, take / Lay::SLOTS & 1, (volatile int *)&s_abort);
     ok = __all_sync(0xffffffffu, ok);
-    return ring + slot * Lay::SLOT;
+    return (const uint8_t *)(my_ring + slot * Lay::SLOT);
   };
 
   for (;;) {
@@ -197,21 +194,20 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
       bad[rr] = (fb >> (lane & ~3) & 15) != 15;
       // q * 2^(14 - e): the largest is in [2^14, 2^15)
       const int e = bad[rr] ? 0 : max(-100, (int)(__float_as_uint(big) >> 23) - 127);
-      const float up = exp2f((float)(14 - e));
+      const float up = bad[rr] ? 0.f : exp2f((float)(14 - e));
       rs[rr] = a.scale * 1.44269504088896341f * exp2f((float)(e - 14));
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        float y[4];
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = bad[rr] ? 0.f : x[4 * k + j] * up;
-        qf[0][k][rr] = pack_f16(y[0], y[1]);
-        qf[0][k][2 + rr] = pack_f16(y[2], y[3]);
-        if constexpr (PL == 2) {
-          const float2 h0 = unpack_f16(qf[0][k][rr]), h1 = unpack_f16(qf[0][k][2 + rr]);
-          qf[PL - 1][k][rr] = pack_f16(y[0] - h0.x, y[1] - h0.y);
-          qf[PL - 1][k][2 + rr] = pack_f16(y[2] - h1.x, y[3] - h1.y);
+        for (int z = 0; z < 2; ++z) {                  // dims 4 k + 2 z, + 1 of the lane's
+          const float y0 = bad[rr] ? 0.f : x[4 * k + 2 * z] * up, y1 = bad[rr] ? 0.f : x[4 * k + 2 * z + 1] * up;
+          const uint32_t h = pack_f16(y0, y1);
+          qf[0][k][2 * z + rr] = h;
+          if constexpr (PL == 2) {
+            const float2 f = unpack_f16(h);
+            qf[PL - 1][k][2 * z + rr] = pack_f16(y0 - f.x, y1 - f.y);
+          }
         }
-      }
     }
     float o[NT][4];
 #pragma unroll
@@ -222,47 +218,47 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
 
 #pragma unroll 1
     for (int u = pc.u0; u < pc.u1; ++u) {
-      const uint32_t kslot = wait();
+      const uint8_t *kslot = wait();
       asm volatile("cp.async.wait_group %0;" ::"n"(Lay::SLOTS / 2 - (Lay::SLOTS == 3 ? 0 : 1)) : "memory");
       __syncwarp();
       const Side sd = side[take / 2 % Lay::SIDE];
       if (!ok) break;
       ++take;
-      if (sd.page < 0) {                               // not in the pool: nothing is seen
-        wait();
-        ++take;
-        __syncwarp();
-        feed();
-        feed();
-        continue;
-      }
       float s[8][4];
+      // two n tiles at a time, whose chains of sums interleave
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        const int key = 16 * (g >> 1) + 2 * j + (g & 1);
-        uint32_t w[HD / 16];
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t w[2][HD / 16];
 #pragma unroll
-        for (int c = 0; c < HD / 64; ++c) {
-          const uint4 v = lds128(kslot + key * HD + t * (HD / 4) + 16 * c);
-          w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+        for (int z = 0; z < 2; ++z) {
+          const uint8_t *row = kslot + (16 * (g >> 1) + 2 * (j + z) + (g & 1)) * HD + t * (HD / 4);
+#pragma unroll
+          for (int c = 0; c < HD / 64; ++c) {
+            const uint4 v = *(const uint4 *)(row + 16 * c);
+            w[z][4 * c] = v.x, w[z][4 * c + 1] = v.y, w[z][4 * c + 2] = v.z, w[z][4 * c + 3] = v.w;
+          }
+          s[j + z][0] = s[j + z][1] = s[j + z][2] = s[j + z][3] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t b0 = e4m3x2_to_f16x2(w[k]), b1 = e4m3x2_to_f16x2(w[k] >> 16);
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int pl = 0; pl < PL; ++pl) mma_f16(s[j], qf[pl][k], b0, b1);
-        }
+          for (int z = 0; z < 2; ++z) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16(w[z][k], b0, b1);
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) mma_f16(s[j + z], qf[pl][k], b0, b1);
+          }
       }
       __syncwarp();                                    // every lane has read the K page
       feed();
       // a lane's tokens: 16 t + 2 j + {0, 1} for n tile j
-      const bool partial = (u + 1) * KV_PAGE > open;
-      const float ev = log2f(sd.vs), iv = 1.f / sd.vs;
+      const bool out = sd.page < 0;                    // not in the pool: nothing of it is seen
+      const bool partial = out || (long long)(u + 1) * KV_PAGE > open;
+      const float ev = out ? 0.f : log2f(sd.vs), iv = out ? 1.f : 1.f / sd.vs;
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
-        const float c = rs[rr] * sd.ks;
+        const float c = out ? 0.f : rs[rr] * sd.ks;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -271,7 +267,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
       if (partial) {
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          const uint32_t hidden = tok[rr] < 0 ? ~0u : ~(uint32_t)(kv8_visible(a, pc.r, tok[rr], u) >> (16 * t));
+          const uint32_t hidden = out || tok[rr] < 0 ? ~0u : ~(uint32_t)(kv8_visible(a, pc.r, tok[rr], u) >> (16 * t));
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -324,15 +320,15 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
             pf[PL - 1][k][i] = pack_f16(x0 - h.x, x1 - h.y);
           }
         }
-      const uint32_t vslot = wait();
+      const uint8_t *vslot = wait();
       if (!ok) break;
       ++take;
       bool nan = false;
       // bytes of tokens that no row sees (a page's tail) may be anything
-      const int tail = min(16, max(0, pc.r.len - u * KV_PAGE - 16 * t));
+      const int tail = out ? 0 : min(16, max(0, pc.r.len - u * KV_PAGE - 16 * t));
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const uint4 v = lds128(vslot + (8 * i + g) * KV_PAGE + 16 * t);
+        const uint4 v = *(const uint4 *)(vslot + (8 * i + g) * KV_PAGE + 16 * t);
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if (partial) {
 #pragma unroll
@@ -346,7 +342,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t b0 = e4m3x2_to_f16x2(w[k]), b1 = e4m3x2_to_f16x2(w[k] >> 16);
+          uint32_t b0, b1;
+          e4m3x4_to_f16(w[k], b0, b1);
 #pragma unroll
           for (int pl = 0; pl < PL; ++pl) mma_f16(o[i], pf[pl][k], b0, b1);
         }
@@ -360,8 +357,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
           uint64_t at = 0;                             // tokens whose value is NaN in that dim
 #pragma unroll 1
           for (int k = 0; k < KV_PAGE; ++k) {
-            uint32_t byte;
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(vslot + (8 * (d >> 1) + 2 * t + (d & 1)) * KV_PAGE + k));
+            const uint32_t byte = vslot[(8 * (d >> 1) + 2 * t + (d & 1)) * KV_PAGE + k];
             at |= (uint64_t)((byte & 0x7f) == 0x7f) << k;
           }
           hit0 |= (uint32_t)((at & vis0) != 0) << d;
@@ -445,7 +441,7 @@ cudaError_t launch_rows(const Kv8AttnArgs &a, cudaStream_t s) {
                                        (int)KmLayout<HD>::SMEM);
   if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD>, dim3(KV8_SMS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
   if (e == cudaSuccess)
-    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, KM_ROWS>, dim3(KV8_SMS * KM_WARPS - 1, 1), dim3(128), 0, s, a);
+    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, KM_ROWS>, dim3(KV8_SMS * 2, 4), dim3(128), 0, s, a, KV8_SMS * KM_WARPS);
   return e;
 }
 

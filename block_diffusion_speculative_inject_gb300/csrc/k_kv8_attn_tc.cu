@@ -102,11 +102,6 @@ __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
 constexpr uint32_t idesc_of(int a_fmt, int b_fmt, int N) {
   return (1u << 4) | (uint32_t)a_fmt << 7 | (uint32_t)b_fmt << 10 | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
-__device__ __forceinline__ uint32_t f32_to_e5m2x2(float a, float b) {
-  uint32_t r;
-  asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e5m2x2.f32 t, %2, %1;\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
@@ -178,15 +173,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     fence_mbar_init();
   }
   pdl_wait();
-  kv8_group_sums<KT_TOKENS, KT_ROWS>(a, sh.grp);
-  const long long total = sh.grp[(a.n_req + 31) / 32];
-  const long long chunk = (total + gridDim.x - 1) / gridDim.x, pos = (long long)blockIdx.x * chunk;
-  if (pos >= total) {                                  // uniform for the CTA
+  long long chunk, item_begin;
+  Kv8Piece pc;
+  if (!kv8_start<KT_TOKENS, KT_ROWS>(a, sh.grp, blockIdx.x, gridDim.x, pc, chunk, item_begin)) {   // uniform for the CTA
     if (threadIdx.x == 0) a.desc[blockIdx.x].units = 0;
     return;
   }
-  long long item_begin;
-  Kv8Piece pc = kv8_first_piece<KT_TOKENS, KT_ROWS>(a, sh.grp, pos, min(chunk, total - pos), item_begin);
   if (threadIdx.x == 0) a.desc[blockIdx.x] = Kv8Desc{item_begin, chunk, pc.units, pc.b, pc.qt, pc.h};
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -640,8 +632,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
             uint32_t f[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              f[2 * k] = e4m3x2_to_f16x2(w[k]);
-              f[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+              e4m3x4_to_f16(w[k], f[2 * k], f[2 * k + 1]);
             }
             const uint32_t at = dst + x * Lay::PAGE16 + j * (KT_WIDEN / 4 * 128);
             sts128(at + 16 * c0, f);
@@ -672,7 +663,7 @@ cudaError_t launch(const KtParams &p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kt_smem<HD>());
   if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_tiles<HD>, dim3(KV8_SMS), dim3(KT_THREADS), kt_smem<HD>(), s, p);
   if (e == cudaSuccess)
-    e = launch_pdl(k_kv8_combine<bf16, HD, KT_TOKENS, KT_ROWS>, dim3(KV8_SMS - 1, 8), dim3(128), 0, s, p.a);
+    e = launch_pdl(k_kv8_combine<bf16, HD, KT_TOKENS, KT_ROWS>, dim3(KV8_SMS - 1, KT_ROWS / 4), dim3(128), 0, s, p.a, KV8_SMS);
   return e;
 }
 }  // namespace

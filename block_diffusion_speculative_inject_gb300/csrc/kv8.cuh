@@ -20,6 +20,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
   asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(b));
   return r;
 }
+// four of them as two pairs
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t b, uint32_t &lo, uint32_t &hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi) : "r"(b));
+}
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t b) {
   const uint32_t h = e4m3x2_to_f16x2(b);
   float2 v;
@@ -32,6 +37,12 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t b) {
 __device__ __forceinline__ uint32_t f32_to_e4m3x2(float a, float b) {
   uint32_t r;
   asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f32_to_e5m2x2(float a, float b) {
+  uint32_t r;
+  asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e5m2x2.f32 t, %2, %1;\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "f"(a), "f"(b));
   return r;
 }
 

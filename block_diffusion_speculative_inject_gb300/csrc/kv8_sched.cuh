@@ -100,72 +100,93 @@ struct Kv8Piece {
   long long left;              // units of the worker after this piece
 };
 
-// Sums of units per group of 32 requests as a prefix in s_grp[0 .. groups]; whole CTA, ends in a barrier.
+// x / y for 0 <= x, 0 < y: one 32-bit division where both fit
+static __device__ __noinline__ long long div_wide(long long x, long long y) { return x / y; }
+__device__ __forceinline__ long long div_ll(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : div_wide(x, y);
+}
+
+__device__ __forceinline__ long long warp_scan_ll(long long x) {       // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += t;
+  }
+  return x;
+}
+
+// The start of worker `me` of `workers`: false if it has nothing to do. The whole CTA calls it (s_grp is for more
+// than 32 requests only); chunk gets the units per worker, item_begin the first unit of the first
+// piece's item. For up to 32 requests every warp sums them up by itself, without a barrier.
 template <int U, int M>
-__device__ __forceinline__ void kv8_group_sums(const Kv8AttnArgs &a, long long *s_grp) {
+__device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp, int me, int workers, Kv8Piece &p,
+                                          long long &chunk, long long &item_begin) {
   const Kv8Tiles<U, M> tl(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (a.n_req + 31) / 32;
-  for (int g = warp; g < groups; g += warps) {
-    const int b = g * 32 + lane;
-    long long t = b < a.n_req ? tl.total(kv8_req(a, b)) : 0;
+  long long total = 0;
+  if (groups > 1) {
+    for (int g = warp; g < groups; g += warps) {
+      const int b = g * 32 + lane;
+      long long t = b < a.n_req ? tl.total(kv8_req(a, b)) : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) s_grp[g + 1] = t;
-  }
-  if (threadIdx.x == 0) s_grp[0] = 0;
-  __syncthreads();
-  if (groups > 1 && warp == 0) {
-    long long base = 0;
-    for (int g0 = 1; g0 <= groups; g0 += 32) {
-      long long x = g0 + lane <= groups ? s_grp[g0 + lane] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += t;
-      }
-      if (g0 + lane <= groups) s_grp[g0 + lane] = base + x;
-      base += __shfl_sync(0xffffffffu, x, 31);
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) s_grp[g + 1] = t;
     }
+    if (threadIdx.x == 0) s_grp[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+      long long before = 0;
+      for (int g0 = 1; g0 <= groups; g0 += 32) {
+        const long long x = warp_scan_ll(g0 + lane <= groups ? s_grp[g0 + lane] : 0);
+        if (g0 + lane <= groups) s_grp[g0 + lane] = before + x;
+        before += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    __syncthreads();
+    total = s_grp[groups];
   }
-  __syncthreads();
-}
-
-// First piece of the worker that owns units [pos, pos + count), pos < s_grp[groups] (one warp, all lanes).
-template <int U, int M>
-__device__ __forceinline__ Kv8Piece kv8_first_piece(const Kv8AttnArgs &a, const long long *s_grp, long long pos,
-                                                    long long count, long long &item_begin) {
-  const Kv8Tiles<U, M> tl(a);
-  const int lane = threadIdx.x & 31, groups = (a.n_req + 31) / 32;
-  int lo = 0, hi = groups - 1;                         // last group with s_grp <= pos
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (s_grp[m] <= pos) lo = m;
-    else hi = m - 1;
-  }
-  const int b0 = lo * 32;
   Kv8Req r{0, 0, 0};
-  long long mine = 0;
-  if (b0 + lane < a.n_req) {
-    r = kv8_req(a, b0 + lane);
-    mine = tl.total(r);
+  long long mine = 0, inc = 0, pos = 0, base = 0;
+  int b0 = 0;
+  if (groups == 1) {
+    if (lane < a.n_req) {
+      r = kv8_req(a, lane);
+      mine = tl.total(r);
+    }
+    inc = warp_scan_ll(mine);
+    total = __shfl_sync(0xffffffffu, inc, 31);
   }
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
+  chunk = div_ll(total + workers - 1, workers);
+  pos = me * chunk;
+  if (pos >= total) return false;
+  if (groups > 1) {
+    int lo = 0, hi = groups - 1;                       // last group with s_grp <= pos
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (s_grp[m] <= pos) lo = m;
+      else hi = m - 1;
+    }
+    b0 = lo * 32;
+    base = s_grp[lo];
+    if (b0 + lane < a.n_req) {
+      r = kv8_req(a, b0 + lane);
+      mine = tl.total(r);
+    }
+    inc = warp_scan_ll(mine);
   }
-  const unsigned past = __ballot_sync(0xffffffffu, s_grp[lo] + inc > pos);
-  const int who = __ffs(past) - 1;                     // the request that holds pos
-  Kv8Piece p;
+  const int who = __ffs(__ballot_sync(0xffffffffu, base + inc > pos)) - 1;     // the request that holds pos
   p.b = b0 + who;
   p.r.n = __shfl_sync(0xffffffffu, r.n, who);
   p.r.len = __shfl_sync(0xffffffffu, r.len, who);
   p.r.row0 = __shfl_sync(0xffffffffu, r.row0, who);
-  const long long start = s_grp[lo] + __shfl_sync(0xffffffffu, inc - mine, who);
-  const long long off = pos - start;
-  if (tl.causal) {
+  const long long off = pos - base - __shfl_sync(0xffffffffu, inc - mine, who);
+  const long long count = min(chunk, total - pos);
+  p.qt = 0;
+  if (!tl.causal) {
+    p.qt = (int)div_ll(off, (long long)tl.units(p.r, 0) * a.nkv);
+  } else {
     int l = 0, h = tl.tiles(p.r) - 1;
     while (l < h) {
       const int m = (l + h + 1) >> 1;
@@ -173,17 +194,15 @@ __device__ __forceinline__ Kv8Piece kv8_first_piece(const Kv8AttnArgs &a, const 
       else h = m - 1;
     }
     p.qt = l;
-  } else {
-    p.qt = (int)(off / ((long long)tl.units(p.r, 0) * a.nkv));
   }
   p.units = tl.units(p.r, p.qt);
   const long long in_tile = off - tl.before(p.r, p.qt) * a.nkv;
-  p.h = (int)(in_tile / p.units);
-  p.u0 = (int)(in_tile % p.units);
+  p.h = (int)div_ll(in_tile, p.units);
+  p.u0 = (int)(in_tile - (long long)p.h * p.units);
   p.u1 = (int)min((long long)p.units, p.u0 + count);
   p.left = count - (p.u1 - p.u0);
   item_begin = pos - p.u0;
-  return p;
+  return true;
 }
 
 // The next piece of the same worker; p.left > 0.

@@ -441,8 +441,8 @@ typedef struct {
 
 /* Writes rows of k and v [rows, n_kv_heads, head_dim] (row strides in elements, multiples of
  * 16 bytes) at slot_map [rows] int64; rows whose slot is outside [0, 64 n_pages) are skipped.
- * A page's rows must be consecutive in slot_map (as dflash_page_plan makes them; skipped rows may
- * lie between); of rows with the same slot the last one stays. Offset 0 among a page's rows starts
+ * A page's rows must follow one another in slot_map with nothing between (as dflash_page_plan makes
+ * them), in any order; of rows with the same slot the last one stays. Offset 0 among a page's rows starts
  * the page afresh: its scale is the smallest power of two s with |x| <= 448 s over its new rows. Else
  * the scale is the larger of that and the one it has, and where it grows the rows below the last
  * new one that are not written are rounded anew to it. Infinities are stored as +-448 s and have no say in
