@@ -3,8 +3,8 @@
 //
 // Few rows (a decoding step, a short block): the cache's bytes bound it, each read once. A worker is
 // a warp with its own ring of K and V pages in shared memory, filled by bulk copies that it issues
-// itself, so that warps never wait for one another; 16 query rows (tokens x heads of a kv head)
-// are the M of mma.m16n8k16. Per page of 64 tokens:
+// itself, so that warps never wait for one another. Per page of 64 tokens, with m16n8k16 products of up to
+// 16 query rows (tokens x heads of a kv head):
 //   S[16, 64] = Q . K^T      K bytes widened to f16 in registers (exact)
 //   P = 2^(S c + log2 s_v - m), S = sum in log2 units, c = scale log2(e) s_k 2^row exponent
 //   O[16, hd] += P . V       V bytes likewise, P in f16
@@ -25,7 +25,6 @@ namespace dflash {
 
 constexpr int KM_WARPS = 8;
 constexpr int KM_THREADS = 32 * KM_WARPS;
-constexpr int KM_ROWS = 16;
 constexpr float KM_BIAS = 14.f;                        // P's largest value is 2^14
 
 template <int HD>
@@ -42,14 +41,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// an 8 x 8 tile of 16-bit values over the warp (row g, columns 2 t and 2 t + 1 in lane (g, t)) transposed
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
-}
+
 // The warp's copies: pages of its units in order, K then V, each into the next slot of its ring.
 template <int HD>
 struct KmFeed {
@@ -59,12 +57,16 @@ struct KmFeed {
   bool v, done;
 };
 
-template <typename T, int HD>
+// ROWS 16: S = Q K^T and O = P V with the query rows as M. ROWS 8: S^T = K Q^T and O^T = V^T P^T, the query rows
+// as N, half the products and half the registers.
+template <typename T, int HD, int ROWS>
 __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnArgs a) {
   typedef KmLayout<HD> Lay;
-  typedef Kv8Tiles<KV_PAGE, KM_ROWS> Tiles;
+  constexpr bool SWAP = ROWS == 8;
   constexpr int KS = HD / 16;                          // k steps of S
-  constexpr int NT = HD / 8;                           // n tiles of O
+  constexpr int ST = SWAP ? 4 : 8;                     // tiles of S: 16 or 8 tokens each
+  constexpr int OT = SWAP ? HD / 16 : HD / 8;          // tiles of O: 16 or 8 dims each
+  constexpr int QF = SWAP ? 2 : 4;                     // registers of a fragment of q or P
   constexpr int PL = sizeof(T) == 4 ? 2 : 1;           // f16 planes of q and P
   extern __shared__ __align__(128) uint8_t km_smem[];
   __shared__ long long s_grp[KV8_GROUPS + 1];
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   const int me = warp * gridDim.x + blockIdx.x;        // few workers spread over all SMs
   long long chunk, item_begin;
   Kv8Piece pc;
-  if (!kv8_start<KV_PAGE, KM_ROWS>(a, s_grp, me, gridDim.x * KM_WARPS, pc, chunk, item_begin)) {
+  if (!kv8_start<KV_PAGE, ROWS>(a, s_grp, me, gridDim.x * KM_WARPS, pc, chunk, item_begin)) {
     if (lane == 0) a.desc[me].units = 0;
     return;                                            // (no barrier of the whole CTA follows)
   }
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
       f.v = !f.v;
       if (!f.v && ++f.u == f.p.u1) {
         if (f.p.left > 0) {
-          kv8_next_piece<KV_PAGE, KM_ROWS>(a, f.p);
+          kv8_next_piece<KV_PAGE, ROWS>(a, f.p);
           f.u = f.p.u0;
           f.tab_u = -32;
         } else {
@@ -146,25 +148,25 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
 #pragma unroll 1
   for (int i = 0; i < Lay::SLOTS; ++i) feed();
 
-  const int group = a.nq / a.nkv, tpt = KM_ROWS / group;
+  const int group = a.nq / a.nkv, tpt = ROWS / group;
   uint32_t take = 0;                                   // pages taken from the ring
   bool ok = true;
   auto wait = [&]() {                                  // the slot of the next page
     const uint32_t slot = take % Lay::SLOTS;
     ok = ok && kv8_wait(bar0 + 8 * slot, take / Lay::SLOTS & 1, (volatile int *)&s_abort);
     ok = __all_sync(0xffffffffu, ok);
-    return (const uint8_t *)(my_ring + slot * Lay::SLOT);
+    return my_ring + slot * Lay::SLOT;
   };
 
   for (;;) {
     // ---------------- this piece's query rows, as f16 fragments
-    // row g (and g + 8) of the tile: token row / group, head row % group
-    uint32_t qf[PL][KS][4];
+    // lanes load row g (and, of 16, g + 8) of the tile: token row / group, head row % group
+    uint32_t qf[PL][KS][QF];
     float rs[2];                                       // scale log2(e) 2^(row exponent)
     bool bad[2];
     int tok[2];
 #pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
+    for (int rr = 0; rr < (SWAP ? 1 : 2); ++rr) {
       const int row = g + 8 * rr, tk = pc.qt * tpt + row / group;
       const bool live = row < tpt * group && tk < pc.r.n;
       tok[rr] = live ? tk : -1;
@@ -189,7 +191,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
         big = fmaxf(big, fabsf(x[i]));
         fin = fin && fabsf(x[i]) <= 3.402823466e38f;
       }
-      big = quad_max(big);
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       const unsigned fb = __ballot_sync(0xffffffffu, fin);
       bad[rr] = (fb >> (lane & ~3) & 15) != 15;
       // q * 2^(14 - e): the largest is in [2^14, 2^15)
@@ -202,16 +205,28 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
         for (int z = 0; z < 2; ++z) {                  // dims 4 k + 2 z, + 1 of the lane's
           const float y0 = bad[rr] ? 0.f : x[4 * k + 2 * z] * up, y1 = bad[rr] ? 0.f : x[4 * k + 2 * z + 1] * up;
           const uint32_t h = pack_f16(y0, y1);
-          qf[0][k][2 * z + rr] = h;
+          qf[0][k][SWAP ? z : 2 * z + rr] = h;
           if constexpr (PL == 2) {
             const float2 f = unpack_f16(h);
-            qf[PL - 1][k][2 * z + rr] = pack_f16(y0 - f.x, y1 - f.y);
+            qf[PL - 1][k][SWAP ? z : 2 * z + rr] = pack_f16(y0 - f.x, y1 - f.y);
           }
         }
     }
-    float o[NT][4];
+    if constexpr (SWAP) {
+      // from here on a lane keeps rows 2 t and 2 t + 1 (of 16: g and g + 8)
+      const float rs0 = rs[0];
+      const int state = (tok[0] << 1) | (int)bad[0];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int rr = 0; rr < 2; ++rr) {
+        rs[rr] = __shfl_sync(0xffffffffu, rs0, (2 * t + rr) * 4);
+        const int st = __shfl_sync(0xffffffffu, state, (2 * t + rr) * 4);
+        tok[rr] = st >> 1;
+        bad[rr] = st & 1;
+      }
+    }
+    float o[OT][4];
+#pragma unroll
+    for (int i = 0; i < OT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     // tokens from `open` on are hidden from some row of the request
     const int open = a.mask == DFLASH_MASK_NONE ? pc.r.len : max(0, pc.r.len - pc.r.n);
@@ -224,18 +239,19 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
       const Side sd = side[take / 2 % Lay::SIDE];
       if (!ok) break;
       ++take;
-      float s[8][4];
-      // two n tiles at a time, whose chains of sums interleave
+      float s[ST][4];
+      // two tiles at a time, whose chains of sums interleave
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        uint32_t w[2][HD / 16];
+      for (int j = 0; j < ST; j += 2) {
+        uint32_t w[2][SWAP ? 2 : 1][HD / 16];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const uint8_t *row = kslot + (16 * (g >> 1) + 2 * (j + z) + (g & 1)) * HD + t * (HD / 4);
 #pragma unroll
-          for (int c = 0; c < HD / 64; ++c) {
-            const uint4 v = *(const uint4 *)(row + 16 * c);
-            w[z][4 * c] = v.x, w[z][4 * c + 1] = v.y, w[z][4 * c + 2] = v.z, w[z][4 * c + 3] = v.w;
+          for (int y = 0; y < (SWAP ? 2 : 1); ++y) {
+            const int token = 16 * (g >> 1) + (g & 1) + (SWAP ? 4 : 2) * (j + z) + 2 * y;
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+              *(uint4 *)&w[z][y][4 * c] = *(const uint4 *)(kslot + token * HD + t * (HD / 4) + 16 * c);
           }
           s[j + z][0] = s[j + z][1] = s[j + z][2] = s[j + z][3] = 0.f;
         }
@@ -243,15 +259,31 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16(w[z][k], b0, b1);
+            uint32_t f[4];
+            if constexpr (SWAP) {
+              e4m3x4_to_f16(w[z][0][k], f[0], f[2]);
+              e4m3x4_to_f16(w[z][SWAP ? 1 : 0][k], f[1], f[3]);
 #pragma unroll
-            for (int pl = 0; pl < PL; ++pl) mma_f16(s[j + z], qf[pl][k], b0, b1);
+              for (int pl = 0; pl < PL; ++pl) mma_f16(s[j + z], f, qf[pl][k][0], qf[pl][k][1]);
+            } else {
+              e4m3x4_to_f16(w[z][0][k], f[0], f[1]);
+#pragma unroll
+              for (int pl = 0; pl < PL; ++pl) mma_f16(s[j + z], *(const uint32_t(*)[4])qf[pl][k], f[0], f[1]);
+            }
           }
       }
       __syncwarp();                                    // every lane has read the K page
       feed();
-      // a lane's tokens: 16 t + 2 j + {0, 1} for n tile j
+      // value i < 2 ST of row rr (of 16: tokens 16 t + i; of 8: 16 (g >> 1) + (g & 1) + 2 i)
+      auto val = [&](int rr, int i) -> float & { return SWAP ? s[i >> 1][rr + 2 * (i & 1)] : s[i >> 1][2 * rr + (i & 1)]; };
+      auto across = [&](float v, bool sum) {           // over the lanes that share the row
+#pragma unroll
+        for (int z = 0; z < (SWAP ? 3 : 2); ++z) {
+          const float w = __shfl_xor_sync(0xffffffffu, v, (SWAP ? 4 : 1) << z);
+          v = sum ? v + w : fmaxf(v, w);
+        }
+        return v;
+      };
       const bool out = sd.page < 0;                    // not in the pool: nothing of it is seen
       const bool partial = out || (long long)(u + 1) * KV_PAGE > open;
       const float ev = out ? 0.f : log2f(sd.vs), iv = out ? 1.f : 1.f / sd.vs;
@@ -260,27 +292,23 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
       for (int rr = 0; rr < 2; ++rr) {
         const float c = out ? 0.f : rs[rr] * sd.ks;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) s[j][2 * rr + e] = fmaf(s[j][2 * rr + e], c, ev);
+        for (int i = 0; i < 2 * ST; ++i) val(rr, i) = fmaf(val(rr, i), c, ev);
       }
       if (partial) {
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          const uint32_t hidden = out || tok[rr] < 0 ? ~0u : ~(uint32_t)(kv8_visible(a, pc.r, tok[rr], u) >> (16 * t));
+          const uint64_t see = out || tok[rr] < 0 ? 0 : kv8_visible(a, pc.r, tok[rr], u);
+          const uint32_t hidden = ~(uint32_t)(see >> (SWAP ? 16 * (g >> 1) + (g & 1) : 16 * t));
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (hidden >> (2 * j + e) & 1) s[j][2 * rr + e] = -INFINITY;
-            }
+          for (int i = 0; i < 2 * ST; ++i)
+            if (hidden >> (SWAP ? 2 * i : i) & 1) val(rr, i) = -INFINITY;
         }
       }
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx[rr] = fmaxf(mx[rr], fmaxf(s[j][2 * rr], s[j][2 * rr + 1]));
-        mx[rr] = fmaxf(quad_max(mx[rr]), m[rr]);
+        for (int i = 0; i < 2 * ST; i += 2) mx[rr] = fmaxf(mx[rr], fmaxf(val(rr, i), val(rr, i + 1)));
+        mx[rr] = fmaxf(across(mx[rr], false), m[rr]);
       }
       float alpha[2], ref[2];
 #pragma unroll
@@ -289,87 +317,109 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
         ref[rr] = top - KM_BIAS;
         alpha[rr] = ex2(m[rr] - top);
         m[rr] = mx[rr];
-        float sum = 0.f;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float &x = s[j][2 * rr + e];
-            x = ex2(x - ref[rr]);
-            sum += x;
-          }
-        l[rr] = fmaf(l[rr], alpha[rr], sum * iv);
+        for (int i = 0; i < 2 * ST; ++i) {
+          float &x = val(rr, i);
+          x = ex2(x - ref[rr]);
+          sum[i & 1] += x;
+        }
+        l[rr] = fmaf(l[rr], alpha[rr], (sum[0] + sum[1]) * iv);
       }
       if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[i][0] *= alpha[0], o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1], o[i][3] *= alpha[1];
+        for (int i = 0; i < OT; ++i) {
+          o[i][0] *= alpha[0], o[i][1] *= alpha[SWAP ? 1 : 0];
+          o[i][2] *= alpha[SWAP ? 0 : 1], o[i][3] *= alpha[1];
         }
       }
-      uint32_t pf[PL][4][4];                           // P fragments of 16 tokens each
+      uint32_t pf[PL][4][QF];                          // P fragments of 16 tokens each
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 2 * k + (i >> 1), rr = i & 1;
-          const float x0 = s[j][2 * rr], x1 = s[j][2 * rr + 1];
-          pf[0][k][i] = pack_f16(x0, x1);
+        for (int i = 0; i < QF; ++i) {
+          // of 16 rows: fragments of S as they are; of 8: S^T's tokens (g) x rows (2 t) turned over
+          const float x0 = SWAP ? s[k][2 * i] : s[SWAP ? 0 : 2 * k + (i >> 1)][2 * (i & 1)];
+          const float x1 = SWAP ? s[k][2 * i + 1] : s[SWAP ? 0 : 2 * k + (i >> 1)][2 * (i & 1) + 1];
+          const uint32_t h = pack_f16(x0, x1);
+          pf[0][k][i] = SWAP ? turn8x8(h) : h;
           if constexpr (PL == 2) {
-            const float2 h = unpack_f16(pf[0][k][i]);
-            pf[PL - 1][k][i] = pack_f16(x0 - h.x, x1 - h.y);
+            const float2 f = unpack_f16(h);
+            const uint32_t lo = pack_f16(x0 - f.x, x1 - f.y);
+            pf[PL - 1][k][i] = SWAP ? turn8x8(lo) : lo;
           }
         }
-      const uint8_t *vslot = wait();
+      uint8_t *vslot = wait();
       if (!ok) break;
       ++take;
       bool nan = false;
-      // bytes of tokens that no row sees (a page's tail) may be anything
-      const int tail = out ? 0 : min(16, max(0, pc.r.len - u * KV_PAGE - 16 * t));
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint4 v = *(const uint4 *)(vslot + (8 * i + g) * KV_PAGE + 16 * t);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if (partial) {
+      if (partial) {
+        // Bytes of tokens that no row sees (a page's tail) may be anything, and a NaN must not meet the zero
+        // weight of a row that does not see it: each lane puts its own bytes in order where they lie.
+        const int tail = out ? 0 : min(16, max(0, pc.r.len - u * KV_PAGE - 16 * t));
+#pragma unroll 1
+        for (int i = 0; i < HD / 8; ++i) {
+          uint4 *at = (uint4 *)(vslot + (8 * i + g) * KV_PAGE + 16 * t);
+          uint4 v = *at;
+          uint32_t *w = (uint32_t *)&v;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int n = tail - 4 * k;
             w[k] = n >= 4 ? w[k] : n <= 0 ? 0u : w[k] & ((1u << 8 * n) - 1);
-            const uint32_t nb = nan_bytes(w[k]);       // a NaN must not meet the zero weight of a row that does not see it
+            const uint32_t nb = nan_bytes(w[k]);
             nan |= nb != 0;
             w[k] &= ~byte_mask(nb);
           }
+          *at = v;
         }
+        fence_proxy_async_smem();                      // before the next copy into the slot
+      }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t b0, b1;
-          e4m3x4_to_f16(w[k], b0, b1);
+      for (int i = 0; i < OT; i += 2) {                // two tiles at a time again
+        uint32_t w[2][SWAP ? 2 : 1][4];
 #pragma unroll
-          for (int pl = 0; pl < PL; ++pl) mma_f16(o[i], pf[pl][k], b0, b1);
-        }
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int y = 0; y < (SWAP ? 2 : 1); ++y)
+            *(uint4 *)w[z][y] = *(const uint4 *)(vslot + ((SWAP ? 16 : 8) * (i + z) + 8 * y + g) * KV_PAGE + 16 * t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            uint32_t f[4];
+            if constexpr (SWAP) {
+              e4m3x4_to_f16(w[z][0][k], f[0], f[2]);
+              e4m3x4_to_f16(w[z][SWAP ? 1 : 0][k], f[1], f[3]);
+#pragma unroll
+              for (int pl = 0; pl < PL; ++pl) mma_f16(o[i + z], f, pf[pl][k][0], pf[pl][k][1]);
+            } else {
+              e4m3x4_to_f16(w[z][0][k], f[0], f[1]);
+#pragma unroll
+              for (int pl = 0; pl < PL; ++pl) mma_f16(o[i + z], *(const uint32_t(*)[4])pf[pl][k], f[0], f[1]);
+            }
+          }
       }
       if (partial && __any_sync(0xffffffffu, nan)) {   // rows that see a NaN value get it (rare)
         const uint64_t vis0 = tok[0] < 0 ? 0 : kv8_visible(a, pc.r, tok[0], u);
         const uint64_t vis1 = tok[1] < 0 ? 0 : kv8_visible(a, pc.r, tok[1], u);
-        uint32_t hit0 = 0, hit1 = 0;                   // bit 2 i + e: dim 8 i + 2 t + e holds one
+        const uint8_t *page = a.vp + kv8_block(sd.page, pc.h, a.nkv, HD);
+        uint32_t hit0 = 0, hit1 = 0;                   // bit 2 i + e: the lane's dim e of tile i holds one
 #pragma unroll 1
-        for (int d = 0; d < 2 * NT; ++d) {
+        for (int d = 0; d < 2 * OT; ++d) {
+          const int dim = SWAP ? 16 * (d >> 1) + 8 * (d & 1) + g : 8 * (d >> 1) + 2 * t + (d & 1);
           uint64_t at = 0;                             // tokens whose value is NaN in that dim
 #pragma unroll 1
-          for (int k = 0; k < KV_PAGE; ++k) {
-            const uint32_t byte = vslot[(8 * (d >> 1) + 2 * t + (d & 1)) * KV_PAGE + k];
-            at |= (uint64_t)((byte & 0x7f) == 0x7f) << k;
-          }
+          for (int k = 0; k < KV_PAGE; ++k) at |= (uint64_t)((page[dim * KV_PAGE + k] & 0x7f) == 0x7f) << k;
           hit0 |= (uint32_t)((at & vis0) != 0) << d;
           hit1 |= (uint32_t)((at & vis1) != 0) << d;
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < OT; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             // adding 0 or NaN, so that no lane branches
-            o[i][e] += __uint_as_float((uint32_t)((int)(hit0 << (31 - 2 * i - e)) >> 31) & 0x7fc00000u);
-            o[i][2 + e] += __uint_as_float((uint32_t)((int)(hit1 << (31 - 2 * i - e)) >> 31) & 0x7fc00000u);
+            o[i][SWAP ? 2 * e : e] += __uint_as_float((uint32_t)((int)(hit0 << (31 - 2 * i - e)) >> 31) & 0x7fc00000u);
+            o[i][SWAP ? 2 * e + 1 : 2 + e] += __uint_as_float((uint32_t)((int)(hit1 << (31 - 2 * i - e)) >> 31) & 0x7fc00000u);
           }
       }
       __syncwarp();                                    // every lane has read the V page
@@ -378,34 +428,48 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
     if (!ok) break;
 
     // ---------------- the piece's result
-    l[0] = quad_sum(l[0]);
-    l[1] = quad_sum(l[1]);
     const bool whole = pc.u1 - pc.u0 == pc.units;
     const int slot = 2 * me + (first ? 0 : 1);
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
+#pragma unroll
+      for (int z = 0; z < (SWAP ? 3 : 2); ++z) l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], (SWAP ? 4 : 1) << z);
       if (tok[rr] < 0) continue;
-      const int row = g + 8 * rr;
+      const int row = SWAP ? 2 * t + rr : g + 8 * rr;
       if (bad[rr]) l[rr] = NAN;
+      const bool one = SWAP ? g == 0 : t == 0;         // one lane of the row
       if (whole) {
         const size_t at = (size_t)(pc.r.row0 + tok[rr]) * a.nq + pc.h * group + row % group;
         const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
-        T *out = (T *)a.out + at * HD + 2 * t;
+        T *out = (T *)a.out + at * HD;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          if constexpr (PL == 1) *(__nv_bfloat162 *)(out + 8 * i) = __floats2bfloat162_rn(o[i][2 * rr] * inv, o[i][2 * rr + 1] * inv);
-          else *(float2 *)(out + 8 * i) = make_float2(o[i][2 * rr] * inv, o[i][2 * rr + 1] * inv);
+        for (int i = 0; i < OT; ++i) {
+          if constexpr (SWAP) {
+            out[16 * i + g] = from_f<T>(o[i][rr] * inv);
+            out[16 * i + 8 + g] = from_f<T>(o[i][2 + rr] * inv);
+          } else if constexpr (PL == 1) {
+            *(__nv_bfloat162 *)(out + 8 * i + 2 * t) = __floats2bfloat162_rn(o[i][2 * rr] * inv, o[i][2 * rr + 1] * inv);
+          } else {
+            *(float2 *)(out + 8 * i + 2 * t) = make_float2(o[i][2 * rr] * inv, o[i][2 * rr + 1] * inv);
+          }
         }
-        if (a.lse && t == 0) a.lse[at] = l[rr] == 0.f ? -INFINITY : (m[rr] - KM_BIAS + log2f(l[rr])) * LN2;
+        if (a.lse && one) a.lse[at] = l[rr] == 0.f ? -INFINITY : (m[rr] - KM_BIAS + log2f(l[rr])) * LN2;
       } else {
-        float *po = a.part_o + ((size_t)slot * KM_ROWS + row) * HD + 2 * t;
+        float *po = a.part_o + ((size_t)slot * ROWS + row) * HD;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) *(float2 *)(po + 8 * i) = make_float2(o[i][2 * rr], o[i][2 * rr + 1]);
-        if (t == 0) *(float2 *)(a.part_ml + ((size_t)slot * KM_ROWS + row) * 2) = make_float2(m[rr] - KM_BIAS, l[rr]);
+        for (int i = 0; i < OT; ++i) {
+          if constexpr (SWAP) {
+            po[16 * i + g] = o[i][rr];
+            po[16 * i + 8 + g] = o[i][2 + rr];
+          } else {
+            *(float2 *)(po + 8 * i + 2 * t) = make_float2(o[i][2 * rr], o[i][2 * rr + 1]);
+          }
+        }
+        if (one) *(float2 *)(a.part_ml + ((size_t)slot * ROWS + row) * 2) = make_float2(m[rr] - KM_BIAS, l[rr]);
       }
     }
     if (pc.left <= 0) break;
-    kv8_next_piece<KV_PAGE, KM_ROWS>(a, pc);
+    kv8_next_piece<KV_PAGE, ROWS>(a, pc);
     first = false;
   }
   if (!ok) {
@@ -421,11 +485,11 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
           for (int d = lane; d < HD; d += 32) ((T *)a.out)[at * HD + d] = from_f<T>(NAN);
           if (a.lse && lane == 0) a.lse[at] = NAN;
         } else if (lane == 0) {
-          *(float2 *)(a.part_ml + ((size_t)slot * KM_ROWS + row) * 2) = make_float2(0.f, NAN);
+          *(float2 *)(a.part_ml + ((size_t)slot * ROWS + row) * 2) = make_float2(0.f, NAN);
         }
       }
       if (pc.left <= 0) break;
-      kv8_next_piece<KV_PAGE, KM_ROWS>(a, pc);
+      kv8_next_piece<KV_PAGE, ROWS>(a, pc);
       first = false;
     }
     const unsigned long long t0 = global_ns();
@@ -435,14 +499,18 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   }
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int ROWS>
 cudaError_t launch_rows(const Kv8AttnArgs &a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_rows<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_rows<T, HD, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)KmLayout<HD>::SMEM);
-  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD>, dim3(KV8_SMS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
+  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD, ROWS>, dim3(KV8_SMS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
   if (e == cudaSuccess)
-    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, KM_ROWS>, dim3(KV8_SMS * 2, 4), dim3(128), 0, s, a, KV8_SMS * KM_WARPS);
+    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, ROWS>, dim3(KV8_SMS * 2, ROWS / 4), dim3(128), 0, s, a, KV8_SMS * KM_WARPS);
   return e;
+}
+template <typename T, int ROWS>
+cudaError_t launch_rows(const Kv8AttnArgs &a, int hd, cudaStream_t s) {
+  return hd == 128 ? launch_rows<T, 128, ROWS>(a, s) : launch_rows<T, 64, ROWS>(a, s);
 }
 
 }  // namespace dflash
@@ -470,7 +538,7 @@ struct Space {
   int64_t desc, ml, o, bytes;
 };
 Space space_of(int hd) {
-  const int64_t workers = KV8_SMS * KM_WARPS, m = KM_ROWS;
+  const int64_t workers = KV8_SMS * KM_WARPS, m = 16;   // the tiles' 152 workers of 128 rows need as much
   Space s;
   s.desc = 0;
   s.ml = (workers * (int64_t)sizeof(Kv8Desc) + 255) / 256 * 256;
@@ -496,9 +564,14 @@ extern "C" dflash_status dflash_kv8_attention(void *stream, const dflash_kv8_cac
                       (const uint8_t *)c->k_pages, (const uint8_t *)c->v_pages, c->k_scale, c->v_scale,
                       (Kv8Desc *)(ws + sp.desc), (float *)(ws + sp.o), (float *)(ws + sp.ml)};
   const cudaStream_t s = (cudaStream_t)stream;
-  const bool tiles = x->dtype == DFLASH_BF16 && (int64_t)x->max_q * (x->n_q_heads / c->n_kv_heads) > KM_ROWS;
-  const cudaError_t e = tiles ? launch_kv8_tiles(a, c->head_dim, s)
-                      : x->dtype == DFLASH_BF16 ? (c->head_dim == 128 ? launch_rows<bf16, 128>(a, s) : launch_rows<bf16, 64>(a, s))
-                                                : (c->head_dim == 128 ? launch_rows<float, 128>(a, s) : launch_rows<float, 64>(a, s));
+  // Rows of a request and kv head, as far as the host knows: up to 8 go to the kernel for 8, up to 16 to the one
+  // for 16, which reads the cache once where two tiles of 8 would read it twice. Above, bf16 goes to the tensor
+  // memory tiles; fp32 stays with 16 rows at a time.
+  const int64_t most = (int64_t)x->max_q * (x->n_q_heads / c->n_kv_heads);
+  const bool wide = x->dtype == DFLASH_BF16;
+  const int hd = c->head_dim;
+  const cudaError_t e = most <= 8 ? (wide ? launch_rows<bf16, 8>(a, hd, s) : launch_rows<float, 8>(a, hd, s))
+                        : !wide ? launch_rows<float, 16>(a, hd, s)
+                        : most <= 16 ? launch_rows<bf16, 16>(a, hd, s) : launch_kv8_tiles(a, hd, s);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
