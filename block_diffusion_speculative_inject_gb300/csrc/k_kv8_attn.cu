@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   long long chunk, item_begin;
   Kv8Piece pc;
   if (!kv8_start<KV_PAGE, ROWS>(a, s_grp, me, gridDim.x * KM_WARPS, pc, chunk, item_begin)) {
-    if (lane == 0) a.desc[me].units = 0;
+    if (lane == 0) a.desc[me].pieces = 0;
     return;                                            // (no barrier of the whole CTA follows)
   }
-  if (lane == 0) a.desc[me] = Kv8Desc{item_begin, chunk, pc.units, pc.b, pc.qt, pc.h};
+  if (lane == 0) a.desc[me] = kv8_desc<KV_PAGE, ROWS>(a, pc, me, chunk, item_begin);
   bool first = true;
 
   KmFeed<HD> f;
@@ -505,7 +505,7 @@ cudaError_t launch_rows(const Kv8AttnArgs &a, cudaStream_t s) {
                                        (int)KmLayout<HD>::SMEM);
   if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_rows<T, HD, ROWS>, dim3(KV8_SMS), dim3(KM_THREADS), KmLayout<HD>::SMEM, s, a);
   if (e == cudaSuccess)
-    e = launch_pdl(k_kv8_combine<T, HD, KV_PAGE, ROWS>, dim3(KV8_SMS * 2, ROWS / 4), dim3(128), 0, s, a, KV8_SMS * KM_WARPS);
+    e = launch_pdl(k_kv8_combine<T, HD, ROWS>, dim3(KV8_SMS * KM_WARPS - 1, 2), dim3(128), 0, s, a);
   return e;
 }
 template <typename T, int ROWS>

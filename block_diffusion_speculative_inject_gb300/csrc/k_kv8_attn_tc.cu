@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
   long long chunk, item_begin;
   Kv8Piece pc;
   if (!kv8_start<KT_TOKENS, KT_ROWS>(a, sh.grp, blockIdx.x, gridDim.x, pc, chunk, item_begin)) {   // uniform for the CTA
-    if (threadIdx.x == 0) a.desc[blockIdx.x].units = 0;
+    if (threadIdx.x == 0) a.desc[blockIdx.x].pieces = 0;
     return;
   }
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = Kv8Desc{item_begin, chunk, pc.units, pc.b, pc.qt, pc.h};
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = kv8_desc<KT_TOKENS, KT_ROWS>(a, pc, blockIdx.x, chunk, item_begin);
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
@@ -663,7 +663,7 @@ cudaError_t launch(const KtParams &p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kt_smem<HD>());
   if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_tiles<HD>, dim3(KV8_SMS), dim3(KT_THREADS), kt_smem<HD>(), s, p);
   if (e == cudaSuccess)
-    e = launch_pdl(k_kv8_combine<bf16, HD, KT_TOKENS, KT_ROWS>, dim3(KV8_SMS - 1, KT_ROWS / 4), dim3(128), 0, s, p.a, KV8_SMS);
+    e = launch_pdl(k_kv8_combine<bf16, HD, KT_ROWS>, dim3(KV8_SMS - 1, 16), dim3(128), 0, s, p.a);
   return e;
 }
 }  // namespace

@@ -39,72 +39,64 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7
 __device__ __forceinline__ uint32_t byte_mask(uint32_t high_bits) { return (high_bits >> 7) * 0xffu; }
 
 // ---------------------------------------------------------------- merge of split items
-// Looks at the descriptors of workers w = 1, 2, ..: if w's first piece continues an item that worker w - 1
-// began, merges that item: the partial (m, l, O) of worker w - 1's last piece and of the first pieces of w,
-// w + 1, .. up to the item's end. Four rows at a time: 128 threads fetch the maxima and sums of 32
-// pieces at once and turn them into weights; then a thread owns one row and four dims, and its
-// loads of the pieces' O do not wait for one another.
-template <typename T, int HD, int U, int M>
-__global__ void __launch_bounds__(128) k_kv8_combine(const Kv8AttnArgs a, int workers) {
-  __shared__ float s_wt[4][32];
+// CTA (w - 1, y) looks at the descriptor of worker w: if w's first piece continues an item that worker w - 1
+// began, it merges rows of that item, a warp each: the partial (m, l, O) of worker w - 1's
+// last piece and of the first pieces of w, w + 1, .. up to the item's end. It is all latency, so nothing but the
+// descriptor is waited for before the loads: lanes fetch the maxima and sums of 32 pieces at once
+// while the first eight pieces' O (a lane owns four dims) are on their way.
+template <typename T, int HD, int M>
+__global__ void __launch_bounds__(128) k_kv8_combine(const Kv8AttnArgs a) {
   pdl_trigger();
   pdl_wait();
-  const Kv8Tiles<U, M> tl(a);
-  const int group = a.nq / a.nkv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int w = blockIdx.x + 1; w < workers; w += gridDim.x) {
-    const Kv8Desc d = a.desc[w];
-    if (d.units == 0) return;                          // nor do the workers after it have any
-    const long long pos = (long long)w * d.chunk;
-    if (d.begin == pos || d.begin < pos - d.chunk) continue;   // starts here, or begun before worker w - 1
-    const Kv8Req r = kv8_req(a, d.b);
-    const int n = (int)div_ll(d.begin + d.units - 1, d.chunk) - w + 2;   // pieces: workers w - 1 .. the last unit's
-    const int slot0 = 2 * (w - 1) + (d.begin == pos - d.chunk ? 0 : 1);
-    const int rows = min(tl.tpt, r.n - d.qt * tl.tpt) * group;
-    auto slot_of = [&](int x) { return (size_t)(x == 0 ? slot0 : 2 * (w - 1 + x)) * M; };
-    for (int row0 = 4 * blockIdx.y; row0 < rows; row0 += 4 * gridDim.y) {
-      const int row = row0 + warp;                     // a warp's row: HD / 4 <= 32 threads hold four dims each
-      const int c = 4 * lane;
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < rows) {
-        for (int x0 = 0; x0 < n; x0 += 32) {
-          float2 ml = make_float2(-INFINITY, 0.f);
-          if (x0 + lane < n) ml = *(const float2 *)(a.part_ml + (slot_of(x0 + lane) + row) * 2);
-          const float top = fmaxf(m, warp_max(ml.x)), ref = top == -INFINITY ? 0.f : top;
-          const float wt = exp2f(ml.x - ref), back = exp2f(m - ref);
-          m = top;
-          l = l * back + warp_sum(ml.y * wt);
-          __syncwarp();
-          s_wt[warp][lane] = wt;
-          __syncwarp();
-          o.x *= back, o.y *= back, o.z *= back, o.w *= back;
-          if (c < HD) {
-            const int k = min(32, n - x0);
-#pragma unroll 8
-            for (int x = 0; x < k; ++x) {
-              const float4 v = *(const float4 *)(a.part_o + (slot_of(x0 + x) + row) * HD + c);
-              const float e = s_wt[warp][x];
-              o.x = fmaf(v.x, e, o.x);
-              o.y = fmaf(v.y, e, o.y);
-              o.z = fmaf(v.z, e, o.z);
-              o.w = fmaf(v.w, e, o.w);
-            }
-          }
+  const int w = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = 4 * lane;
+  const int4 d0 = *(const int4 *)&a.desc[w];
+  const int h = a.desc[w].h, n = d0.x, slot0 = d0.y, row0 = d0.z, rows = d0.w;
+  if (n == 0) return;
+  for (int row = 4 * blockIdx.y + warp; row < rows; row += 4 * gridDim.y) {
+    auto slot_of = [&](int x) { return (size_t)(x == 0 ? slot0 : 2 * (w - 1 + x)) * M + row; };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < n; x0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (x0 + lane < n) ml = *(const float2 *)(a.part_ml + slot_of(x0 + lane) * 2);
+      const int k = min(32, n - x0);
+      float4 v[8];
+#pragma unroll
+      for (int z = 0; z < 8; ++z) v[z] = z < k && c < HD ? *(const float4 *)(a.part_o + slot_of(x0 + z) * HD + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float top = fmaxf(m, warp_max(ml.x)), ref = top == -INFINITY ? 0.f : top;
+      const float wt = exp2f(ml.x - ref), back = exp2f(m - ref);
+      m = top;
+      l = l * back + warp_sum(ml.y * wt);
+      o.x *= back, o.y *= back, o.z *= back, o.w *= back;
+      for (int x = 0; x < k; x += 8) {
+        if (x) {
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            v[z] = x + z < k && c < HD ? *(const float4 *)(a.part_o + slot_of(x0 + x + z) * HD + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t at = (size_t)(r.row0 + d.qt * tl.tpt + row / group) * a.nq + d.h * group + row % group;
-        T *out = (T *)a.out + at * HD + c;
-        if (c < HD) {
-          if constexpr (sizeof(T) == 2) {
-            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
-            *(uint2 *)out = *(const uint2 *)h;
-          } else {
-            *(float4 *)out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-          }
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float e = __shfl_sync(0xffffffffu, wt, x + z);
+          o.x = fmaf(v[z].x, e, o.x);
+          o.y = fmaf(v[z].y, e, o.y);
+          o.z = fmaf(v[z].z, e, o.z);
+          o.w = fmaf(v[z].w, e, o.w);
         }
-        if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * LN2;
       }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int group = a.nq / a.nkv;
+    const size_t at = (size_t)(row0 + row / group) * a.nq + h * group + row % group;
+    T *out = (T *)a.out + at * HD + c;
+    if (c < HD) {
+      if constexpr (sizeof(T) == 2) {
+        __nv_bfloat162 b[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+        *(uint2 *)out = *(const uint2 *)b;
+      } else {
+        *(float4 *)out = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      }
+    }
+    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * LN2;
   }
 }
 

@@ -30,11 +30,11 @@ struct Kv8AttnArgs {
   float *part_o, *part_ml;     // [2 workers][M][hd], [2 workers][M][2] (max in log2 units, sum)
 };
 
-// What the merge needs to know of a worker's first piece.
-struct Kv8Desc {
-  long long begin, chunk;      // first unit of the item, units per worker
-  int units;                   // of the item; 0: the worker has nothing to do
-  int b, qt, h;
+// What the merge needs to know of a worker's first piece: 0 pieces unless it continues an item that the worker
+// before it began.
+struct alignas(16) Kv8Desc {
+  int pieces, slot0;           // partial results to merge: slot0, then the first ones of this and the next workers
+  int row0, rows, h, pad[3];   // first query row (token) of the tile, its rows (tokens x heads), kv head
 };
 
 // sum over i < n of floor((a i + b) / m), for a, b >= 0
@@ -203,6 +203,22 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
   p.left = count - (p.u1 - p.u0);
   item_begin = pos - p.u0;
   return true;
+}
+
+// The descriptor of worker `me`, whose first piece is p.
+template <int U, int M>
+__device__ __forceinline__ Kv8Desc kv8_desc(const Kv8AttnArgs &a, const Kv8Piece &p, int me, long long chunk, long long item_begin) {
+  Kv8Desc d{0, 0, 0, 0, 0, {0, 0, 0}};
+  const long long pos = me * chunk;
+  if (item_begin < pos && item_begin >= pos - chunk) {
+    const Kv8Tiles<U, M> tl(a);
+    d.pieces = (int)div_ll(item_begin + p.units - 1, chunk) - me + 2;       // up to the worker of the last unit
+    d.slot0 = 2 * (me - 1) + (item_begin == pos - chunk ? 0 : 1);
+    d.row0 = p.r.row0 + p.qt * tl.tpt;
+    d.rows = min(tl.tpt, p.r.n - p.qt * tl.tpt) * (a.nq / a.nkv);
+    d.h = p.h;
+  }
+  return d;
 }
 
 // The next piece of the same worker; p.left > 0.
