@@ -26,16 +26,28 @@
 // descriptors to the uniform datapath (a lone lane took over twice as long to issue a tile as the
 // tensor cores take to do it). Warps 2-9 run the softmax, two threads per row, one page each: warps w
 // and w + 4 share the rows of lane quarter w % 4 and trade their maxima. They also load Q (of the next
-// piece, ahead) and write results, half of the dims each. Warps 10-11 widen V. All walk the
-// same pieces on their own. All waits are bounded; rows whose wait ran out become NaN.
+// piece, ahead) and write results, half of the dims each, by way of shared memory so that four lanes
+// handle a row. Warps 10-11 widen V. The copying warp, which is ahead of all, finds the pieces and leaves them in
+// a ring. All waits are bounded; rows whose wait ran out become NaN.
+//
+// Code that runs once a piece is mostly fetched rather than run, so what is not a tile's inner work is
+// rolled up or shared: V widened a page at a time and one copy of the Q code took 8 trees of 256 from
+// 168 to 148 us. Measured, with the merge: 8 x 16 rows x 40 heads over 32768 tokens 135 us (537 MB, 4.0 TB/s),
+// the trees 146 us. A tile's softmax is the longest stage: 1600 cycles with two warps per SM partition,
+// where its arithmetic alone takes 840 and the MMAs 1030.
 #include "kv8_attn.cuh"
 
 namespace dflash {
+
+constexpr int KT_TOKENS = 128;                         // tokens of a tile: two pages
 
 constexpr int KT_THREADS = 384;
 constexpr int KT_WIDEN = 64;                             // threads that widen V
 constexpr int KT_STAGES = 4;
 constexpr int KT_SIDE = 2 * KT_STAGES;                 // tiles whose page ids and scales are kept
+constexpr int KT_COST = 8;                             // what an item's start and end cost, in tiles (8 trees of
+                                                       // 256 over 1000 .. 5000 tokens: 163 us with 3, 147 with 6, 146 with 8)
+constexpr int KT_RING = 16;                            // pieces kept: the one found last is at most 7 ahead of the one written
 constexpr float KT_BIAS = 7.f;
 constexpr uint32_t TM_O = 256, TM_Q = 384;
 
@@ -49,7 +61,7 @@ struct KtLayout {
   static constexpr uint32_t PAGE8 = KV_PAGE * HD;      // a K or V page, 8 bits
   static constexpr uint32_t PAGE16 = KV_PAGE * HD * 2; // a V page in f16
   static constexpr uint32_t K0 = 0, V0 = K0 + KT_STAGES * 2 * PAGE8, W0 = V0 + KT_STAGES * 2 * PAGE8;
-  static constexpr uint32_t END = W0 + 2 * 2 * PAGE16;
+  static constexpr uint32_t OUT0 = W0 + 2 * 2 * PAGE16, END = OUT0 + 8 * 2048;   // per softmax warp 32 rows x 64 bytes of results
 };
 
 struct KtSide {
@@ -65,6 +77,9 @@ struct KtShared {
   KtSide side[KT_SIDE];
   float xmax[2][2][128], lsum[2][2][128];              // per tile (piece) parity, half and row
   int xgrow[2][2][4];                                  // a row of the warp outgrew its reference
+  uint64_t known[KT_RING];
+  Kv8Piece ring[KT_RING];                              // pieces by ordinal, found by the copying warp for all
+  Kv8Piece piece[8];                                   // of each softmax warp (it has no registers to spare)
   int nan_piece[4];                                    // per piece ordinal mod 4 (two are ahead): ordinal + 1 if V held a NaN
   int abort;
   uint32_t tmem;
@@ -138,7 +153,7 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t *w) {
 template <int HD>
 __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_constant__ KtParams p) {
   typedef KtLayout<HD> Lay;
-  typedef Kv8Tiles<KT_TOKENS, KT_ROWS> Tiles;
+  typedef Kv8Tiles<KT_TOKENS, KT_ROWS, KT_COST> Tiles;
   const Kv8AttnArgs &a = p.a;
   extern __shared__ uint8_t kt_raw[];
   const uint32_t raw = smem_u32(kt_raw), base = (raw + 1023u) & ~1023u;
@@ -165,6 +180,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         mbar_init(bar(sh.l_ready[i][1][j]), 1);
       }
     }
+    for (int i = 0; i < KT_RING; ++i) mbar_init(bar(sh.known[i]), 1);
     mbar_init(bar(sh.o_full), 1);
     mbar_init(bar(sh.drain[0]), 1);
     mbar_init(bar(sh.o_empty), 8);
@@ -175,11 +191,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
   pdl_wait();
   long long chunk, item_begin;
   Kv8Piece pc;
-  if (!kv8_start<KT_TOKENS, KT_ROWS>(a, sh.grp, blockIdx.x, gridDim.x, pc, chunk, item_begin)) {   // uniform for the CTA
+  if (!kv8_start<KT_TOKENS, KT_ROWS, KT_COST>(a, sh.grp, blockIdx.x, gridDim.x, pc, chunk, item_begin)) {   // uniform for the CTA
     if (threadIdx.x == 0) a.desc[blockIdx.x].pieces = 0;
     return;
   }
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = kv8_desc<KT_TOKENS, KT_ROWS>(a, pc, blockIdx.x, chunk, item_begin);
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = kv8_desc<KT_TOKENS, KT_ROWS, KT_COST>(a, pc, blockIdx.x, chunk, item_begin);
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
@@ -190,32 +206,40 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
   const uint32_t tmem = sh.tmem;
   volatile int *abort_flag = (volatile int *)&sh.abort;
   auto wait = [&](uint64_t &b, uint32_t parity) { return kv8_wait(bar(b), parity & 1, abort_flag); };
+  auto known = [&](uint32_t n) { return __all_sync(0xffffffffu, wait(sh.known[n % KT_RING], n / KT_RING)) != 0; };
 
   if (warp == 0) {
     // ---------------- copies
     if (lane == 0) tma_prefetch_map(&p.kmap);
     uint32_t i = 0;
     bool go = true;
-    for (;;) {
-      // lane x: page x (and its scales) of the 16 tiles of this piece from tab_u on, and of the 16 after
-      // them, whose table entries and then scales are fetched while these are used
-      const int limit = Tiles(a).limit(pc.r, pc.qt);
-      int tab_u = pc.u0, next_page = -1;
-      auto table = [&](int from) {
-        const int x = 2 * from + lane;
-        return (long long)x * KV_PAGE < limit && x < 2 * pc.u1 ? a.table[(size_t)pc.b * a.width + x] : -1;
-      };
-      auto scales = [&](int &pg, float &k, float &v) {
-        if (pg < 0 || pg >= a.n_pages) pg = -1;
-        k = v = 1.f;
-        if (pg >= 0) {
-          k = a.ks[(size_t)pg * a.nkv + pc.h];
-          v = a.vs[(size_t)pg * a.nkv + pc.h];
-        }
-      };
-      float ks, vs, next_ks = 1.f, next_vs = 1.f;
-      int page = table(tab_u);
-      scales(page, ks, vs);
+    auto publish = [&](const Kv8Piece &x, uint32_t n) {
+      if (lane == 0) {
+        sh.ring[n % KT_RING] = x;
+        mbar_arrive(bar(sh.known[n % KT_RING]));
+      }
+    };
+    // lane x: page x (and its scales) of 16 tiles of a piece, and of the 16 after them (of the next
+    // piece's first), whose table entries and then scales are fetched while these are used
+    auto table = [&](const Kv8Piece &x, int from) {
+      const int pg = 2 * from + lane;
+      return (long long)pg * KV_PAGE < Tiles(a).limit(x.r, x.qt) && pg < 2 * x.u1 ? a.table[(size_t)x.b * a.width + pg] : -1;
+    };
+    auto scales = [&](int h, int &pg, float &k, float &v) {
+      if (pg < 0 || pg >= a.n_pages) pg = -1;
+      k = v = 1.f;
+      if (pg >= 0) {
+        k = a.ks[(size_t)pg * a.nkv + h];
+        v = a.vs[(size_t)pg * a.nkv + h];
+      }
+    };
+    float ks, vs, next_ks = 1.f, next_vs = 1.f, piece_ks = 1.f, piece_vs = 1.f;
+    int page = table(pc, pc.u0), next_page = -1, piece_page = -1;
+    publish(pc, 0);
+    scales(pc.h, page, ks, vs);
+    Kv8Piece nx = pc;
+    for (uint32_t pn = 0;; ++pn) {
+      int tab_u = pc.u0;
       float ev = log2f(vs), iv = 1.f / vs;
       for (int u = pc.u0; u < pc.u1 && go; ++u, ++i) {
         if (u == tab_u + 16) {
@@ -225,8 +249,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
           ev = log2f(next_vs);
           iv = 1.f / next_vs;
         }
-        if (u == tab_u + 4) next_page = table(tab_u + 16);
-        if (u == tab_u + 10) scales(next_page, next_ks, next_vs);
+        if (u == tab_u + 4) next_page = table(pc, tab_u + 16);
+        if (u == tab_u + 10) scales(pc.h, next_page, next_ks, next_vs);
         const int at = 2 * (u - tab_u), stg = i % KT_STAGES;
         const uint32_t use = i / KT_STAGES;
         go = use == 0 || (wait(sh.kempty[stg], use - 1) && wait(sh.vempty[stg], use - 1));
@@ -256,9 +280,20 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
           tma_load_3d(base + Lay::K0 + (2 * stg + x) * Lay::PAGE8, &p.kmap, 0, 0, page * a.nkv + pc.h, bar(sh.kfull[stg]));
           bulk_load(base + Lay::V0 + (2 * stg + x) * Lay::PAGE8, a.vp + kv8_block(page, pc.h, a.nkv, HD), Lay::PAGE8, bar(sh.vfull[stg]));
         }
+        if (pc.left > 0) {
+          if (u == pc.u0) {
+            kv8_next_piece<KT_TOKENS, KT_ROWS, KT_COST>(a, nx);
+            publish(nx, pn + 1);
+            piece_page = table(nx, nx.u0);
+          }
+          if (u == min(pc.u0 + 1, pc.u1 - 1)) scales(nx.h, piece_page, piece_ks, piece_vs);
+        }
       }
       if (!go || pc.left <= 0) break;
-      kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
+      pc = nx;
+      page = piece_page;
+      ks = piece_ks;
+      vs = piece_vs;
     }
     // copies in flight end before the CTA does (bounded; at once unless a wait ran out)
     const unsigned long long t0 = global_ns();
@@ -273,8 +308,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     auto wait_all = [&](uint64_t &b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
     const uint64_t k0 = HD == 128 ? sw128_desc(base + Lay::K0) : sw64_desc(base + Lay::K0), w0 = sw128_desc(base + Lay::W0);
     const uint32_t k_hi = (uint32_t)(k0 >> 32), w_hi = (uint32_t)(w0 >> 32);
-    Kv8Piece sp = pc;                                  // the piece whose S is issued next
-    int s_left = sp.u1 - sp.u0;                        // its tiles without S
+    int s_left = pc.u1 - pc.u0;                        // tiles without S of the piece whose S is issued next
     uint32_t si = 0, spn = 0;                          // tile and piece ordinals of S
     bool new_q = true, more = true;
     auto issue_s = [&]() {
@@ -293,20 +327,22 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       if (lead) mbar_arrive(bar(sh.s_full[par]));
       ++si;
       if (--s_left == 0) {
-        more = sp.left > 0;
+        more = sh.ring[spn % KT_RING].left > 0;
         if (more) {
-          kv8_next_piece<KT_TOKENS, KT_ROWS>(a, sp);
-          s_left = sp.u1 - sp.u0;
           ++spn;
+          if (!known(spn)) return false;
+          s_left = sh.ring[spn % KT_RING].u1 - sh.ring[spn % KT_RING].u0;
           new_q = true;
         }
       }
       return true;
     };
-    bool go = issue_s();
+    bool go = known(0) && issue_s();
     uint32_t i = 0;
     for (uint32_t pn = 0; go; ++pn) {
-      const int n = pc.u1 - pc.u0;
+      if (!(go = known(pn))) break;
+      const Kv8Piece &now = sh.ring[pn % KT_RING];
+      const int n = now.u1 - now.u0;
       for (int x = 0; x < n; ++x, ++i) {
         if (more && !(go = issue_s())) break;
         const uint32_t par = i & 1;
@@ -323,8 +359,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       }
       if (!go) break;
       commit_lead(lead, bar(sh.o_full));
-      if (pc.left <= 0) break;
-      kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
+      if (now.left <= 0) break;
     }
     // MMAs in flight end before the tensor memory is given back
     __syncwarp();
@@ -342,29 +377,63 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     // an infinity or NaN)
     auto load_q = [&](const Kv8Piece &x, uint32_t pn) {
       const int tk = x.qt * tpt + r / group;
-      const bool live = r < tpt * group && tk < x.r.n;
-      constexpr int N = HD / 2;                        // dims of a half
-      float big = 0.f;
-      bool fin = true;
-      const bf16 *src = (const bf16 *)a.q + (int64_t)(x.r.row0 + tk) * a.q_stride + (int64_t)(x.h * group + r % group) * HD;
+      const unsigned alive = __ballot_sync(0xffffffffu, r < tpt * group && tk < x.r.n);
+      constexpr int N = HD / 2, R = N / 32;            // dims of a half, rounds of 64 bytes of each row
+      const int64_t from = (int64_t)(x.r.row0 + tk) * a.q_stride + (int64_t)(x.h * group + r % group) * HD;
+      // Four lanes read a row, 16 bytes each: this half of 8 rows at a time into shared memory, the other
+      // half for the row's maximum only.
       uint4 w[N / 8];
+      float t0 = 0.f, t1 = 0.f;                        // largest magnitudes of the row's even and odd dims; NaN stays
+      uint4 mine[R][4], other[R][4];
 #pragma unroll
-      for (int hf = 1; hf >= 0; --hf) {                // the other half for the row's maximum, then this one
+      for (int k = 0; k < 4; ++k) {
+        const int y = 8 * k + (lane >> 2);
+        const bf16 *src = (const bf16 *)a.q + __shfl_sync(0xffffffffu, from, y) + 8 * (lane & 3);
+        const bool there = alive >> y & 1;
 #pragma unroll
-        for (int i = 0; i < N / 8; ++i) w[i] = live ? *(const uint4 *)(src + N * (half ^ hf) + 8 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-          const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float v0 = __uint_as_float(e[j] << 16), v1 = __uint_as_float(e[j] & 0xffff0000u);
-            big = fmaxf(big, fmaxf(fabsf(v0), fabsf(v1)));
-            fin = fin && fabsf(v0) <= 3.402823466e38f && fabsf(v1) <= 3.402823466e38f;
-          }
+        for (int z = 0; z < R; ++z) {
+          mine[z][k] = there ? *(const uint4 *)(src + N * half + 32 * z) : make_uint4(0, 0, 0, 0);
+          other[z][k] = there ? *(const uint4 *)(src + N * (half ^ 1) + 32 * z) : make_uint4(0, 0, 0, 0);
         }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t top = 0;
+        auto take = [&](uint32_t e) {
+          const __nv_bfloat162 m = __hmax2_nan(*(const __nv_bfloat162 *)&top, __habs2(*(const __nv_bfloat162 *)&e));
+          top = *(const uint32_t *)&m;
+        };
+#pragma unroll
+        for (int z = 0; z < R; ++z) {
+          take(mine[z][k].x), take(mine[z][k].y), take(mine[z][k].z), take(mine[z][k].w);
+          take(other[z][k].x), take(other[z][k].y), take(other[z][k].z), take(other[z][k].w);
+        }
+        take(__shfl_xor_sync(0xffffffffu, top, 1));
+        take(__shfl_xor_sync(0xffffffffu, top, 2));
+        top = __shfl_sync(0xffffffffu, top, 4 * (lane & 7));       // of row 8 k + lane % 8
+        if (lane >> 3 == k) {
+          t0 = __uint_as_float(top << 16);
+          t1 = __uint_as_float(top & 0xffff0000u);
+        }
+      }
+      const uint32_t stage = base + Lay::OUT0 + (warp - 2) * 2048;
+#pragma unroll
+      for (int z = 0; z < R; ++z) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int y = 8 * k + (lane >> 2);
+          sts128(stage + 64 * y + 16 * ((lane & 3) ^ (y >> 1 & 3)), (const uint32_t *)&mine[z][k]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[4 * z + c] = lds128(stage + 64 * lane + 16 * (c ^ (lane >> 1 & 3)));
+      }
+      const bool fin = t0 <= 3.402823466e38f && t1 <= 3.402823466e38f;
+      const float big = fmaxf(t0, t1);
       const int e = fin ? max(-100, (int)(__float_as_uint(big) >> 23) - 127) : 0;
-      const float up = exp2f((float)(7 - e));
+      const float up = __uint_as_float((uint32_t)(134 - e) << 23);             // 2^(7 - e)
+      const uint32_t keep = fin ? ~0u : 0u;
       const uint32_t dst = lane_base + TM_Q + (pn & 1) * 64 + half * (N / 4);
 #pragma unroll
       for (int c = 0; c < N / 4; c += 8) {
@@ -372,15 +441,16 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint4 &b = w[(c + j) / 2];
-          const uint32_t e0 = j & 1 ? b.z : b.x, e1 = j & 1 ? b.w : b.y;
-          float y[4] = {__uint_as_float(e0 << 16), __uint_as_float(e0 & 0xffff0000u), __uint_as_float(e1 << 16),
-                        __uint_as_float(e1 & 0xffff0000u)};
+          uint32_t h[2], l[2];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) y[z] = fin ? y[z] * up : 0.f;
-          const uint32_t h0 = f32_to_e4m3x2(y[0], y[1]), h1 = f32_to_e4m3x2(y[2], y[3]);
-          const float2 f0 = e4m3x2_to_f32(h0), f1 = e4m3x2_to_f32(h1);
-          hi[j] = h0 | h1 << 16;
-          lo[j] = f32_to_e5m2x2(y[0] - f0.x, y[1] - f0.y) | f32_to_e5m2x2(y[2] - f1.x, y[3] - f1.y) << 16;
+          for (int z = 0; z < 2; ++z) {                // f16 holds the scaled value and the difference exactly
+            const uint32_t e = (j & 1 ? (z ? b.w : b.z) : (z ? b.y : b.x)) & keep;
+            const uint32_t y = pack_f16(__uint_as_float(e << 16) * up, __uint_as_float(e & 0xffff0000u) * up);
+            h[z] = f16x2_to_e4m3x2(y);
+            l[z] = f16x2_to_e5m2x2(sub_f16x2(y, e4m3x2_to_f16x2(h[z])));
+          }
+          hi[j] = h[0] | h[1] << 16;
+          lo[j] = l[0] | l[1] << 16;
         }
         tmem_st8(dst + c, hi);
         tmem_st8(dst + 32 + c, lo);
@@ -389,39 +459,47 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.q_full[pn & 1]));
-      return fin ? a.scale * 1.44269504088896341f * exp2f((float)(e - 7)) : NAN;
+      return fin ? a.scale * 1.44269504088896341f * __uint_as_float((uint32_t)(120 + e) << 23) : NAN;
     };
-    float rs_next = load_q(pc, 0);
-    uint32_t i = 0, pn = 0;                            // tile and piece ordinals
+    Kv8Piece &mine = sh.piece[warp - 2];
+    auto keep = [&](const Kv8Piece &x) {
+      __syncwarp();
+      if (lane == 0) mine = x;
+      __syncwarp();
+    };
+    keep(pc);
+    uint32_t i = 0, pn = 0, qn = 0;                    // tile and piece ordinals, the piece whose Q is next
+    float rs = 0.f, rs_next = 0.f;
     bool first = true;
     for (;; ++pn) {
-      const float rs = rs_next;
-      if (pc.left > 0) {
-        Kv8Piece nx = pc;
-        kv8_next_piece<KT_TOKENS, KT_ROWS>(a, nx);
-        rs_next = load_q(nx, pn + 1);
+#pragma unroll 1
+      for (; qn <= pn + 1; ++qn) {                     // at first its own Q, then the next piece's
+        rs = rs_next;
+        if ((qn == 0 || mine.left > 0) && known(qn)) rs_next = load_q(sh.ring[qn % KT_RING], qn);
       }
-      const int tk = pc.qt * tpt + r / group;
-      const bool live = r < tpt * group && tk < pc.r.n;
+      const int tk = mine.qt * tpt + r / group;
+      const bool live = r < tpt * group && tk < mine.r.n;
       const bool quiet = !__any_sync(0xffffffffu, live);       // no row of this warp: only the barriers
-      const int open = a.mask == DFLASH_MASK_NONE ? pc.r.len : max(0, pc.r.len - pc.r.n);
+      const int u0 = mine.u0, u1 = mine.u1;
+      // pages from `open` on hold a token that some row of the request does not see
+      const int open = (a.mask == DFLASH_MASK_NONE ? mine.r.len : max(0, mine.r.len - mine.r.n)) / KV_PAGE;
       const float fac = live && rs == rs ? rs : 0.f;
       float m_used = -INFINITY, l = 0.f;
-      for (int u = pc.u0; u < pc.u1; ++u, ++i) {
+      for (int u = u0; u < u1; ++u, ++i) {
         const int par = i & 1;
         ok = __all_sync(0xffffffffu, ok && wait(sh.s_full[par], i >> 1));
         if (!ok) break;
         const uint32_t sa = lane_base + par * 128 + half * 64;   // my 64 tokens
         const KtSide &sd = sh.side[i % KT_SIDE];
         const float c = fac * sd.ks[half], ev = sd.ev[half];
-        const bool partial = sd.page[half] < 0 || (long long)(2 * u + half + 1) * KV_PAGE > open;
+        const bool partial = sd.page[half] < 0 || 2 * u + half >= open;
         // S of my tokens, without what the row does not see
         auto load_s = [&](float *sc) {
           tmem_ld32(sa, sc);
           tmem_ld32(sa + 32, sc + 32);
           tmem_ld_wait();
           if (partial) {
-            const uint64_t see = live && sd.page[half] >= 0 ? kv8_visible(a, pc.r, tk, 2 * u + half) : 0;
+            const uint64_t see = live && sd.page[half] >= 0 ? kv8_visible(a, mine.r, tk, 2 * u + half) : 0;
             const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -465,37 +543,39 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         // The maxima are traded with the other half's warp. A first tile waits for them; any other keeps the
         // reference and makes half of its P meanwhile, in vain only if some row of the pair outgrew
         // its reference by 2^8.
-        bool grow = u == pc.u0 || __any_sync(0xffffffffu, mt > m_used + 8.f);
+        bool grow = u == u0 || __any_sync(0xffffffffu, mt > m_used + 8.f);
         sh.xmax[par][half][r] = mt;
         if (lane == 0) sh.xgrow[par][half][q] = grow;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.x_ready[par][q]));
-        if (!grow && !quiet) sum = exps(sc, pw);
-        ok = __all_sync(0xffffffffu, wait(sh.x_ready[par][q], i >> 1));
-        if (!ok) break;
-        grow = grow || *(volatile int *)&sh.xgrow[par][half ^ 1][q] != 0;
-        if (grow) {
+#pragma unroll 1
+        for (bool traded = false;; traded = true) {    // (one copy of the code for before and after the trade)
+          if ((traded || !grow) && !quiet) sum = exps(sc, pw);
+          if (traded) break;
+          ok = __all_sync(0xffffffffu, wait(sh.x_ready[par][q], i >> 1));
+          if (!ok) break;
+          grow = grow || *(volatile int *)&sh.xgrow[par][half ^ 1][q] != 0;
+          if (!grow) break;
           const float m_new = fmaxf(m_used, fmaxf(mt, sh.xmax[par][half ^ 1][r]));
           const float corr = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
           m_used = m_new;
-          if (u > pc.u0) {
-            // O so far is scaled down (P.V of the tile before must be done; this one's waits for this warp)
-            l *= corr;
-            ok = __all_sync(0xffffffffu, wait(sh.pv_done[par ^ 1], (i - 1) >> 1));
-            if (!ok) break;
-            tc_fence_after();
+          if (u == u0) continue;
+          // O so far is scaled down (P.V of the tile before must be done; this one's waits for this warp)
+          l *= corr;
+          ok = __all_sync(0xffffffffu, wait(sh.pv_done[par ^ 1], (i - 1) >> 1));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < HD / 2; c0 += 16) {
-              const uint32_t oa = lane_base + TM_O + (HD / 2) * half + c0;
-              tmem_ld16(oa, pw);
-              tmem_ld_wait();
+          for (int c0 = 0; c0 < HD / 2; c0 += 16) {
+            const uint32_t oa = lane_base + TM_O + (HD / 2) * half + c0;
+            tmem_ld16(oa, pw);
+            tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) pw[j] = __float_as_uint(__uint_as_float(pw[j]) * corr);
-              tmem_st16(oa, pw);
-            }
+            for (int j = 0; j < 16; ++j) pw[j] = __float_as_uint(__uint_as_float(pw[j]) * corr);
+            tmem_st16(oa, pw);
           }
-          if (!quiet) sum = exps(sc, pw);
         }
+        if (!ok) break;
         if (!quiet) {
           tmem_st16(sa, pw);
           sum += exps(sc + 32, pw);
@@ -508,6 +588,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         if (lane == 0) mbar_arrive(bar(sh.p_full[par]));
       }
       // the row's sum over both halves (by piece parity: the other warp may be a piece ahead)
+      const Kv8Piece pc = mine;
       float l_row = 0.f;
       const int pp = pn & 1;
       sh.lsum[pp][half][r] = l;
@@ -527,23 +608,41 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         else if (a.lse) a.lse[at] = l_row == 0.f ? -INFINITY : (m_used - KT_BIAS + log2f(l_row)) * LN2;
       }
       const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
+      // A warp's results go through shared memory, 64 bytes of each row at a time, so that four lanes
+      // write a row: a store of one row per lane costs a cycle per row.
+      const uint32_t stage = base + Lay::OUT0 + (warp - 2) * 2048;
+      const uint32_t put = stage + lane * 64;          // chunk c of row x at c ^ (x >> 1 & 3)
+      const int64_t to = whole ? (int64_t)at * HD * 2 : (int64_t)(slot * KT_ROWS + r) * HD * 4;
+      uint8_t *dst = whole ? (uint8_t *)a.out : (uint8_t *)a.part_o;
+      const unsigned alive = __ballot_sync(0xffffffffu, live);
+      auto flush = [&](int byte) {                     // 64 bytes of each row, from `byte` of the row on
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = 8 * k + (lane >> 2), c = lane & 3;
+          const int64_t row = __shfl_sync(0xffffffffu, to, x);
+          const uint4 y = lds128(stage + x * 64 + 16 * (c ^ (x >> 1 & 3)));
+          if (alive >> x & 1) *(uint4 *)(dst + row + byte + 16 * c) = y;
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int c0 = 0; c0 < HD / 2; c0 += 16) {
         uint32_t t[16];
         const int d0 = (HD / 2) * half + c0;
-        if (ok && !quiet) {
+        if (quiet) break;
+        if (ok) {
           tmem_ld16(lane_base + TM_O + d0, t);
           tmem_ld_wait();
         }
-        if (!live) continue;
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = ok ? __uint_as_float(t[j]) : NAN;
-        if (nan_v) {                                   // rows that see a NaN value get it (rare)
+        if (nan_v && live) {                           // rows that see a NaN value get it (rare)
           uint32_t hit = 0;
           const int lim = Tiles(a).limit(pc.r, pc.qt);
 #pragma unroll 1
-          for (int x = max(2 * pc.u0, open / KV_PAGE); x < 2 * pc.u1 && (long long)x * KV_PAGE < lim; ++x) {
+          for (int x = max(2 * pc.u0, open); x < 2 * pc.u1 && (long long)x * KV_PAGE < lim; ++x) {
             const int page = a.table[(size_t)pc.b * a.width + x];
             if (page < 0 || page >= a.n_pages) continue;
             const uint64_t see = kv8_visible(a, pc.r, tk, x);
@@ -556,27 +655,37 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
           for (int j = 0; j < 16; ++j)
             if (hit >> j & 1) v[j] = NAN;
         }
-        if (whole) {
-          uint32_t h[8];
+        uint32_t h[16];
+        const int sw = lane >> 1 & 3;
+        if (whole) {                                   // 32 bytes of the row: two rounds fill the 64
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j] * inv, v[2 * j + 1] * inv);
             h[j] = *(const uint32_t *)&b;
           }
-          uint4 *dst = (uint4 *)((bf16 *)a.out + at * HD + d0);
-          dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-          dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          const int c = c0 >> 3 & 2;
+          sts128(put + 16 * (c ^ sw), h);
+          sts128(put + 16 * ((c + 1) ^ sw), h + 4);
+          if (c) flush(2 * (d0 - 16));
         } else {
-          float4 *dst = (float4 *)(a.part_o + (slot * KT_ROWS + r) * HD + d0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 16; ++j) h[j] = __float_as_uint(v[j]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sts128(put + 16 * (c ^ sw), h + 4 * c);
+          flush(4 * d0);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.o_empty));
       if (pc.left <= 0) break;
-      kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
+      if (known(pn + 1)) {
+        keep(sh.ring[(pn + 1) % KT_RING]);
+      } else {                                         // a wait ran out: the rows left become NaN all the same
+        Kv8Piece nx = pc;
+        kv8_next_piece<KT_TOKENS, KT_ROWS, KT_COST>(a, nx);
+        keep(nx);
+      }
       first = false;
     }
   } else {
@@ -585,59 +694,60 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     uint32_t i = 0;
     bool go = true;
     for (uint32_t pn = 0; go; ++pn) {
+      if (!(go = known(pn))) break;
+      const Kv8Piece pc = sh.ring[pn % KT_RING];
       const int open = a.mask == DFLASH_MASK_NONE ? pc.r.len : max(0, pc.r.len - pc.r.n);
       for (int u = pc.u0; u < pc.u1; ++u, ++i) {
         const int stg = i % KT_STAGES, par = i & 1;
         go = wait(sh.vfull[stg], i / KT_STAGES) && (i < 2 || wait(sh.pv_done[par], (i >> 1) - 1));
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
-        constexpr int N = HD * 4 / KT_WIDEN;           // pieces of 16 tokens of one dim: all loads first
-        uint4 v[2][N];
-        const uint32_t src = base + Lay::V0 + 2 * stg * Lay::PAGE8 + tid * 16;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[x][j] = lds128(src + x * Lay::PAGE8 + KT_WIDEN * 16 * j);
-        const KtSide &sd = sh.side[i % KT_SIDE];
-        if (sd.page[0] < 0 || sd.page[1] < 0 || (long long)(u + 1) * KT_TOKENS > open) {
-          bool nan = false;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            // tokens that exist, from this thread's 16: the rest may be anything
-            const int tail = sd.page[x] < 0 ? 0 : pc.r.len - (2 * u + x) * KV_PAGE - 16 * (tid & 3);
-            const bool hidden = (long long)(2 * u + x + 1) * KV_PAGE > open;   // some row does not see some token
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-              uint32_t *w = (uint32_t *)&v[x][j];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int n = tail - 4 * k;
-                w[k] = n >= 4 ? w[k] : n <= 0 ? 0u : w[k] & ((1u << 8 * n) - 1);
-                const uint32_t nb = hidden ? nan_bytes(w[k]) : 0u;   // must not meet a hidden token's zero weight
-                nan |= nb != 0;
-                w[k] &= ~byte_mask(nb);
-              }
-            }
-          }
-          if (nan) *(volatile int *)&sh.nan_piece[pn & 3] = (int)pn + 1;
-        }
         // row d of V^T in 128-byte rows, its 16-byte chunk c at c ^ (d & 7); d & 7 is the same for all j
-        const uint32_t dst = base + Lay::W0 + 2 * par * Lay::PAGE16 + (tid >> 2) * 128;
         const uint32_t c0 = (2 * (tid & 3)) ^ (tid >> 2 & 7), c1 = c0 ^ 1;
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          constexpr int N = HD * 4 / KT_WIDEN;         // pieces of 16 tokens of one dim: all loads first
+          uint4 v[N];
+          const uint32_t src = base + Lay::V0 + (2 * stg + x) * Lay::PAGE8 + tid * 16;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const uint32_t w[4] = {v[x][j].x, v[x][j].y, v[x][j].z, v[x][j].w};
-            uint32_t f[8];
+          for (int j = 0; j < N; ++j) v[j] = lds128(src + KT_WIDEN * 16 * j);
+          const int page = sh.side[i % KT_SIDE].page[x];
+          const long long end = (long long)(2 * u + x + 1) * KV_PAGE;
+          if (page < 0 || end > open) {
+            // tokens that exist, from this thread's 16: the rest may be anything
+            const int tail = page < 0 ? 0 : pc.r.len - (2 * u + x) * KV_PAGE - 16 * (tid & 3);
+            uint32_t any = 0;                          // some row does not see some token: a NaN must not meet its zero weight
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              e4m3x4_to_f16(w[k], f[2 * k], f[2 * k + 1]);
+              const int n = tail - 4 * k;
+              const uint32_t there = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << 8 * n) - 1;
+#pragma unroll
+              for (int j = 0; j < N; ++j) {
+                uint32_t &w = ((uint32_t *)&v[j])[k];
+                w &= there;
+                any |= nan_bytes(w);
+              }
             }
-            const uint32_t at = dst + x * Lay::PAGE16 + j * (KT_WIDEN / 4 * 128);
-            sts128(at + 16 * c0, f);
-            sts128(at + 16 * c1, f + 4);
+            if (any) {
+#pragma unroll
+              for (int j = 0; j < 4 * N; ++j) {
+                uint32_t &w = ((uint32_t *)&v[j / 4])[j % 4];
+                w &= ~byte_mask(nan_bytes(w));
+              }
+              *(volatile int *)&sh.nan_piece[pn & 3] = (int)pn + 1;
+            }
           }
+          const uint32_t dst = base + Lay::W0 + (2 * par + x) * Lay::PAGE16 + (tid >> 2) * 128;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e4m3x4_to_f16(w[k], f[2 * k], f[2 * k + 1]);
+            sts128(dst + j * (KT_WIDEN / 4 * 128) + 16 * c0, f);
+            sts128(dst + j * (KT_WIDEN / 4 * 128) + 16 * c1, f + 4);
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -646,7 +756,6 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         }
       }
       if (!go || pc.left <= 0) break;
-      kv8_next_piece<KT_TOKENS, KT_ROWS>(a, pc);
     }
   }
   tc_fence_before();

@@ -40,9 +40,20 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x2(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t f32_to_e5m2x2(float a, float b) {
+// the same from f16 pairs, and to e5m2
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
   uint32_t r;
-  asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e5m2x2.f32 t, %2, %1;\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "f"(a), "f"(b));
+  asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t h) {
+  uint32_t r;
+  asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e5m2x2.f16x2 t, %1;\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 

@@ -114,8 +114,8 @@ __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile
   }
 }
 
-// The kernel for many query rows (bf16): tiles of 128 rows and 128 tokens, one worker per SM.
-constexpr int KT_ROWS = 128, KT_TOKENS = 128;
+// The kernel for many query rows (bf16): tiles of 128 rows, one worker per SM.
+constexpr int KT_ROWS = 128;
 cudaError_t launch_kv8_tiles(const Kv8AttnArgs &a, int hd, cudaStream_t s);
 
 }  // namespace dflash

@@ -1,12 +1,13 @@
 // The work of one attention call over the 8-bit cache, cut into equal pieces on the GPU.
 //
 // An item is (request, tile of query tokens, kv head); its units are the U-token stretches of the
-// context that its rows may see. All units, in the order requests > tiles > heads > units, form
-// one line that is cut into equal chunks, one per worker; a worker thus owns at most two
-// pieces of items that others also work on (its first and its last), whose partial results go to
-// the workspace and are merged by k_kv8_combine. Every worker finds its start by itself from the
-// lengths on the GPU: unit counts of 32 requests are summed by a warp, the sums of those
-// groups sit in shared memory, and the unit counts inside a request have a closed form.
+// context that its rows may see. All items, in the order requests > tiles > heads, each as C + its units
+// long (C: what its start and end cost a worker), form one line that is cut into equal chunks, one per
+// worker; a worker thus owns at most two pieces of items that others also work on (its
+// first and its last), whose partial results go to the workspace and are merged by k_kv8_combine. An item
+// whose first C fall to a worker without any of its units begins with the next worker. Every worker finds its
+// start by itself from the lengths on the GPU: lengths of 32 requests are summed by a warp, the sums of those
+// groups sit in shared memory, and the lengths inside a request have a closed form.
 #pragma once
 #include "kv8.cuh"
 
@@ -37,7 +38,8 @@ struct alignas(16) Kv8Desc {
   int row0, rows, h, pad[3];   // first query row (token) of the tile, its rows (tokens x heads), kv head
 };
 
-// sum over i < n of floor((a i + b) / m), for a, b >= 0
+// sum over i < n of floor((a i + b) / m), for a, b >= 0 (called, not inlined, as what follows: the start of a kernel is
+// mostly the fetching of its code)
 static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   while (n > 0) {
@@ -54,6 +56,13 @@ static __device__ __noinline__ long long floor_sum(long long n, long long m, lon
   return s;
 }
 
+// weight of a causal request's tiles before qt; first: position of its first row
+static __device__ __noinline__ long long kv8_before_causal(int U, int C, int tpt, int qt, int first) {
+  if (qt == 0) return 0;
+  const int t0 = first < 0 ? min(qt, -first / tpt) : 0;          // tiles that see nothing have one unit
+  return (long long)qt * C + t0 + floor_sum(qt - t0, U, tpt, first + (long long)(t0 + 1) * tpt + U - 1);
+}
+
 struct Kv8Req {
   int n, len, row0;            // rows, context length, first row
 };
@@ -66,7 +75,7 @@ __device__ __forceinline__ Kv8Req kv8_req(const Kv8AttnArgs &a, int b) {
 }
 
 // Tokens of a tile, tokens it may see, units: M rows of a tile hold M / group tokens.
-template <int U, int M>
+template <int U, int M, int C>
 struct Kv8Tiles {
   int tpt, nkv, causal;
   __device__ __forceinline__ Kv8Tiles(const Kv8AttnArgs &a)
@@ -78,17 +87,15 @@ struct Kv8Tiles {
                   : r.len;
   }
   __device__ __forceinline__ int units(const Kv8Req &r, int qt) const { return max(1, (limit(r, qt) + U - 1) / U); }
-  // units of one head's tiles before qt, for qt < tiles
+  // what an item takes on the line: C units for its start and end, then its units
+  __device__ __forceinline__ long long weight(const Kv8Req &r, int qt) const { return C + (long long)units(r, qt); }
+  // weight of one head's tiles before qt, for qt < tiles
   __device__ __forceinline__ long long before(const Kv8Req &r, int qt) const {
-    if (!causal) return (long long)qt * units(r, 0);
-    if (qt == 0) return 0;
-    const long long A = (long long)r.len - r.n;                // the row before the first one's position + 1
-    const int t0 = (int)min((long long)qt, A < 0 ? -A / tpt : 0ll);   // tiles that see nothing have one unit
-    return t0 + floor_sum(qt - t0, U, tpt, A + (long long)(t0 + 1) * tpt + U - 1);
+    return causal ? kv8_before_causal(U, C, tpt, qt, r.len - r.n) : qt * weight(r, 0);
   }
   __device__ __forceinline__ long long total(const Kv8Req &r) const {
     const int nt = tiles(r);
-    return nt ? nkv * (before(r, nt - 1) + units(r, nt - 1)) : 0;
+    return nt ? nkv * (before(r, nt - 1) + weight(r, nt - 1)) : 0;
   }
 };
 
@@ -97,7 +104,7 @@ struct Kv8Piece {
   Kv8Req r;
   int b, qt, h;
   int u0, u1, units;           // [u0, u1) of the item's units
-  long long left;              // units of the worker after this piece
+  long long left;              // of the worker's stretch after this piece; 0: no more pieces
 };
 
 // x / y for 0 <= x, 0 < y: one 32-bit division where both fit
@@ -117,12 +124,12 @@ __device__ __forceinline__ long long warp_scan_ll(long long x) {       // inclus
 }
 
 // The start of worker `me` of `workers`: false if it has nothing to do. The whole CTA calls it (s_grp is for more
-// than 32 requests only); chunk gets the units per worker, item_begin the first unit of the first
-// piece's item. For up to 32 requests every warp sums them up by itself, without a barrier.
-template <int U, int M>
+// than 32 requests only); chunk gets a worker's length of the line, item_begin where the first
+// piece's item begins. For up to 32 requests every warp sums them up by itself, without a barrier.
+template <int U, int M, int C>
 __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp, int me, int workers, Kv8Piece &p,
                                           long long &chunk, long long &item_begin) {
-  const Kv8Tiles<U, M> tl(a);
+  const Kv8Tiles<U, M, C> tl(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (a.n_req + 31) / 32;
   long long total = 0;
@@ -185,7 +192,7 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
   const long long count = min(chunk, total - pos);
   p.qt = 0;
   if (!tl.causal) {
-    p.qt = (int)div_ll(off, (long long)tl.units(p.r, 0) * a.nkv);
+    p.qt = (int)div_ll(off, tl.weight(p.r, 0) * a.nkv);
   } else {
     int l = 0, h = tl.tiles(p.r) - 1;
     while (l < h) {
@@ -197,23 +204,27 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
   }
   p.units = tl.units(p.r, p.qt);
   const long long in_tile = off - tl.before(p.r, p.qt) * a.nkv;
-  p.h = (int)div_ll(in_tile, p.units);
-  p.u0 = (int)(in_tile - (long long)p.h * p.units);
-  p.u1 = (int)min((long long)p.units, p.u0 + count);
-  p.left = count - (p.u1 - p.u0);
-  item_begin = pos - p.u0;
-  return true;
+  const long long w = C + (long long)p.units;
+  p.h = (int)div_ll(in_tile, w);
+  const long long x0 = in_tile - p.h * w, x1 = min(w, x0 + count);
+  item_begin = pos - x0;
+  p.u0 = (int)max(0ll, x0 - C);
+  p.u1 = (int)max(0ll, x1 - C);
+  p.left = count - (x1 - x0);
+  if (p.left <= C) p.left = 0;                         // the next item's units are all the next worker's
+  return p.u1 > 0;
 }
 
 // The descriptor of worker `me`, whose first piece is p.
-template <int U, int M>
+template <int U, int M, int C>
 __device__ __forceinline__ Kv8Desc kv8_desc(const Kv8AttnArgs &a, const Kv8Piece &p, int me, long long chunk, long long item_begin) {
   Kv8Desc d{0, 0, 0, 0, 0, {0, 0, 0}};
   const long long pos = me * chunk;
-  if (item_begin < pos && item_begin >= pos - chunk) {
-    const Kv8Tiles<U, M> tl(a);
-    d.pieces = (int)div_ll(item_begin + p.units - 1, chunk) - me + 2;       // up to the worker of the last unit
-    d.slot0 = 2 * (me - 1) + (item_begin == pos - chunk ? 0 : 1);
+  const long long begin = item_begin + C;              // the item's first unit
+  if (begin < pos && begin >= pos - chunk) {
+    const Kv8Tiles<U, M, C> tl(a);
+    d.pieces = (int)div_ll(begin + p.units - 1, chunk) - me + 2;       // up to the worker of the last unit
+    d.slot0 = 2 * (me - 1) + (item_begin <= pos - chunk ? 0 : 1);
     d.row0 = p.r.row0 + p.qt * tl.tpt;
     d.rows = min(tl.tpt, p.r.n - p.qt * tl.tpt) * (a.nq / a.nkv);
     d.h = p.h;
@@ -222,9 +233,9 @@ __device__ __forceinline__ Kv8Desc kv8_desc(const Kv8AttnArgs &a, const Kv8Piece
 }
 
 // The next piece of the same worker; p.left > 0.
-template <int U, int M>
+template <int U, int M, int C>
 __device__ __forceinline__ void kv8_next_piece(const Kv8AttnArgs &a, Kv8Piece &p) {
-  const Kv8Tiles<U, M> tl(a);
+  const Kv8Tiles<U, M, C> tl(a);
   if (++p.h == a.nkv) {
     p.h = 0;
     if (++p.qt == tl.tiles(p.r)) {
@@ -241,8 +252,9 @@ __device__ __forceinline__ void kv8_next_piece(const Kv8AttnArgs &a, Kv8Piece &p
     p.units = tl.units(p.r, p.qt);
   }
   p.u0 = 0;
-  p.u1 = (int)min((long long)p.units, p.left);
-  p.left -= p.u1;
+  p.u1 = (int)min((long long)p.units, p.left - C);
+  p.left -= C + p.u1;
+  if (p.left <= C) p.left = 0;
 }
 
 // Which of the 64 tokens of page `page_no` the row of `token` (index among the request's rows) sees,
