@@ -208,9 +208,28 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  x = fabsf(x);
-  return x <= 3.402823466e38f ? x : 0.f;              // infinities and NaN have no say
+// The largest |x| of 16 bytes, NaN left out; and with infinities left out too.
+template <typename T>
+__device__ __forceinline__ float largest(const uint4 &q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (sizeof(T) == 4)
+    return fmaxf(fmaxf(fabsf(__uint_as_float(w[0])), fabsf(__uint_as_float(w[1]))),
+                 fmaxf(fabsf(__uint_as_float(w[2])), fabsf(__uint_as_float(w[3]))));
+  __nv_bfloat162 m = __habs2(*(const __nv_bfloat162 *)&w[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) m = __hmax2(m, __habs2(*(const __nv_bfloat162 *)&w[j]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <typename T>
+__device__ __forceinline__ float largest_finite(const uint4 &q) {
+  const T *t = (const T *)&q;
+  float big = 0.f;
+#pragma unroll
+  for (int j = 0; j < (int)(16 / sizeof(T)); ++j) {
+    const float x = fabsf(to_f(t[j]));
+    if (x <= 3.402823466e38f) big = fmaxf(big, x);
+  }
+  return big;
 }
 
 // four e4m3 bytes times a factor, rounded again
@@ -220,7 +239,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(KA_THREADS) k_kv8_append(const AppendArgs<T> a) {
+__global__ void __launch_bounds__(KA_THREADS, 6) k_kv8_append(const AppendArgs<T> a) {
   constexpr int V = 16 / sizeof(T);                   // values of a 16-byte load
   constexpr int TPR = HD / V;                         // threads of a row
   constexpr int NP = KV_PAGE * TPR / KA_THREADS;      // neighbouring rows of a thread
@@ -280,21 +299,23 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv8_append(const AppendArgs<T> a
     }
     // the CTA's rows of the page, one 16-byte piece per thread and row
     const int c = tid % TPR, off0 = tid / TPR * NP;
+    const uint32_t mine = (uint32_t)(owned >> off0);   // bit p: row p of the thread
     uint4 q[NP];
     float big = 0.f;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const int off = off0 + p, row = plain ? i + off - first : owner[off];
-      q[p] = owned >> off & 1 ? *(const uint4 *)(src + (int64_t)row * stride + (int64_t)h * HD + c * V) : make_uint4(0, 0, 0, 0);
+      q[p] = mine >> p & 1 ? *(const uint4 *)(src + (int64_t)row * stride + (int64_t)h * HD + c * V) : make_uint4(0, 0, 0, 0);
     }
     float *sp = (isv ? a.vscale : a.kscale) + (size_t)page * a.nkv + h;
     const bool fresh = owned & 1;
     const float old = fresh ? 0.f : *sp;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const T *t = (const T *)&q[p];
+    for (int p = 0; p < NP; ++p) big = fmaxf(big, largest<T>(q[p]));
+    if (!(big <= 3.402823466e38f)) {                  // infinities and NaN have no say
+      big = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) big = fmaxf(big, finite_abs(to_f(t[j])));
+      for (int p = 0; p < NP; ++p) big = fmaxf(big, largest_finite<T>(q[p]));
     }
     big = warp_max(big);
     if (lane == 0) s_max[tid >> 5] = big;
@@ -319,14 +340,15 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv8_append(const AppendArgs<T> a
                       f32_to_e4m3x2(to_f(t[j + 2]) * inv, to_f(t[j + 3]) * inv) << 16;
     }
     if (!isv) {
+      const uint32_t keep = (uint32_t)(kept >> off0);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int off = off0 + p;
         uint8_t *dst = blk + off * HD + c * V;
-        if (kept >> off & 1) {
+        if (keep >> p & 1) {
 #pragma unroll
           for (int j = 0; j < V / 4; ++j) w[p][j] = rescale4(*(const uint32_t *)(dst + 4 * j), again);
-        } else if (!(owned >> off & 1)) {
+        } else if (!(mine >> p & 1)) {
           continue;
         }
         if constexpr (V == 8) *(uint2 *)dst = make_uint2(w[p][0], w[p][1]);
@@ -334,19 +356,37 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv8_append(const AppendArgs<T> a
       }
       __syncthreads();                                // s_max and owner are free again
     } else {
+      auto at = [&](int d, int off) { return &tile[d * (KV_PAGE / 4) + ((off >> 2) ^ (d >> 3 & 15))]; };
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < V; j += 4) {
         const int d = c * V + j;
-        auto byte = [&](int p) { return w[p][j / 4] >> (8 * (j & 3)) & 0xff; };
-        auto at = [&](int off) { return (uint8_t *)&tile[d * (KV_PAGE / 4) + ((off >> 2) ^ (d >> 3 & 15))] + (off & 3); };
         if constexpr (NP >= 4) {
 #pragma unroll
-          for (int p = 0; p < NP; p += 4) *(uint32_t *)at(off0 + p) = byte(p) | byte(p + 1) << 8 | byte(p + 2) << 16 | byte(p + 3) << 24;
+          for (int p = 0; p < NP; p += 4) {           // four tokens' four dims turned into four dims' four tokens
+            const uint32_t x0 = w[p][j / 4], x1 = w[p + 1][j / 4], x2 = w[p + 2][j / 4], x3 = w[p + 3][j / 4];
+            const uint32_t a0 = __byte_perm(x0, x1, 0x5140), a1 = __byte_perm(x2, x3, 0x5140);
+            const uint32_t b0 = __byte_perm(x0, x1, 0x7362), b1 = __byte_perm(x2, x3, 0x7362);
+            *at(d, off0 + p) = __byte_perm(a0, a1, 0x5410);
+            *at(d + 1, off0 + p) = __byte_perm(a0, a1, 0x7632);
+            *at(d + 2, off0 + p) = __byte_perm(b0, b1, 0x5410);
+            *at(d + 3, off0 + p) = __byte_perm(b0, b1, 0x7632);
+          }
         } else {
-          *(uint16_t *)at(off0) = (uint16_t)(byte(0) | byte(1) << 8);
+          const uint32_t a = __byte_perm(w[0][j / 4], w[1][j / 4], 0x5140), b = __byte_perm(w[0][j / 4], w[1][j / 4], 0x7362);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *((uint16_t *)at(d + k, off0) + (off0 >> 1 & 1)) = (uint16_t)((k < 2 ? a : b) >> 16 * (k & 1));
         }
       }
       __syncthreads();
+      if (!~owned) {                                  // a whole page: 16 tokens of a dim at a time
+#pragma unroll
+        for (int t = tid; t < HD * (KV_PAGE / 16); t += KA_THREADS) {
+          const int d = t / (KV_PAGE / 16), o = t % (KV_PAGE / 16) * 4, x = d >> 3 & 15;
+          const uint32_t *row = &tile[d * (KV_PAGE / 4)];
+          *(uint4 *)(blk + 16 * t) = make_uint4(row[o ^ x], row[(o + 1) ^ x], row[(o + 2) ^ x], row[(o + 3) ^ x]);
+        }
+      } else
 #pragma unroll 4
       for (int t = tid; t < HD * (KV_PAGE / 4); t += KA_THREADS) {
         const int d = t / (KV_PAGE / 4), o = t % (KV_PAGE / 4);

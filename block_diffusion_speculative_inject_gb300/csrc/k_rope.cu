@@ -50,44 +50,54 @@ struct alignas(N * sizeof(T)) Vec {
   T v[N];
 };
 
-// ROWS rows of a CTA; V elements per access (16 bytes, or one element where a row, a head or the
-// rotated part does not keep 16-byte alignment).
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ RopeArgs a, int rows_per_cta) {
-  extern __shared__ float2 cs[];                      // [rows][pairs]
+// A CTA turns one row; V elements per access (16 bytes, or one element where a row, a head or the
+// rotated part does not keep 16-byte alignment). EARLY: for rows of one chunk per thread, whose loads are then on
+// their way while the angles are made (5003 rows of 16 x 64 fp32: 10.1 against 13.7 us). Longer rows have more
+// loads after the first, and the registers held across the barrier cost them more (32768 rows of 48 x 128 bf16: 152
+// against 123 us, 6.5 TB/s).
+template <typename T, int V, bool INTER, bool EARLY>
+__global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ RopeArgs a) {
+  extern __shared__ float2 cs[];                      // [pairs]
   pdl_trigger();
   pdl_wait();
-  const int pairs = a.rot / 2;
-  const int r0 = blockIdx.x * rows_per_cta, nr = min(rows_per_cta, a.rows - r0);
-  for (int i = threadIdx.x; i < nr * pairs; i += ROPE_THREADS) {
-    const int r = i / pairs, p = i - r * pairs;
-    float2 t = phase_cs((uint64_t)(int64_t)a.positions[r0 + r] * a.turn[p]);
-    t.x *= a.magnitude;
-    t.y *= a.transpose ? -a.magnitude : a.magnitude;
-    cs[i] = t;
-  }
-  __syncthreads();
+  const int pairs = a.rot / 2, row = blockIdx.x;
   // Chunks of a head: the half layout takes V dims of the first half with their partners, the
   // interleaved one V neighbouring dims (V / 2 pairs, one pair where V is 1); then the copied tail.
   constexpr int IW = INTER && V == 1 ? 2 : V;         // dims of an interleaved chunk
   const int rot_chunks = INTER ? a.rot / IW : pairs / V;
   const int chunks = rot_chunks + (a.hd - a.rot) / V;
   const int per_row = (a.nq + a.nk) * chunks;
-  for (int i = threadIdx.x; i < nr * per_row; i += ROPE_THREADS) {
-    const int r = i / per_row, w = i - r * per_row;
-    int h = w / chunks;
-    const int c = w - h * chunks;
+  typedef Vec<T, V> VT;
+  VT early_x, early_y;
+  if (EARLY && threadIdx.x < per_row) {
+    int h = threadIdx.x / chunks;
+    const int c = threadIdx.x - h * chunks, d = c >= rot_chunks ? a.rot + (c - rot_chunks) * V : c * IW;
     const bool isk = h >= a.nq;
     if (isk) h -= a.nq;
-    const T *src = isk ? (const T *)a.k + (size_t)(r0 + r) * a.ks : (const T *)a.q + (size_t)(r0 + r) * a.qs;
-    T *dst = isk ? (T *)a.ko + (size_t)(r0 + r) * a.kos : (T *)a.qo + (size_t)(r0 + r) * a.qos;
+    const T *src = (isk ? (const T *)a.k + (size_t)row * a.ks : (const T *)a.q + (size_t)row * a.qs) + (size_t)h * a.hd + d;
+    early_x = *(const VT *)src;
+    if (!INTER && c < rot_chunks) early_y = *(const VT *)(src + pairs);
+  }
+  for (int p = threadIdx.x; p < pairs; p += ROPE_THREADS) {
+    float2 t = phase_cs((uint64_t)(int64_t)a.positions[row] * a.turn[p]);
+    t.x *= a.magnitude;
+    t.y *= a.transpose ? -a.magnitude : a.magnitude;
+    cs[p] = t;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < per_row; i += ROPE_THREADS) {
+    int h = i / chunks;
+    const int c = i - h * chunks;
+    const bool isk = h >= a.nq;
+    if (isk) h -= a.nq;
+    const T *src = isk ? (const T *)a.k + (size_t)row * a.ks : (const T *)a.q + (size_t)row * a.qs;
+    T *dst = isk ? (T *)a.ko + (size_t)row * a.kos : (T *)a.qo + (size_t)row * a.qos;
     src += (size_t)h * a.hd;
     dst += (size_t)h * a.hd;
-    const float2 *t = cs + r * pairs;
-    typedef Vec<T, V> VT;
+    const float2 *t = cs;
     if (c >= rot_chunks) {
       const int d = a.rot + (c - rot_chunks) * V;
-      if (src != dst) *(VT *)(dst + d) = *(const VT *)(src + d);
+      if (src != dst) *(VT *)(dst + d) = EARLY ? early_x : *(const VT *)(src + d);
     } else if (INTER) {
       const int d = c * IW;
       if constexpr (V == 1) {
@@ -95,7 +105,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
         dst[d] = from_f<T>(z.x);
         dst[d + 1] = from_f<T>(z.y);
       } else {
-        VT x = *(const VT *)(src + d);
+        VT x = EARLY ? early_x : *(const VT *)(src + d);
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
           const float2 z = turned(to_f(x.v[j]), to_f(x.v[j + 1]), t[(d + j) / 2]);
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
       }
     } else {
       const int d = c * V;
-      VT x = *(const VT *)(src + d), y = *(const VT *)(src + d + pairs);
+      VT x = EARLY ? early_x : *(const VT *)(src + d), y = EARLY ? early_y : *(const VT *)(src + d + pairs);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float2 z = turned(to_f(x.v[j]), to_f(y.v[j]), t[d + j]);
@@ -122,13 +132,13 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
 template <typename T>
 cudaError_t launch_rope(const RopeArgs &a, bool inter, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int rows_per_cta = 1;
-  const dim3 g((a.rows + rows_per_cta - 1) / rows_per_cta), b(ROPE_THREADS);
-  const size_t sm = (size_t)rows_per_cta * (a.rot / 2) * sizeof(float2);
-  if (vec) return inter ? launch_pdl(k_rope<T, V, true>, g, b, sm, s, a, rows_per_cta)
-                        : launch_pdl(k_rope<T, V, false>, g, b, sm, s, a, rows_per_cta);
-  return inter ? launch_pdl(k_rope<T, 1, true>, g, b, sm, s, a, rows_per_cta)
-               : launch_pdl(k_rope<T, 1, false>, g, b, sm, s, a, rows_per_cta);
+  const dim3 g(a.rows), b(ROPE_THREADS);
+  const size_t sm = (size_t)(a.rot / 2) * sizeof(float2);
+  const int chunks = (inter ? a.rot / V : a.rot / 2 / V) + (a.hd - a.rot) / V;
+  if (vec && (int64_t)(a.nq + a.nk) * chunks <= ROPE_THREADS)
+    return inter ? launch_pdl(k_rope<T, V, true, true>, g, b, sm, s, a) : launch_pdl(k_rope<T, V, false, true>, g, b, sm, s, a);
+  if (vec) return inter ? launch_pdl(k_rope<T, V, true, false>, g, b, sm, s, a) : launch_pdl(k_rope<T, V, false, false>, g, b, sm, s, a);
+  return inter ? launch_pdl(k_rope<T, 1, true, false>, g, b, sm, s, a) : launch_pdl(k_rope<T, 1, false, false>, g, b, sm, s, a);
 }
 
 }  // namespace dflash
