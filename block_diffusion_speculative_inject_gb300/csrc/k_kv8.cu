@@ -184,7 +184,10 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
 // shared tile, since its pages are transposed: a thread holds neighbouring tokens of its dims, so that
 // the tile is written in words of four tokens.
 //
-// Bound by latency for a few rows (scale, rows and slots are dependent loads) and by memory for many.
+// Bound by latency for a few rows (scale, rows and slots are dependent loads: 8 x 16 rows of 8 x 128 take 7.4 us)
+// and by instructions for many (8 x 4096 rows: 43.6 us, 4.6 TB/s), so the maximum is taken on pairs, bytes are
+// turned with permutes and a whole page of V is copied 16 bytes at a time (59.7 us without these). Six CTAs
+// per SM are asked for: 46.1 us with the five that 48 registers leave, 44.2 with eight, which spill.
 // The slots of a run are found by every warp for itself (a run whose slots rise by one, which is what a
 // plan makes, needs no barrier); only two barriers are left, around the CTA's maximum and V's tile.
 constexpr int KA_THREADS = 256;
@@ -386,25 +389,26 @@ __global__ void __launch_bounds__(KA_THREADS, 6) k_kv8_append(const AppendArgs<T
           const uint32_t *row = &tile[d * (KV_PAGE / 4)];
           *(uint4 *)(blk + 16 * t) = make_uint4(row[o ^ x], row[(o + 1) ^ x], row[(o + 2) ^ x], row[(o + 3) ^ x]);
         }
-      } else
+      } else {
 #pragma unroll 4
-      for (int t = tid; t < HD * (KV_PAGE / 4); t += KA_THREADS) {
-        const int d = t / (KV_PAGE / 4), o = t % (KV_PAGE / 4);
-        const uint32_t mo = (uint32_t)(owned >> (4 * o)) & 15, mk = (uint32_t)(kept >> (4 * o)) & 15;
-        if (!(mo | mk)) continue;
-        uint32_t *dst = (uint32_t *)(blk + 4 * t);
-        uint32_t x = tile[d * (KV_PAGE / 4) + (o ^ (d >> 3 & 15))];
-        if (mo != 15) {                               // keep or round anew the word's other bytes
-          const uint32_t was = *dst, re = mk ? rescale4(was, again) : was;
-          uint32_t bo = 0, bk = 0;
+        for (int t = tid; t < HD * (KV_PAGE / 4); t += KA_THREADS) {
+          const int d = t / (KV_PAGE / 4), o = t % (KV_PAGE / 4);
+          const uint32_t mo = (uint32_t)(owned >> (4 * o)) & 15, mk = (uint32_t)(kept >> (4 * o)) & 15;
+          if (!(mo | mk)) continue;
+          uint32_t *dst = (uint32_t *)(blk + 4 * t);
+          uint32_t x = tile[d * (KV_PAGE / 4) + (o ^ (d >> 3 & 15))];
+          if (mo != 15) {                               // keep or round anew the word's other bytes
+            const uint32_t was = *dst, re = mk ? rescale4(was, again) : was;
+            uint32_t bo = 0, bk = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            bo |= (mo >> j & 1) ? 0xffu << 8 * j : 0;
-            bk |= (mk >> j & 1) ? 0xffu << 8 * j : 0;
+            for (int j = 0; j < 4; ++j) {
+              bo |= (mo >> j & 1) ? 0xffu << 8 * j : 0;
+              bk |= (mk >> j & 1) ? 0xffu << 8 * j : 0;
+            }
+            x = (x & bo) | (re & bk) | (was & ~(bo | bk));
           }
-          x = (x & bo) | (re & bk) | (was & ~(bo | bk));
+          *dst = x;
         }
-        *dst = x;
       }
       __syncthreads();                                // the tile, s_max and owner are free again
     }

@@ -94,21 +94,20 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
     T *dst = isk ? (T *)a.ko + (size_t)row * a.kos : (T *)a.qo + (size_t)row * a.qos;
     src += (size_t)h * a.hd;
     dst += (size_t)h * a.hd;
-    const float2 *t = cs;
     if (c >= rot_chunks) {
       const int d = a.rot + (c - rot_chunks) * V;
       if (src != dst) *(VT *)(dst + d) = EARLY ? early_x : *(const VT *)(src + d);
     } else if (INTER) {
       const int d = c * IW;
       if constexpr (V == 1) {
-        const float2 z = turned(to_f(src[d]), to_f(src[d + 1]), t[c]);
+        const float2 z = turned(to_f(src[d]), to_f(src[d + 1]), cs[c]);
         dst[d] = from_f<T>(z.x);
         dst[d + 1] = from_f<T>(z.y);
       } else {
         VT x = EARLY ? early_x : *(const VT *)(src + d);
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
-          const float2 z = turned(to_f(x.v[j]), to_f(x.v[j + 1]), t[(d + j) / 2]);
+          const float2 z = turned(to_f(x.v[j]), to_f(x.v[j + 1]), cs[(d + j) / 2]);
           x.v[j] = from_f<T>(z.x);
           x.v[j + 1] = from_f<T>(z.y);
         }
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
       VT x = EARLY ? early_x : *(const VT *)(src + d), y = EARLY ? early_y : *(const VT *)(src + d + pairs);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float2 z = turned(to_f(x.v[j]), to_f(y.v[j]), t[d + j]);
+        const float2 z = turned(to_f(x.v[j]), to_f(y.v[j]), cs[d + j]);
         x.v[j] = from_f<T>(z.x);
         y.v[j] = from_f<T>(z.y);
       }
