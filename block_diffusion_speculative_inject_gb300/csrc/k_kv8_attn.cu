@@ -26,13 +26,15 @@ namespace dflash {
 constexpr int KM_WARPS = 8;
 constexpr int KM_THREADS = 32 * KM_WARPS;
 constexpr int KM_COST = 2;                             // what an item's start and end cost, in pages (64 requests
-                                                       // of one token: 98.6 us with 0, 95.5 with 2, 96.1 with 4)
+                                                       // of one token: 92.8 us with 0, 91.4 with 2, 92.0 with 4)
 constexpr float KM_BIAS = 14.f;                        // P's largest value is 2^14
 
 template <int HD>
 struct KmLayout {
   static constexpr int SLOT = KV_PAGE * HD;            // bytes of a K or V page of one head
-  static constexpr int SLOTS = HD == 128 ? 3 : 6;      // 24 KB per warp
+  // 16 KB per warp: a page of K and one of V under way. 64 requests of one token took 91.7 us, 96.8 with three
+  // slots (8 warps); with two, 93.1 with 6 warps and 95.0 with 12; 102.3 with 4 warps of four.
+  static constexpr int SLOTS = HD == 128 ? 2 : 4;
   static constexpr int RING = SLOT * SLOTS;
   static constexpr int SIDE = 4;                       // units whose page and scales are kept
   static constexpr size_t SMEM = 128 + (size_t)KM_WARPS * (RING + SLOTS * 8 + SIDE * 16);
@@ -568,7 +570,12 @@ extern "C" dflash_status dflash_kv8_attention(void *stream, const dflash_kv8_cac
   const cudaStream_t s = (cudaStream_t)stream;
   // Rows of a request and kv head, as far as the host knows: up to 8 go to the kernel for 8, up to 16 to the one
   // for 16, which reads the cache once where two tiles of 8 would read it twice. Above, bf16 goes to the tensor
-  // memory tiles; fp32 stays with 16 rows at a time.
+  // memory tiles; fp32 stays with 16 rows at a time. 8 requests x 8 kv heads of 128 over 32768 tokens, us:
+  //   rows       8      12      16      24      64
+  //   8 a go    88     124     124     244     455
+  //   16        90      92      94     147     325
+  //   tiles    121     121     121     122     133
+  // and over 2048 tokens 8 rows 14 / 15 / 23, 16 rows 18.5 / 17.7 / 23, 24 rows 22.7 / 22.0 / 23.4, 64 rows 42 / 32 / 25.
   const int64_t most = (int64_t)x->max_q * (x->n_q_heads / c->n_kv_heads);
   const bool wide = x->dtype == DFLASH_BF16;
   const int hd = c->head_dim;
