@@ -410,6 +410,16 @@ def test_attention_many_requests(n_q):
     _check_attn(c, table, q, cu, ctx, "none", tree, torch.bfloat16, max_q=n_q)
 
 
+@pytest.mark.parametrize("dtype,n_q", [(torch.bfloat16, 1), (torch.bfloat16, 6), (torch.bfloat16, 40), (torch.float32, 5)])
+@pytest.mark.parametrize("n", [2, 9, 61, 170])
+@pytest.mark.parametrize("mask", ["none", "causal"])
+def test_attention_cuts_between_short_and_long_items(dtype, n_q, n, mask):
+    """Items of one page among long ones: workers that get none of an item's pages, items that begin with the next one."""
+    ctx = [1 + 61 * i % 130 if i % 7 else 700 + 64 * i for i in range(n)]
+    c, table, q, cu, tree = _attn_case(n + n_q, ctx, [n_q - i % 2 for i in range(n)], 1, 64, 2, mask, dtype)
+    _check_attn(c, table, q, cu, ctx, mask, tree, dtype, max_q=n_q)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("n_q", [3, 40])
 def test_attention_nan_and_infinity_in_hidden_places(dtype, n_q):
