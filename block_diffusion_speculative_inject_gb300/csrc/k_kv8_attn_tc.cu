@@ -33,8 +33,9 @@
 // Code that runs once a piece is mostly fetched rather than run, so what is not a tile's inner work is
 // rolled up or shared: V widened a page at a time and one copy of the Q code took 8 trees of 256 from
 // 168 to 148 us. Measured, with the merge: 8 x 16 rows x 40 heads over 32768 tokens 135 us (537 MB, 4.0 TB/s),
-// the trees 146 us. A tile's softmax is the longest stage: 1600 cycles with two warps per SM partition,
-// where its arithmetic alone takes 840 and the MMAs 1030.
+// the trees 146 us, about 1800 cycles a tile of which the MMAs are 1030. What bounds it is tensor memory, which the
+// MMAs and the softmax use in turn: timed without exponentials, maxima, sums and the trade it still takes
+// 130 us, without the loads of S and the stores of P 114, with a quarter of the MMAs 112 (the copies alone: 90).
 #include "kv8_attn.cuh"
 
 namespace dflash {
