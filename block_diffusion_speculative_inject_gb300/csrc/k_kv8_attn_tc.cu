@@ -1,7 +1,7 @@
 // Attention over the 8-bit paged cache for many query rows per kv head (bf16): verify blocks, draft
 // trees, prompt chunks. One persistent CTA per SM walks its share of the work (kv8_sched.cuh) in tiles
 // of 128 rows (tokens x query heads of the kv head) and 128 tokens (two pages):
-//   S[128, 128] = Q . K^T        kind::f8f6f4, A = Q in tensor memory, B = the K pages as they are
+//   S[128, 128] = Q . K^T        kind::f8f6f4, both operands in shared memory, the K pages as they are
 //   P = 2^(S c + log2 s_v - m)   f16, written over S
 //   O[128, hd] += P . V          kind::f16, A = P in tensor memory, B = V pages widened to f16
 // Q's row, scaled by a power of two so that its largest entry is in [128, 256), is the sum of an e4m3 and
@@ -10,47 +10,45 @@
 // exact for entries of q down to 2^-14 of the row's largest (below, q is off by at most 2^-21 of it).
 // P could not go the same way: rows with one loud token and many quiet ones need its small values, so
 // P is f16 (11 bits, largest 2^7 .. 2^15, normal to 2^-14) and two warps widen V (exact) into a second
-// pair of tiles. That costs shared-memory traffic of 3x V's bytes per tile, 144 KB in all with the MMAs'
-// own reads, about 0.6 us at 128 B/clk against 0.74 us that an SM's share of HBM takes for the tile's 32 KB.
+// pair of tiles. That costs shared-memory traffic of 3x V's bytes per tile, 176 KB in all with the MMAs'
+// own reads, 1400 cycles at 128 B/clk against 1400 that an SM's share of HBM takes for the tile's 32 KB.
 //
 // The running maximum is lazy: O is rescaled only when a row's maximum grows by more than 2^8. The
 // pages' scales enter as in the few-row kernel: s_k in c, s_v in the exponent of P.
 //
-// Tensor memory (512 columns): S/P at 0 and 128 (tile parity), O at 256, Q at 384 and 448 (piece
-// parity: 32 columns of the e4m3 part, then 32 of the e5m2 part). P of a page's 64 tokens lies in the first 32
-// of their own 64 columns of S.
+// Tensor memory (512 columns): S/P at 0, 128 and 256 (tile modulo 3), O at 384. P of a page's 64 tokens lies in
+// the first 32 of their own 64 columns of S. With three buffers S of tile i + 2 need not wait for P.V of tile i;
+// with Q in tensor memory and two, the block below took 134 us and the trees 146.
 //
 // Roles (384 threads, 168 registers): warp 0 copies K (TMA, 128- or 64-byte swizzle) and V (bulk, as stored)
-// into rings of 4 tiles; warp 1 issues the MMAs, S of the next tile ahead of P.V of this one, across
-// piece borders; it runs converged, with the MMAs themselves predicated on one lane, which leaves the
-// descriptors to the uniform datapath (a lone lane took over twice as long to issue a tile as the
-// tensor cores take to do it). Warps 2-9 run the softmax, two threads per row, one page each: warps w
-// and w + 4 share the rows of lane quarter w % 4 and trade their maxima. They also load Q (of the next
-// piece, ahead) and write results, half of the dims each, by way of shared memory so that four lanes
-// handle a row. Warps 10-11 widen V. The copying warp, which is ahead of all, finds the pieces and leaves them in
-// a ring. All waits are bounded; rows whose wait ran out become NaN.
+// into rings of 3 tiles, is ahead of all, finds the pieces and leaves them in a ring. Warp 1 issues the MMAs, S
+// two tiles ahead of P.V within a piece; it runs converged, with the MMAs themselves predicated on one
+// lane, which leaves the descriptors to the uniform datapath (a lone lane took over twice as long to issue a
+// tile as the tensor cores take to do it). Warps 2-9 run the softmax, two threads per row, one page each:
+// warps w and w + 4 share the rows of lane quarter w % 4 and trade their maxima. They also load Q (of the
+// next piece as soon as S of this one's last tile is there) and write results, half of the dims each, in both
+// four lanes to a row. Warps 10-11 widen V. All waits are bounded; rows whose wait ran out become NaN.
 //
 // Code that runs once a piece is mostly fetched rather than run, so what is not a tile's inner work is
-// rolled up or shared: V widened a page at a time and one copy of the Q code took 8 trees of 256 from
-// 168 to 148 us. Measured, with the merge: 8 x 16 rows x 40 heads over 32768 tokens 135 us (537 MB, 4.0 TB/s),
-// the trees 146 us, about 1800 cycles a tile of which the MMAs are 1030. What bounds it is tensor memory, which the
-// MMAs and the softmax use in turn: timed without exponentials, maxima, sums and the trade it still takes
-// 130 us, without the loads of S and the stores of P 114, with a quarter of the MMAs 112 (the copies alone: 90).
+// rolled up: V widened a page at a time took the trees from 168 to 148 us. Measured, with the merge: 8 x 16
+// rows x 40 heads over 32768 tokens 126 us (537 MB, 4.3 TB/s), 8 trees of 256 rows x 32 heads over 1000 .. 5000
+// tokens 134 us; about 1700 cycles a tile, of which the MMAs are 1030. What bounds it is tensor memory, which the MMAs
+// and the softmax use in turn: without exponentials, maxima, sums and the trade the form with Q in tensor
+// memory still took 130 of its 134 us, without the loads of S and the stores of P 114.
 #include "kv8_attn.cuh"
 
 namespace dflash {
 
 constexpr int KT_TOKENS = 128;                         // tokens of a tile: two pages
-
 constexpr int KT_THREADS = 384;
-constexpr int KT_WIDEN = 64;                             // threads that widen V
-constexpr int KT_STAGES = 4;
-constexpr int KT_SIDE = 2 * KT_STAGES;                 // tiles whose page ids and scales are kept
-constexpr int KT_COST = 8;                             // what an item's start and end cost, in tiles (8 trees of
-                                                       // 256 over 1000 .. 5000 tokens: 163 us with 3, 147 with 6, 146 with 8)
+constexpr int KT_WIDEN = 64;                           // threads that widen V
+constexpr int KT_STAGES = 3;
+constexpr int KT_SIDE = 8;                             // tiles whose page ids and scales are kept
+constexpr int KT_COST = 8;                             // what an item's start and end cost, in tiles (the trees
+                                                       // above: 141 us with 4, 134 with 6 and with 8, 138 with 12)
 constexpr int KT_RING = 16;                            // pieces kept: the one found last is at most 7 ahead of the one written
 constexpr float KT_BIAS = 7.f;
-constexpr uint32_t TM_O = 256, TM_Q = 384;
+constexpr uint32_t TM_O = 384;
 
 struct KtParams {
   CUtensorMap kmap;
@@ -62,7 +60,8 @@ struct KtLayout {
   static constexpr uint32_t PAGE8 = KV_PAGE * HD;      // a K or V page, 8 bits
   static constexpr uint32_t PAGE16 = KV_PAGE * HD * 2; // a V page in f16
   static constexpr uint32_t K0 = 0, V0 = K0 + KT_STAGES * 2 * PAGE8, W0 = V0 + KT_STAGES * 2 * PAGE8;
-  static constexpr uint32_t OUT0 = W0 + 2 * 2 * PAGE16, END = OUT0 + 8 * 2048;   // per softmax warp 32 rows x 64 bytes of results
+  static constexpr uint32_t PLANE = 128 * HD;          // Q's e4m3 part; the e5m2 part follows
+  static constexpr uint32_t Q0 = W0 + 2 * 2 * PAGE16, OUT0 = Q0 + 2 * PLANE, END = OUT0 + 8 * 2048;   // per softmax warp 32 rows x 64 bytes of results
 };
 
 struct KtSide {
@@ -72,7 +71,7 @@ struct KtSide {
 
 struct KtShared {
   uint64_t kfull[KT_STAGES], kempty[KT_STAGES], vfull[KT_STAGES], vempty[KT_STAGES];
-  uint64_t s_full[2], p_full[2], w_full[2], pv_done[2], q_full[2], o_full, o_empty, drain[1];
+  uint64_t s_full[3], p_full[3], w_full[2], pv_done[2], q_full, o_full, o_empty, drain[1];
   uint64_t x_ready[2][4];                              // maxima traded: per tile parity and lane quarter
   uint64_t l_ready[2][2][4];                           // row sums: per piece parity, half and lane quarter
   KtSide side[KT_SIDE];
@@ -96,9 +95,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(c2), "r"(mbar) : "memory");
 }
 // MMAs and commits of the one thread with `lead` set; the whole warp runs them. hi: the descriptors' upper word
-__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 b, {%2, %3};\n"
-               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi),
+__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n}\n" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi),
                "r"(idesc), "r"(acc), "r"(lead) : "memory");
 }
 __device__ __forceinline__ void mma_f16(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
@@ -117,10 +116,6 @@ __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
 // D fp32, M = 128, N columns; A and B formats as the kind numbers them
 constexpr uint32_t idesc_of(int a_fmt, int b_fmt, int N) {
   return (1u << 4) | (uint32_t)a_fmt << 7 | (uint32_t)b_fmt << 10 | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 // 32 columns of this thread's lane, without the wait
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
@@ -147,6 +142,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t *w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
@@ -170,17 +168,19 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       mbar_init(bar(sh.vempty[i]), KT_WIDEN / 32);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(sh.s_full[i]), 2);                 // the MMAs, and their issuer for the side words that it has seen
-      mbar_init(bar(sh.p_full[i]), 8);
       mbar_init(bar(sh.w_full[i]), KT_WIDEN / 32);
       mbar_init(bar(sh.pv_done[i]), 1);
-      mbar_init(bar(sh.q_full[i]), 8);
       for (int j = 0; j < 4; ++j) {
         mbar_init(bar(sh.x_ready[i][j]), 2);
         mbar_init(bar(sh.l_ready[i][0][j]), 1);
         mbar_init(bar(sh.l_ready[i][1][j]), 1);
       }
     }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(bar(sh.s_full[i]), 2);                 // the MMAs, and their issuer for the side words that it has seen
+      mbar_init(bar(sh.p_full[i]), 8);
+    }
+    mbar_init(bar(sh.q_full), 8);
     for (int i = 0; i < KT_RING; ++i) mbar_init(bar(sh.known[i]), 1);
     mbar_init(bar(sh.o_full), 1);
     mbar_init(bar(sh.drain[0]), 1);
@@ -309,54 +309,45 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     auto wait_all = [&](uint64_t &b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
     const uint64_t k0 = HD == 128 ? sw128_desc(base + Lay::K0) : sw64_desc(base + Lay::K0), w0 = sw128_desc(base + Lay::W0);
     const uint32_t k_hi = (uint32_t)(k0 >> 32), w_hi = (uint32_t)(w0 >> 32);
-    int s_left = pc.u1 - pc.u0;                        // tiles without S of the piece whose S is issued next
-    uint32_t si = 0, spn = 0;                          // tile and piece ordinals of S
-    bool new_q = true, more = true;
+    const uint32_t qd = (uint32_t)k0 + ((Lay::Q0 - Lay::K0) >> 4);
+    uint32_t si = 0;                                   // tiles whose S is issued
     auto issue_s = [&]() {
-      if (new_q && !wait_all(sh.q_full[spn & 1], spn >> 1)) return false;
-      new_q = false;
-      const uint32_t stg = si % KT_STAGES, par = si & 1;
+      const uint32_t stg = si % KT_STAGES, sb = si % 3;
       if (!wait_all(sh.kfull[stg], si / KT_STAGES)) return false;
       tc_fence_after();
-      const uint32_t kd = (uint32_t)k0 + stg * (2 * Lay::PAGE8 >> 4), d = tmem + par * 128, q = tmem + TM_Q + (spn & 1) * 64;
+      const uint32_t kd = (uint32_t)k0 + stg * (2 * Lay::PAGE8 >> 4), d = tmem + sb * 128;
 #pragma unroll
       for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
-        for (int k = 0; k < HD / 32; ++k) mma_f8(lead, d, q + 32 * pl + 8 * k, kd + 2 * k, k_hi, pl ? idS1 : idS0, (pl | k) ? 1u : 0u);
-      commit_lead(lead, bar(sh.s_full[par]));
+        for (int k = 0; k < HD / 32; ++k)
+          mma_f8(lead, d, qd + pl * (Lay::PLANE >> 4) + 2 * k, kd + 2 * k, k_hi, pl ? idS1 : idS0, (pl | k) ? 1u : 0u);
+      commit_lead(lead, bar(sh.s_full[sb]));
       commit_lead(lead, bar(sh.kempty[stg]));
-      if (lead) mbar_arrive(bar(sh.s_full[par]));
+      if (lead) mbar_arrive(bar(sh.s_full[sb]));
       ++si;
-      if (--s_left == 0) {
-        more = sh.ring[spn % KT_RING].left > 0;
-        if (more) {
-          ++spn;
-          if (!known(spn)) return false;
-          s_left = sh.ring[spn % KT_RING].u1 - sh.ring[spn % KT_RING].u0;
-          new_q = true;
-        }
-      }
       return true;
     };
-    bool go = known(0) && issue_s();
+    bool go = true;
     uint32_t i = 0;
     for (uint32_t pn = 0; go; ++pn) {
-      if (!(go = known(pn))) break;
+      if (!(go = known(pn) && wait_all(sh.q_full, pn))) break;
       const Kv8Piece &now = sh.ring[pn % KT_RING];
       const int n = now.u1 - now.u0;
-      for (int x = 0; x < n; ++x, ++i) {
-        if (more && !(go = issue_s())) break;
-        const uint32_t par = i & 1;
+      for (int x = -2; x < n; ++x) {                   // S two tiles ahead of P.V, within the piece
+        if (x + 2 < n && !(go = issue_s())) break;
+        if (x < 0) continue;
+        const uint32_t par = i & 1, sb = i % 3;
         if (!(go = wait_all(sh.w_full[par], i >> 1))) break;
         if (x == 0 && pn > 0 && !(go = wait_all(sh.o_empty, pn - 1))) break;
-        if (!(go = wait_all(sh.p_full[par], i >> 1))) break;
+        if (!(go = wait_all(sh.p_full[sb], i / 3))) break;
         tc_fence_after();
-        const uint32_t wd = (uint32_t)w0 + par * (2 * Lay::PAGE16 >> 4), pa = tmem + par * 128;
+        const uint32_t wd = (uint32_t)w0 + par * (2 * Lay::PAGE16 >> 4), pa = tmem + sb * 128;
 #pragma unroll
         for (int k = 0; k < 8; ++k)                    // 16 tokens each; k >> 2: the page
           mma_f16(lead, tmem + TM_O, pa + 64 * (k >> 2) + 8 * (k & 3), wd + (k >> 2) * (Lay::PAGE16 >> 4) + (k & 3) * 2, w_hi, idO,
                   k ? 1u : (uint32_t)(x > 0));
         commit_lead(lead, bar(sh.pv_done[par]));
+        ++i;
       }
       if (!go) break;
       commit_lead(lead, bar(sh.o_full));
@@ -376,91 +367,72 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     bool ok = true;
     // writes this half of the dims of Q of a piece; returns the row's factor (NaN: the row holds
     // an infinity or NaN)
-    auto load_q = [&](const Kv8Piece &x, uint32_t pn) {
+    auto load_q = [&](const Kv8Piece &x) {
       const int tk = x.qt * tpt + r / group;
       const unsigned alive = __ballot_sync(0xffffffffu, r < tpt * group && tk < x.r.n);
       constexpr int N = HD / 2, R = N / 32;            // dims of a half, rounds of 64 bytes of each row
       const int64_t from = (int64_t)(x.r.row0 + tk) * a.q_stride + (int64_t)(x.h * group + r % group) * HD;
-      // Four lanes read a row, 16 bytes each: this half of 8 rows at a time into shared memory, the other
-      // half for the row's maximum only.
-      uint4 w[N / 8];
-      float t0 = 0.f, t1 = 0.f;                        // largest magnitudes of the row's even and odd dims; NaN stays
-      uint4 mine[R][4], other[R][4];
+      // Four lanes read a row, 16 bytes each: this half of 8 rows at a time, the other half for the row's
+      // maximum only.
+      float factor = NAN;
+#pragma unroll 1
+      for (int k0 = 0; k0 < 4; k0 += 2) {
+        uint4 mine[R][2], other[R][2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int y = 8 * k + (lane >> 2);
-        const bf16 *src = (const bf16 *)a.q + __shfl_sync(0xffffffffu, from, y) + 8 * (lane & 3);
-        const bool there = alive >> y & 1;
+        for (int k = 0; k < 2; ++k) {
+          const int y = 8 * (k0 + k) + (lane >> 2);
+          const bf16 *src = (const bf16 *)a.q + __shfl_sync(0xffffffffu, from, y) + 8 * (lane & 3);
+          const bool there = alive >> y & 1;
 #pragma unroll
-        for (int z = 0; z < R; ++z) {
-          mine[z][k] = there ? *(const uint4 *)(src + N * half + 32 * z) : make_uint4(0, 0, 0, 0);
-          other[z][k] = there ? *(const uint4 *)(src + N * (half ^ 1) + 32 * z) : make_uint4(0, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t top = 0;
-        auto take = [&](uint32_t e) {
-          const __nv_bfloat162 m = __hmax2_nan(*(const __nv_bfloat162 *)&top, __habs2(*(const __nv_bfloat162 *)&e));
-          top = *(const uint32_t *)&m;
-        };
-#pragma unroll
-        for (int z = 0; z < R; ++z) {
-          take(mine[z][k].x), take(mine[z][k].y), take(mine[z][k].z), take(mine[z][k].w);
-          take(other[z][k].x), take(other[z][k].y), take(other[z][k].z), take(other[z][k].w);
-        }
-        take(__shfl_xor_sync(0xffffffffu, top, 1));
-        take(__shfl_xor_sync(0xffffffffu, top, 2));
-        top = __shfl_sync(0xffffffffu, top, 4 * (lane & 7));       // of row 8 k + lane % 8
-        if (lane >> 3 == k) {
-          t0 = __uint_as_float(top << 16);
-          t1 = __uint_as_float(top & 0xffff0000u);
-        }
-      }
-      const uint32_t stage = base + Lay::OUT0 + (warp - 2) * 2048;
-#pragma unroll
-      for (int z = 0; z < R; ++z) {
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int y = 8 * k + (lane >> 2);
-          sts128(stage + 64 * y + 16 * ((lane & 3) ^ (y >> 1 & 3)), (const uint32_t *)&mine[z][k]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[4 * z + c] = lds128(stage + 64 * lane + 16 * (c ^ (lane >> 1 & 3)));
-      }
-      const bool fin = t0 <= 3.402823466e38f && t1 <= 3.402823466e38f;
-      const float big = fmaxf(t0, t1);
-      const int e = fin ? max(-100, (int)(__float_as_uint(big) >> 23) - 127) : 0;
-      const float up = __uint_as_float((uint32_t)(134 - e) << 23);             // 2^(7 - e)
-      const uint32_t keep = fin ? ~0u : 0u;
-      const uint32_t dst = lane_base + TM_Q + (pn & 1) * 64 + half * (N / 4);
-#pragma unroll
-      for (int c = 0; c < N / 4; c += 8) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 &b = w[(c + j) / 2];
-          uint32_t h[2], l[2];
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {                // f16 holds the scaled value and the difference exactly
-            const uint32_t e = (j & 1 ? (z ? b.w : b.z) : (z ? b.y : b.x)) & keep;
-            const uint32_t y = pack_f16(__uint_as_float(e << 16) * up, __uint_as_float(e & 0xffff0000u) * up);
-            h[z] = f16x2_to_e4m3x2(y);
-            l[z] = f16x2_to_e5m2x2(sub_f16x2(y, e4m3x2_to_f16x2(h[z])));
+          for (int z = 0; z < R; ++z) {
+            mine[z][k] = there ? *(const uint4 *)(src + N * half + 32 * z) : make_uint4(0, 0, 0, 0);
+            other[z][k] = there ? *(const uint4 *)(src + N * (half ^ 1) + 32 * z) : make_uint4(0, 0, 0, 0);
           }
-          hi[j] = h[0] | h[1] << 16;
-          lo[j] = l[0] | l[1] << 16;
         }
-        tmem_st8(dst + c, hi);
-        tmem_st8(dst + 32 + c, lo);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t top = 0;                            // largest magnitudes of the row's even and odd dims; NaN stays
+          auto take = [&](uint32_t e) {
+            const __nv_bfloat162 m = __hmax2_nan(*(const __nv_bfloat162 *)&top, __habs2(*(const __nv_bfloat162 *)&e));
+            top = *(const uint32_t *)&m;
+          };
+#pragma unroll
+          for (int z = 0; z < R; ++z) {
+            take(mine[z][k].x), take(mine[z][k].y), take(mine[z][k].z), take(mine[z][k].w);
+            take(other[z][k].x), take(other[z][k].y), take(other[z][k].z), take(other[z][k].w);
+          }
+          take(__shfl_xor_sync(0xffffffffu, top, 1));
+          take(__shfl_xor_sync(0xffffffffu, top, 2));
+          const float t0 = __uint_as_float(top << 16), t1 = __uint_as_float(top & 0xffff0000u);
+          const bool fin = t0 <= 3.402823466e38f && t1 <= 3.402823466e38f;
+          const int e = fin ? max(-100, (int)(__float_as_uint(fmaxf(t0, t1)) >> 23) - 127) : 0;
+          const float up = __uint_as_float((uint32_t)(134 - e) << 23);           // 2^(7 - e)
+          const uint32_t keep = fin ? ~0u : 0u;
+          const int y = q * 32 + 8 * (k0 + k) + (lane >> 2), swz = HD == 128 ? y & 7 : y >> 1 & 3;
+#pragma unroll
+          for (int z = 0; z < R; ++z) {
+            const uint32_t w[4] = {mine[z][k].x, mine[z][k].y, mine[z][k].z, mine[z][k].w};
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {              // f16 holds the scaled value and the difference exactly
+              const uint32_t v = w[j] & keep, x16 = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+              h[j] = f16x2_to_e4m3x2(x16);
+              l[j] = f16x2_to_e5m2x2(sub_f16x2(x16, e4m3x2_to_f16x2(h[j])));
+            }
+            const int c = (N * half + 32 * z) / 16 + (lane >> 1 & 1);          // 16-byte chunk of the row
+            const uint32_t dst = base + Lay::Q0 + y * HD + 16 * (c ^ swz) + 8 * (lane & 1);
+            sts64(dst, h[0] | h[1] << 16, h[2] | h[3] << 16);
+            sts64(dst + Lay::PLANE, l[0] | l[1] << 16, l[2] | l[3] << 16);
+          }
+          const float f = fin ? a.scale * 1.44269504088896341f * __uint_as_float((uint32_t)(120 + e) << 23) : NAN;
+          const float own = __shfl_sync(0xffffffffu, f, 4 * (lane & 7));         // of row 8 k + lane % 8
+          if (lane >> 3 == k0 + k) factor = own;
+        }
       }
-      tmem_st_wait();
-      tc_fence_before();
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh.q_full[pn & 1]));
-      return fin ? a.scale * 1.44269504088896341f * __uint_as_float((uint32_t)(120 + e) << 23) : NAN;
+      if (lane == 0) mbar_arrive(bar(sh.q_full));
+      return factor;
     };
     Kv8Piece &mine = sh.piece[warp - 2];
     auto keep = [&](const Kv8Piece &x) {
@@ -469,15 +441,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       __syncwarp();
     };
     keep(pc);
-    uint32_t i = 0, pn = 0, qn = 0;                    // tile and piece ordinals, the piece whose Q is next
-    float rs = 0.f, rs_next = 0.f;
+    uint32_t i = 0, pn = 0;                            // tile and piece ordinals
+    float rs_next = load_q(pc);
     bool first = true;
     for (;; ++pn) {
-#pragma unroll 1
-      for (; qn <= pn + 1; ++qn) {                     // at first its own Q, then the next piece's
-        rs = rs_next;
-        if ((qn == 0 || mine.left > 0) && known(qn)) rs_next = load_q(sh.ring[qn % KT_RING], qn);
-      }
+      const float rs = rs_next;
       const int tk = mine.qt * tpt + r / group;
       const bool live = r < tpt * group && tk < mine.r.n;
       const bool quiet = !__any_sync(0xffffffffu, live);       // no row of this warp: only the barriers
@@ -487,10 +455,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       const float fac = live && rs == rs ? rs : 0.f;
       float m_used = -INFINITY, l = 0.f;
       for (int u = u0; u < u1; ++u, ++i) {
-        const int par = i & 1;
-        ok = __all_sync(0xffffffffu, ok && wait(sh.s_full[par], i >> 1));
+        const int par = i & 1, sb = i % 3;
+        ok = __all_sync(0xffffffffu, ok && wait(sh.s_full[sb], i / 3));
         if (!ok) break;
-        const uint32_t sa = lane_base + par * 128 + half * 64;   // my 64 tokens
+        const uint32_t sa = lane_base + sb * 128 + half * 64;    // my 64 tokens
         const KtSide &sd = sh.side[i % KT_SIDE];
         const float c = fac * sd.ks[half], ev = sd.ev[half];
         const bool partial = sd.page[half] < 0 || 2 * u + half >= open;
@@ -586,8 +554,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.p_full[par]));
+        if (lane == 0) mbar_arrive(bar(sh.p_full[sb]));
       }
+      // the next piece's Q: this one's products are done with it, as its last S is there
+      if (mine.left > 0 && known(pn + 1)) rs_next = load_q(sh.ring[(pn + 1) % KT_RING]);
       // the row's sum over both halves (by piece parity: the other warp may be a piece ahead)
       const Kv8Piece pc = mine;
       float l_row = 0.f;
