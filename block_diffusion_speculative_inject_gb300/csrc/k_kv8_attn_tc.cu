@@ -32,9 +32,9 @@
 // Code that runs once a piece is mostly fetched rather than run, so what is not a tile's inner work is
 // rolled up: V widened a page at a time took the trees from 168 to 148 us. Measured, with the merge: 8 x 16
 // rows x 40 heads over 32768 tokens 126 us (537 MB, 4.3 TB/s), 8 trees of 256 rows x 32 heads over 1000 .. 5000
-// tokens 134 us; about 1700 cycles a tile, of which the MMAs are 1030. What bounds it is tensor memory, which the MMAs
-// and the softmax use in turn: without exponentials, maxima, sums and the trade the form with Q in tensor
-// memory still took 130 of its 134 us, without the loads of S and the stores of P 114.
+// tokens 134 us; about 1700 cycles a tile, of which the MMAs are 1030 and the softmax's arithmetic 840. No one part
+// bounds it: the block takes 116 us without the trade of maxima, 119 without exponentials or without the widening,
+// 120 and 123 with a quarter of the products of S and of P.V, 103 without loads of S and stores of P.
 #include "kv8_attn.cuh"
 
 namespace dflash {
