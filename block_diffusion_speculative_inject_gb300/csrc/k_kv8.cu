@@ -184,10 +184,11 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
 // shared tile, since its pages are transposed: a thread holds neighbouring tokens of its dims, so that
 // the tile is written in words of four tokens.
 //
-// Bound by latency for a few rows (scale, rows and slots are dependent loads: 8 x 16 rows of 8 x 128 take 7.4 us)
-// and by instructions for many (8 x 4096 rows: 43.6 us, 4.6 TB/s), so the maximum is taken on pairs, bytes are
+// Bound by latency for a few rows (scale, rows and slots are dependent loads: 8 x 16 rows of 8 x 128 take 7.7 us)
+// and by instructions for many (8 x 4096 rows: 42.0 us, 4.8 TB/s), so the maximum is taken on pairs, bytes are
 // turned with permutes and a whole page of V is copied 16 bytes at a time (59.7 us without these). Six CTAs
-// per SM are asked for: 46.1 us with the five that 48 registers leave, 44.2 with eight, which spill.
+// per SM are asked for (44.5 us with five). A warp looks for a window's next run in 64 slots at once: row by
+// row, 7849 rows of 4 x 128 took 34.8 us, now 16.2.
 // The slots of a run are found by every warp for itself (a run whose slots rise by one, which is what a
 // plan makes, needs no barrier); only two barriers are left, around the CTA's maximum and V's tile.
 constexpr int KA_THREADS = 256;
@@ -262,16 +263,23 @@ __global__ void __launch_bounds__(KA_THREADS, 6) k_kv8_append(const AppendArgs<T
     return s < n_slots && s >= 0 ? s : -1;
   };
   const int w0 = blockIdx.x * a.window, w1 = min(w0 + a.window, a.rows);
-  int i = w0;
-  while (i < w1) {                                    // uniform: all threads read the same slots
-    const int64_t s0 = slot_of(i), before = slot_of(i - 1);
-    const int page = (int)(s0 / KV_PAGE);
-    if (s0 < 0 || (before >= 0 && (int)(before / KV_PAGE) == page)) {   // skipped, or of a run begun before
-      ++i;
-      continue;
-    }
+  auto page_of = [&](int64_t x) { return x < 0 ? -1 : (int)(x / KV_PAGE); };
+  for (int i = w0; i < w1;) {                         // uniform: all warps read the same slots
     // the run: slots s0, s0 + 1, .. as a rule
     const int64_t s1 = slot_of(i + lane), s2 = slot_of(i + 32 + lane);
+    const int before = page_of(slot_of(i - 1));
+    const int64_t s0 = __shfl_sync(0xffffffffu, s1, 0);
+    const int page = page_of(s0);
+    if (page < 0 || page == before) {                 // skipped, or of a run begun before: on to the row that begins one
+      const int p1 = page_of(s1), p2 = page_of(s2), last = __shfl_sync(0xffffffffu, p1, 31);
+      int b1 = __shfl_up_sync(0xffffffffu, p1, 1), b2 = __shfl_up_sync(0xffffffffu, p2, 1);
+      if (lane == 0) b1 = before, b2 = last;
+      const uint64_t begins = (uint64_t)__ballot_sync(0xffffffffu, p2 >= 0 && p2 != b2) << 32 |
+                              __ballot_sync(0xffffffffu, p1 >= 0 && p1 != b1);
+      if (!begins) break;                             // (a window has 64 rows at most)
+      i += __ffsll((long long)begins) - 1;
+      continue;
+    }
     const uint64_t rising = (uint64_t)__ballot_sync(0xffffffffu, s2 == s0 + 32 + lane && s2 / KV_PAGE == page) << 32 |
                             __ballot_sync(0xffffffffu, s1 == s0 + lane && s1 / KV_PAGE == page);
     const int first = (int)(s0 % KV_PAGE), len = ~rising ? __ffsll(~rising) - 1 : 64;
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(KA_THREADS, 6) k_kv8_append(const AppendArgs<T
       }
       __syncthreads();                                // the tile, s_max and owner are free again
     }
-    i = min(end, w1);
+    i = end;
   }
 }
 
@@ -422,9 +430,10 @@ cudaError_t launch_append(const dflash_kv8_cache *c, int rows, const void *k, in
   AppendArgs<T> a{rows, 1, c->n_kv_heads, c->n_pages, (const T *)k, (const T *)v, ks, vs, slot,
                   (uint8_t *)c->k_pages, (uint8_t *)c->v_pages, c->k_scale, c->v_scale};
   // Rows of a window: one, so that every row of a few may start a page of its own at once, up to a
-  // page's worth when there are CTAs enough for about two waves of 8 per SM without.
+  // page's worth when that leaves CTAs enough for 8 per SM (half of it, for twice as many: 11.8 against 9.8 us at 33 x 8
+  // rows of 8 x 128, 8.4 against 5.9 us at 29 x 48 .. 96 of 1 x 64, 13.4 against 16.7 at 7849 rows of 4 x 128).
   const long ctas = (long)rows * c->n_kv_heads * 2;
-  a.window = (int)(ctas / (KV8_CTAS * 2));
+  a.window = (int)(ctas / KV8_CTAS);
   a.window = a.window < 1 ? 1 : a.window > KV_PAGE ? KV_PAGE : a.window;
   const dim3 g((rows + a.window - 1) / a.window, c->n_kv_heads, 2), b(KA_THREADS);
   return c->head_dim == 128 ? launch_pdl(k_kv8_append<T, 128>, g, b, 0, s, a)

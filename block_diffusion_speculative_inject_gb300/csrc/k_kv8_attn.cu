@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
 #pragma unroll 1
     for (int u = pc.u0; u < pc.u1; ++u) {
       const uint8_t *kslot = wait();
-      asm volatile("cp.async.wait_group %0;" ::"n"(Lay::SLOTS / 2 - (Lay::SLOTS == 3 ? 0 : 1)) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(Lay::SLOTS / 2 - 1) : "memory");
       __syncwarp();
       const Side sd = side[take / 2 % Lay::SIDE];
       if (!ok) break;

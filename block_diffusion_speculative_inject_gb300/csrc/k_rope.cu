@@ -50,8 +50,8 @@ struct alignas(N * sizeof(T)) Vec {
   T v[N];
 };
 
-// A CTA turns one row; V elements per access (16 bytes, or one element where a row, a head or the
-// rotated part does not keep 16-byte alignment). EARLY: for rows of one chunk per thread, whose loads are then on
+// A CTA turns one row; V elements per access (16 or 8 bytes, or two elements or one where a row, a
+// head or the rotated part does not keep the alignment). EARLY: for rows of one chunk per thread, whose loads are then on
 // their way while the angles are made (5003 rows of 16 x 64 fp32: 10.1 against 13.7 us). Longer rows have more
 // loads after the first, and the registers held across the barrier cost them more (32768 rows of 48 x 128 bf16: 152
 // against 123 us, 6.5 TB/s).
@@ -128,16 +128,21 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
   }
 }
 
-template <typename T>
-cudaError_t launch_rope(const RopeArgs &a, bool inter, bool vec, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(T);
+template <typename T, int V, bool EARLY>
+cudaError_t launch_rope(const RopeArgs &a, bool inter, cudaStream_t s) {
   const dim3 g(a.rows), b(ROPE_THREADS);
   const size_t sm = (size_t)(a.rot / 2) * sizeof(float2);
+  return inter ? launch_pdl(k_rope<T, V, true, EARLY>, g, b, sm, s, a) : launch_pdl(k_rope<T, V, false, EARLY>, g, b, sm, s, a);
+}
+// width: elements that every access may take at once
+template <typename T>
+cudaError_t launch_rope(const RopeArgs &a, bool inter, int width, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
   const int chunks = (inter ? a.rot / V : a.rot / 2 / V) + (a.hd - a.rot) / V;
-  if (vec && (int64_t)(a.nq + a.nk) * chunks <= ROPE_THREADS)
-    return inter ? launch_pdl(k_rope<T, V, true, true>, g, b, sm, s, a) : launch_pdl(k_rope<T, V, false, true>, g, b, sm, s, a);
-  if (vec) return inter ? launch_pdl(k_rope<T, V, true, false>, g, b, sm, s, a) : launch_pdl(k_rope<T, V, false, false>, g, b, sm, s, a);
-  return inter ? launch_pdl(k_rope<T, 1, true, false>, g, b, sm, s, a) : launch_pdl(k_rope<T, 1, false, false>, g, b, sm, s, a);
+  if (width == V && (int64_t)(a.nq + a.nk) * chunks <= ROPE_THREADS) return launch_rope<T, V, true>(a, inter, s);
+  if (width == V) return launch_rope<T, V, false>(a, inter, s);
+  if (width == V / 2) return launch_rope<T, V / 2, false>(a, inter, s);
+  return width == 2 ? launch_rope<T, 2, false>(a, inter, s) : launch_rope<T, 1, false>(a, inter, s);
 }
 
 }  // namespace dflash
@@ -215,13 +220,17 @@ extern "C" dflash_status dflash_rope_apply(void *stream, const dflash_rope *rope
   a.ks = k_stride;
   a.qos = q_out_stride;
   a.kos = k_out_stride;
-  // 16-byte accesses need every row, every head and both rotated halves on 16 bytes
-  const int V = 16 / es;
-  bool vec = aligned(q, 16) && aligned(q_out, 16) && q_stride % V == 0 && q_out_stride % V == 0 && head_dim % V == 0 &&
-             a.rot % (rope->interleaved ? V : 2 * V) == 0;
-  if (nk) vec = vec && aligned(k, 16) && aligned(k_out, 16) && k_stride % V == 0 && k_out_stride % V == 0;
+  // Wide accesses need every row, every head and both rotated halves on their boundary: 16 bytes, else 8, else
+  // two elements, else one (33870 rows of 18 x 64 bf16, 20 dims rotated: 66 us by four, 94 by two, 124 by one).
+  auto fits = [&](int n) {
+    bool y = aligned(q, n * es) && aligned(q_out, n * es) && q_stride % n == 0 && q_out_stride % n == 0 && head_dim % n == 0 &&
+             a.rot % (rope->interleaved ? n : 2 * n) == 0;
+    if (nk) y = y && aligned(k, n * es) && aligned(k_out, n * es) && k_stride % n == 0 && k_out_stride % n == 0;
+    return y;
+  };
+  const int V = 16 / es, width = fits(V) ? V : fits(V / 2) ? V / 2 : fits(2) ? 2 : 1;
   const cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = dtype == DFLASH_BF16 ? launch_rope<bf16>(a, rope->interleaved, vec, st)
-                                             : launch_rope<float>(a, rope->interleaved, vec, st);
+  const cudaError_t e = dtype == DFLASH_BF16 ? launch_rope<bf16>(a, rope->interleaved, width, st)
+                                             : launch_rope<float>(a, rope->interleaved, width, st);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }

@@ -256,6 +256,32 @@ def test_append_long_runs_and_windows():
     _same_cache(gpu, want)
 
 
+@pytest.mark.parametrize("hd,dtype", [(64, torch.bfloat16), (128, torch.float32)])
+@pytest.mark.parametrize("gap", [0, 5, 70, 300])
+def test_append_short_runs_in_wide_windows(hd, dtype, gap):
+    """Runs of 1 to 5 rows, and whole pages with rows out of order, between stretches of skipped rows: windows that
+    begin inside a run, inside a stretch, or hold none or many."""
+    from block_diffusion_speculative_inject_gb300 import kv8_append
+    n_pages, nkv = 400, 8
+    g = torch.Generator().manual_seed(gap + hd)
+    slots = []
+    for p in torch.randperm(n_pages, generator=g).tolist():
+        if len(slots) > 9000:
+            break
+        if p % 50 == 7:
+            slots += [p * PAGE + o for o in torch.randint(0, PAGE, (90,), generator=g).tolist()]
+        else:
+            n, o = 1 + p % 5, int(torch.randint(0, PAGE - 5, (1,), generator=g))
+            slots += [p * PAGE + o + i for i in range(n)]
+        slots += [-1] * int(torch.randint(0, gap + 1, (1,), generator=g))
+    k, v = (torch.randn((len(slots), nkv, hd), generator=g).to(dtype) for _ in range(2))
+    want = _cache_cpu(2, n_pages, nkv, hd)
+    gpu = _to_gpu(want)
+    kv8_append(gpu, k.cuda(), v.cuda(), torch.tensor(slots, device="cuda"))
+    R.append(want, k, v, slots)
+    _same_cache(gpu, want)
+
+
 def test_append_special_values():
     """Zeros (scale 2^-64), infinities (saturate, no say in the scale), NaN (kept), the largest and smallest
     fp32 values, amax on and just above a scale's edge; the last of two rows with one slot stays."""
