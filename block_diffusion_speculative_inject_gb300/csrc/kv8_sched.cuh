@@ -3,17 +3,22 @@
 // An item is (request, tile of query tokens, kv head); its units are the U-token stretches of the
 // context that its rows may see. All items, in the order requests > tiles > heads, each as C + its units
 // long (C: what its start and end cost a worker), form one line that is cut into equal chunks, one per
-// worker; a worker thus owns at most two pieces of items that others also work on (its
-// first and its last), whose partial results go to the workspace and are merged by k_kv8_combine. An item
-// whose first C fall to a worker without any of its units begins with the next worker. Every worker finds its
-// start by itself from the lengths on the GPU: lengths of 32 requests are summed by a warp, the sums of those
-// groups sit in shared memory, and the lengths inside a request have a closed form.
+// worker (longer ones where an item would fall into too many pieces). A worker thus owns at most two pieces
+// of items that others also work on (its first and its last), whose partial results go to the workspace
+// and are merged by k_kv8_combine. An item whose first C fall to a worker without any of its units begins
+// with the next worker. Every worker finds its start by itself from the lengths on the GPU: lengths of 32
+// requests are summed by a warp, the sums of those groups sit in shared memory, and the lengths inside a
+// request have a closed form.
 #pragma once
 #include "kv8.cuh"
 
 namespace dflash {
 
 constexpr int KV8_GROUPS = KV8_MAX_REQ / 32;
+// The longest item is cut into about this many pieces at most, since its merge takes eight of them at a time:
+// a token with 8 heads over 65536 tokens of one kv head took 70 us in 1025 pieces, 34 in 64, 26 in 128, 25 in 256;
+// one with 2 heads of 64 over 48222 tokens 31, 25, 21 and 24. (The tiles' 152 workers are not held back.)
+constexpr int KV8_PIECES = 152;
 
 struct Kv8AttnArgs {
   int n_req, rows, nq, nkv, width, mask, words, n_pages;
@@ -89,6 +94,7 @@ struct Kv8Tiles {
   __device__ __forceinline__ int units(const Kv8Req &r, int qt) const { return max(1, (limit(r, qt) + U - 1) / U); }
   // what an item takes on the line: C units for its start and end, then its units
   __device__ __forceinline__ long long weight(const Kv8Req &r, int qt) const { return C + (long long)units(r, qt); }
+  __device__ __forceinline__ int longest(const Kv8Req &r) const { return r.n ? units(r, tiles(r) - 1) : 0; }
   // weight of one head's tiles before qt, for qt < tiles
   __device__ __forceinline__ long long before(const Kv8Req &r, int qt) const {
     return causal ? kv8_before_causal(U, C, tpt, qt, r.len - r.n) : qt * weight(r, 0);
@@ -133,13 +139,25 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (a.n_req + 31) / 32;
   long long total = 0;
+  int longest = 0;                                     // units of the longest item
+  __shared__ int s_longest[KV8_GROUPS];
   if (groups > 1) {
     for (int g = warp; g < groups; g += warps) {
       const int b = g * 32 + lane;
-      long long t = b < a.n_req ? tl.total(kv8_req(a, b)) : 0;
+      long long t = 0;
+      int u = 0;
+      if (b < a.n_req) {
+        const Kv8Req r = kv8_req(a, b);
+        t = tl.total(r);
+        u = tl.longest(r);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (lane == 0) s_grp[g + 1] = t;
+      u = __reduce_max_sync(0xffffffffu, u);
+      if (lane == 0) {
+        s_grp[g + 1] = t;
+        s_longest[g] = u;
+      }
     }
     if (threadIdx.x == 0) s_grp[0] = 0;
     __syncthreads();
@@ -153,6 +171,7 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
     }
     __syncthreads();
     total = s_grp[groups];
+    for (int g = lane; g < groups; g += 32) longest = max(longest, s_longest[g]);
   }
   Kv8Req r{0, 0, 0};
   long long mine = 0, inc = 0, pos = 0, base = 0;
@@ -161,11 +180,13 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
     if (lane < a.n_req) {
       r = kv8_req(a, lane);
       mine = tl.total(r);
+      longest = tl.longest(r);
     }
     inc = warp_scan_ll(mine);
     total = __shfl_sync(0xffffffffu, inc, 31);
   }
-  chunk = div_ll(total + workers - 1, workers);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  chunk = max(div_ll(total + workers - 1, workers), (long long)(longest + KV8_PIECES - 1) / KV8_PIECES);
   pos = me * chunk;
   if (pos >= total) return false;
   if (groups > 1) {

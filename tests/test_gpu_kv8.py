@@ -420,6 +420,15 @@ def test_attention_one_long_context(dtype, n_q):
     _check_attn(c, table, q, cu, ctx, "causal", tree, dtype, max_q=n_q[0])
 
 
+@pytest.mark.parametrize("others", [0, 3, 40])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention_one_item_of_many_pieces(others, dtype):
+    """A context of several hundred pages for one head beside empty and short ones: its pieces are kept few."""
+    ctx = [(i * 29) % 70 for i in range(others // 2)] + [30011] + [(i * 31) % 90 for i in range(others - others // 2)]
+    c, table, q, cu, tree = _attn_case(13 + others, ctx, [1] * len(ctx), 1, 64, 2, "causal", dtype)
+    _check_attn(c, table, q, cu, ctx, "causal", tree, dtype, max_q=1)
+
+
 @pytest.mark.parametrize("hd,n_q", [(64, 17), (128, 40), (128, 2)])
 def test_attention_long_pieces(hd, n_q):
     """Several items and many tiles per worker: every ring wraps a few times within a piece."""
