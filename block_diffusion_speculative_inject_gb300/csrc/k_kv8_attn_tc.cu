@@ -460,7 +460,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         if (!ok) break;
         const uint32_t sa = lane_base + sb * 128 + half * 64;    // my 64 tokens
         const KtSide &sd = sh.side[i % KT_SIDE];
-        const float c = fac * sd.ks[half], ev = sd.ev[half];
+        // Never zero, so that the -infinity of a hidden token stays one: a row of zeros (factor 2^-110 or so) and a page of
+        // zero keys (scale 2^-64) would underflow. |S| is below 2^24, so a score moves by 2^-102 at most.
+        const float c = fmaxf(fac * sd.ks[half], 1.17549435e-38f), ev = sd.ev[half];
         const bool partial = sd.page[half] < 0 || 2 * u + half >= open;
         // S of my tokens, without what the row does not see
         auto load_s = [&](float *sc) {
@@ -478,7 +480,6 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
           }
         };
         // P of 32 tokens for the present reference, as f16 pairs; returns their sum
-        // (a factor of zero may meet the -infinity of a hidden token: such rows are not written)
         auto exps = [&](const float *v, uint32_t *pw) {
           const float off = ev + KT_BIAS - (m_used == -INFINITY ? 0.f : m_used);
           float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};

@@ -523,6 +523,25 @@ def test_attention_scales_and_scores_of_very_different_size(dtype, n_q):
     _check_attn(c, table, q, cu, ctx, "none", tree, dtype, scale=3.0, max_q=n_q)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("mask", ["none", "causal", "tree"])
+@pytest.mark.parametrize("n_q,hint", [(3, 3), (3, 100), (40, 1), (40, 40)])
+def test_attention_zero_and_tiny_queries_over_zero_keys(dtype, mask, n_q, hint):
+    """Pages of zero keys have the smallest scale, 2^-64, and a row of zeros or of tiny entries a factor near 2^-110: their
+    product is below fp32's range. Such rows weigh all that they see alike, in every kernel that the hint may choose,
+    also on pages of which they see a part."""
+    ctx = [100 + n_q, 64, n_q, 200]
+    c, table, q, cu, tree = _attn_case(8, ctx, [n_q] * 4, 1, 128, 4, mask, dtype)
+    for b in (0, 1, 2):                                # the last request's keys stay as they are
+        for i in range(R.pages_of(ctx[b])):
+            p, live = int(table[b, i]), min(PAGE, ctx[b] - i * PAGE)
+            c["k_pages"].view(torch.uint8)[p, :, :live] = 0
+            c["k_scale"][p] = 2.0 ** -64
+    q[0::3] = 0
+    q[1::3] = (q[1::3].float() * 2.0 ** -90).to(dtype)
+    _check_attn(c, table, q, cu, ctx, mask, tree, dtype, max_q=hint)
+
+
 @pytest.mark.parametrize("hint", [0, 1, 16, 17, 10 ** 6])
 def test_attention_max_q_only_steers(hint):
     """Any max_q gives the rows of every request."""
