@@ -161,12 +161,13 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
     const int b = find_pre(s_gone, a.n, x);
     a.stack[n_free + x] = a.table[(size_t)b * a.width + (s_new[b] + KV_PAGE - 1) / KV_PAGE + x - s_gone[b]];
   }
-  for (int r = t0; r < a.max_rows; r += step) {
+  for (uint32_t u = t0; u < (uint32_t)a.max_rows; u += step) {     // (the last step may pass 2^31)
+    const int r = (int)u;
     int64_t slot = -1;
     int pos = 0;
     if (r < s_rows[a.n]) {
       const int b = find_pre(s_rows, a.n, r);
-      pos = s_len[b] + r - s_rows[b];
+      pos = s_len[b] + (r - s_rows[b]);
       const int i = pos / KV_PAGE, op = (s_len[b] + KV_PAGE - 1) / KV_PAGE;
       const int page = i < op ? a.table[(size_t)b * a.width + i] : granted(s_need[b] + i - op);
       slot = (int64_t)page * KV_PAGE + pos % KV_PAGE;

@@ -96,6 +96,23 @@ def test_page_plan_corrupt_lengths_stay_in_bounds():
     assert p["slot_map"].tolist()[:3] == [11 * 64, 11 * 64 + 1, 11 * 64 + 2]
 
 
+def test_page_plan_most_rows():
+    """The largest max_rows: a thread's next row index passes 2^31 before the loop ends."""
+    from block_diffusion_speculative_inject_gb300 import page_plan
+    most = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    p = page_plan(_i4([60, 0]), _i4([8, 3]), _i4([[4, -1], [-1, -1]]), _i4([0, 1, 2]), _i4([3]), most)
+    assert p["cu_rows"].tolist() == [0, 8, 11] and p["refused"].tolist() == [0, 0]
+    assert p["slot_map"].numel() == most and p["positions"].numel() == most
+    assert p["slot_map"][:11].tolist() == [4 * 64 + i for i in range(60, 64)] + [2 * 64 + i for i in range(4)] + [64, 65, 66]
+    assert p["positions"][:11].tolist() == list(range(60, 68)) + [0, 1, 2]
+    for at in range(11, most, 1 << 28):
+        assert bool((p["slot_map"][at:at + (1 << 28)] == -1).all()) and bool((p["positions"][at:at + (1 << 28)] == 0).all())
+    del p
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- rotary positions
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,nq,nk,hd,rot,inter,scaling", [
