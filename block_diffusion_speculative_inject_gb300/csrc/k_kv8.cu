@@ -23,8 +23,7 @@ struct PlanArgs {
 };
 
 struct Sum3 {
-  long long need, rows;
-  int gone;
+  long long need, rows, gone;                         // (4096 lengths of 2^24 pages: up to 2^36)
 };
 __device__ __forceinline__ Sum3 add3(const Sum3 &a, const Sum3 &b) {
   return Sum3{a.need + b.need, a.rows + b.rows, a.gone + b.gone};
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
   Sum3 total;
   Sum3 pre = block_scan(mine, warp_tot, total);
   const int n_free = max(0, min(a.n_free[0], a.n_pages));
-  const int have = min(a.n_pages, n_free + total.gone);
+  const int have = (int)min((long long)a.n_pages, n_free + total.gone);
   if (total.need > have || total.rows > a.max_rows) {  // uniform: some request is refused
     Sum3 run = pre, kept{0, 0, 0};
 #pragma unroll
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
     if (i >= ipt || b >= a.n) continue;
     s_need[b] = (int)pre.need;
     s_rows[b] = (int)pre.rows;
-    s_gone[b] = pre.gone;
+    s_gone[b] = (int)min(pre.gone, 1ll << 30);        // only the first n_pages <= 2^24 are looked up
     s_len[b] = len[i];
     s_new[b] = to[i];
     const int op = (len[i] + KV_PAGE - 1) / KV_PAGE, np = (to[i] + KV_PAGE - 1) / KV_PAGE;
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
   if (tid == 0) {
     s_need[a.n] = (int)total.need;
     s_rows[a.n] = (int)total.rows;
-    s_gone[a.n] = total.gone;
+    s_gone[a.n] = (int)min(total.gone, 1ll << 30);
     if (blockIdx.x == 0) {
       a.cu_rows[a.n] = (int)total.rows;
       a.n_free_out[0] = have - (int)total.need;

@@ -369,8 +369,8 @@ dflash_status dflash_ddtree_walk(void *stream, int32_t n_req, int32_t L, int32_t
  *   ctx_len [n_req], n_new [n_req] int32; block_table [n_req, max_blocks] int32, entry i the page
  *   of tokens 64 i .. 64 i + 63; free_list [n_pages] int32, a stack whose first n_free[0] entries
  *   are the free pages (n_free [1] int32).
- * Given back pages (whole pages past the new end) are pushed in request order; then the requests
- * that grow pop theirs off the top, in request order. A request is refused, and keeps its length,
+ * Given back pages (whole pages past the new end) are pushed in request order, as far as the stack's
+ * n_pages entries go; then the requests that grow pop theirs off the top, in request order. A request is refused, and keeps its length,
  * when its new length needs more than max_blocks pages, when the pages asked for by it and the
  * requests before it are more than there are, or when their rows are more than max_rows.
  *   Outputs: new_len [n_req], n_free_out [1], cu_rows [n_req + 1] (prefix sums of the rows that

@@ -96,6 +96,28 @@ def test_page_plan_corrupt_lengths_stay_in_bounds():
     assert p["slot_map"].tolist()[:3] == [11 * 64, 11 * 64 + 1, 11 * 64 + 2]
 
 
+def test_page_plan_gives_back_more_than_2_31_pages():
+    """The table's width is the caller's, so the pages given back may be more than 2^31 (and than the stack holds):
+    the first of them fill the stack, and the requests that grow take theirs from its top."""
+    from block_diffusion_speculative_inject_gb300 import page_plan
+    n, width, n_pages = 4096, (1 << 19) + 300, 100
+    assert (n - 1) * width > 2 ** 31
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    table = torch.zeros((n, width), dtype=torch.int32, device="cuda")
+    table[0, :200] = torch.arange(200, dtype=torch.int32)
+    ctx, add = [width * PAGE] * (n - 1) + [0], [-width * PAGE] * (n - 1) + [130]
+    stack = _i4([1000 + i for i in range(n_pages)])
+    p = page_plan(_i4(ctx), _i4(add), table, stack, _i4([40]), 130)
+    assert p["new_len"].tolist() == [0] * (n - 1) + [130] and int(p["refused"].sum()) == 0
+    assert p["n_free"].tolist() == [97]
+    assert stack.tolist() == [1000 + i for i in range(40)] + list(range(60))
+    assert table[n - 1, :3].tolist() == [59, 58, 57] and int(table[n - 1, 3:].sum()) == 0
+    assert p["slot_map"].tolist() == [(59 - i // PAGE) * PAGE + i % PAGE for i in range(130)]
+    del table
+    torch.cuda.empty_cache()
+
+
 def test_page_plan_most_rows():
     """The largest max_rows: a thread's next row index passes 2^31 before the loop ends."""
     from block_diffusion_speculative_inject_gb300 import page_plan
