@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) k_kv8_attn_rows(const Kv8AttnAr
   if (lane < Lay::SLOTS) mbar_init(bar0 + 8 * lane, 1);
   if (threadIdx.x == 0) s_abort = 0;
   fence_mbar_init();
+  __syncthreads();                                     // every warp reads s_abort, every lane the warp's barriers
   pdl_wait();
   const int me = warp * gridDim.x + blockIdx.x;        // few workers spread over all SMs
   long long chunk, item_begin;

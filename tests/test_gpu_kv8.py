@@ -728,6 +728,24 @@ def test_round_in_a_graph_and_on_another_stream():
         q, k, v = (x.cuda() for x in eager.draw(n * blk))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_few_rows_after_kernels_that_fill_shared_memory(dtype):
+    """Small few-row calls (no request is beyond the 32 that a warp sums up alone) between many-row ones, whose tiles of
+    random bytes stay in shared memory: the abort word and the barriers are set before any warp looks at them."""
+    from block_diffusion_speculative_inject_gb300 import kv8_attention
+    c, table, q, cu, _ = _attn_case(41, [300, 70], [2, 2], 8, 128, 16, "causal", dtype)
+    few = (_to_gpu(c), q.cuda(), _i4(cu), _i4([300, 70]), table.cuda())
+    c, table, q, cu, _ = _attn_case(42, [900] * 4, [64] * 4, 8, 128, 16, "causal", torch.bfloat16)
+    many = (_to_gpu(c), q.cuda(), _i4(cu), _i4([900] * 4), table.cuda())
+    want = kv8_attention(*few, max_q=2)
+    assert bool(want.isfinite().all())
+    got = []
+    for _ in range(100):
+        kv8_attention(*many, max_q=64)
+        got += [kv8_attention(*few, max_q=2) for _ in range(2)]
+    assert all(torch.equal(x, want) for x in got)
+
+
 @pytest.mark.parametrize("n_q", [1, 20])
 def test_two_calls_at_once(n_q):
     """Two streams, their own workspaces, split contexts: each equals its call alone, bit for bit, many times."""
