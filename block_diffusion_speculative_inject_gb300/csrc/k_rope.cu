@@ -1,9 +1,9 @@
 // Rotary positions (dflash_rope_init / dflash_rope_apply).
 //
-// Pair i turns by position * f_i. The host keeps F_i = frac(f_i / 2 pi) * 2^64; the 64-bit
-// product position * F_i, whose overflow drops whole turns, is then the angle as a fraction of a
-// turn. Its error is position * 2^-55 turns (F_i comes from a double), below fp32's own for
-// every int32 position, and there is no table: no memory, no position limit.
+// Pair i turns by position * f_i. The host keeps F_i = frac(f_i / 2 pi) * 2^64, to the nearest integer;
+// the 64-bit product position * F_i, whose overflow drops whole turns, is then the angle as a fraction
+// of a turn. Its error is position * 2^-65 turns, 2^-34 turns (4e-10 rad) at the last int32 position and thus
+// below fp32's own everywhere, and there is no table: no memory, no position limit.
 //
 // Every element of q and k is read and written once, which bounds it: the sine and cosine of a
 // row's pairs (at most 128) are computed once in shared memory and used by all of its heads.
@@ -149,6 +149,47 @@ cudaError_t launch_rope(const RopeArgs &a, bool inter, int width, cudaStream_t s
 
 using namespace dflash;
 
+namespace {
+// A double's 53 bits would leave position * 2^-54 turns, 6e-7 rad at 2^31. The table is made in sums of two doubles
+// instead (over 100 bits), with error-free sums and products (Dekker 1971), the same on every host: products are
+// kept from being contracted into the sums that follow.
+struct Two {
+  double hi, lo;
+};
+Two sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return Two{s, (a - (s - t)) + (b - t)};
+}
+Two add(Two a, Two b) {
+  const Two s = sum(a.hi, b.hi);
+  return sum(s.hi, s.lo + (a.lo + b.lo));
+}
+Two mul(Two a, Two b) {
+  volatile double p = a.hi * b.hi;
+  const double e = std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi);
+  return sum(p, e);
+}
+Two div(Two a, Two b) {
+  const double q = a.hi / b.hi;
+  const Two p = mul(Two{q, 0}, b), r = add(a, Two{-p.hi, -p.lo});
+  return sum(q, r.hi / b.hi);
+}
+// e^x for |x| < 90: 18 terms of the series at x / 1024, then squared ten times
+Two exponential(Two x) {
+  const Two y{x.hi / 1024, x.lo / 1024};
+  Two e{1, 0};
+  for (int n = 18; n > 0; --n) e = add(Two{1, 0}, mul(div(y, Two{(double)n, 0}), e));
+  for (int n = 0; n < 10; ++n) e = mul(e, e);
+  return e;
+}
+// ln x: one step of Newton's method from the double
+Two logarithm(double x) {
+  const double l = std::log(x);
+  const Two e = mul(Two{x, 0}, exponential(Two{-l, 0}));
+  return add(Two{l, 0}, add(e, Two{-1, 0}));
+}
+}  // namespace
+
 extern "C" dflash_status dflash_rope_init(const dflash_rope_params *p, dflash_rope *rope) {
   if (!p || !rope || p->rot_dim < 2 || p->rot_dim > 256 || p->rot_dim % 2 || (p->interleaved & ~1) ||
       p->scaling < DFLASH_ROPE_NONE || p->scaling > DFLASH_ROPE_YARN || !(p->theta > 1.f) || !std::isfinite(p->theta))
@@ -159,6 +200,7 @@ extern "C" dflash_status dflash_rope_init(const dflash_rope_params *p, dflash_ro
        !(p->beta_fast > p->beta_slow) || !std::isfinite(p->beta_fast)))
     return DFLASH_ERR_INVALID_ARG;
   const double pi = 3.14159265358979323846, rot = p->rot_dim, lt = std::log((double)p->theta);
+  const Two log_theta = logarithm(p->theta), per_turn{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};   // 1 / (2 pi)
   double lo = 0, hi = 0;
   if (p->scaling == DFLASH_ROPE_YARN) {
     auto dim = [&](double beta) { return rot * std::log(p->original_positions / (beta * 2 * pi)) / (2 * lt); };
@@ -168,14 +210,17 @@ extern "C" dflash_status dflash_rope_init(const dflash_rope_params *p, dflash_ro
   for (int i = 0; i < 128; ++i) {
     rope->turn[i] = 0;
     if (i >= p->rot_dim / 2) continue;
-    double f = std::exp(-2.0 * i / rot * lt);
-    if (p->scaling == DFLASH_ROPE_LINEAR) f /= p->factor;
-    if (p->scaling == DFLASH_ROPE_YARN) {
-      const double g = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
-      f = f / p->factor * g + f * (1 - g);
+    Two f = exponential(div(mul(log_theta, Two{-2.0 * i, 0}), Two{rot, 0}));
+    if (p->scaling == DFLASH_ROPE_LINEAR) f = div(f, Two{p->factor, 0});
+    if (p->scaling == DFLASH_ROPE_YARN && i > lo) {
+      const double past = i - lo, width = std::fmax(hi - lo, 0.001);
+      const Two g = past < width ? div(Two{past, 0}, Two{width, 0}) : Two{1, 0};
+      f = add(mul(div(f, Two{p->factor, 0}), g), mul(f, add(Two{1, 0}, Two{-g.hi, -g.lo})));
     }
     // f <= 1, so the fraction of a turn is below 0.16 and fits 64 bits
-    rope->turn[i] = (uint64_t)(f / (2 * pi) * 0x1p64);
+    f = mul(f, per_turn);
+    const double turns = f.hi * 0x1p64, whole = std::floor(turns);
+    rope->turn[i] = (uint64_t)whole + (uint64_t)(int64_t)std::floor((turns - whole) + f.lo * 0x1p64 + 0.5);
   }
   rope->magnitude = p->scaling == DFLASH_ROPE_YARN ? (float)(0.1 * std::log((double)p->factor) + 1.0) : 1.f;
   rope->rot_dim = p->rot_dim;

@@ -391,12 +391,12 @@ dflash_status dflash_page_plan(void *stream, int32_t n_req, int32_t max_blocks, 
  * f_i = theta^(-2 i / rot_dim), scaled for contexts longer than those trained on:
  *   DFLASH_ROPE_LINEAR  f_i / factor (position interpolation);
  *   DFLASH_ROPE_YARN    f_i ((1 - g_i) + g_i / factor) with the ramp g_i = clamp((i - lo) / (hi - lo))
- *     between the pairs that make beta_fast and beta_slow turns over original_positions,
+ *     (a step behind pair lo where hi <= lo) between the pairs that make beta_fast and beta_slow turns over original_positions,
  *     lo = floor(d(beta_fast)) >= 0, hi = ceil(d(beta_slow)) <= rot_dim - 1, d(b) = rot_dim
  *     ln(original_positions / (2 pi b)) / (2 ln theta); the rotated dims are multiplied by
  *     0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN", 3.2-3.4).
- * Angles are kept as 64-bit fixed-point fractions of a turn, so that they are as exact at the
- * last int32 position as at the first. */
+ * Angles are kept as 64-bit fixed-point fractions of a turn, frequencies to half of the last bit: at the last
+ * int32 position an angle is off by 4e-10 rad, which is far below what fp32 can say of it. */
 typedef enum { DFLASH_ROPE_NONE = 0, DFLASH_ROPE_LINEAR = 1, DFLASH_ROPE_YARN = 2 } dflash_rope_scaling;
 typedef struct {
   int32_t rot_dim;             /* even, 2 .. 256                                          */

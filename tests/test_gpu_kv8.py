@@ -179,6 +179,24 @@ def test_rope_far_and_negative_positions():
     assert bool(((got.cpu().double() - want).abs() <= 2 * x.double().abs().amax(-1, keepdim=True) * 1.8e-6).all())
 
 
+@pytest.mark.parametrize("theta", [1e4, 1e6])
+def test_rope_is_as_exact_far_away_as_near(theta):
+    """One bound for positions near 0 and at both ends of int32. The phase is off by 2^31 * 2^-65 turns (4e-10 rad); the
+    reduced angle (at most pi/4) is rounded to fp32 (pi/4 2^-24 = 4.7e-8), sine and cosine below 1 are within two units of
+    2^-24 (1.2e-7), the second product is rounded once, and the output once."""
+    from block_diffusion_speculative_inject_gb300 import Rope, rope
+    freq, mag = R.rope_freq(128, theta)
+    pos = [2 ** 31 - 1 - 7 ** i for i in range(11)] + [-2 ** 31 + 5 ** i for i in range(12)] + list(range(-9, 9))
+    pos = torch.tensor(pos, dtype=torch.int32)
+    x = torch.randn((len(pos), 4, 128), generator=torch.Generator().manual_seed(4))
+    x[:, 2, :64], x[:, 3, 64:] = 0, 0
+    got, _ = rope(Rope(128, theta=theta), pos.cuda(), x.cuda())
+    want = R.rope(x.double(), pos.tolist(), 128, freq, mag, False)
+    mine, other = x.double().abs(), x.double().abs().roll(64, -1)
+    tol = (mine + other) * (4e-10 + 4.7e-8 + 1.2e-7) + torch.maximum(mine, other) * 2.0 ** -24 + want.abs() * 2.0 ** -24
+    assert bool(((got.cpu().double() - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("shift", [0, 1])

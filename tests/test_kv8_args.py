@@ -81,6 +81,38 @@ def test_rope_table_matches_its_definition(lib, rot, theta, kw):
     assert abs(t.magnitude - mag) <= 2.0 ** -23 * mag
 
 
+@pytest.mark.parametrize("rot,theta,kw", [
+    (64, 1e4, {}), (128, 1e6, {}), (256, 5e5, {}), (2, 1.5, {}), (6, 3e38, {}), (128, 1e7, dict(scaling="linear", factor=3.7)),
+    (128, 1e6, dict(scaling="yarn", factor=4.0, original=32768.0)), (20, 1e4, dict(scaling="yarn", factor=40.0, original=4096.0)),
+    (64, 1e4, dict(scaling="yarn", factor=2.5, original=4.0)), (256, 1e6, dict(scaling="yarn", factor=1.0, original=131072.0))])
+def test_rope_table_to_its_last_bit(lib, rot, theta, kw):
+    """Turns per position to 60 digits, the ramp as a fraction of whole numbers: the table holds the nearest multiple of
+    2^-64 (half a unit, and 2^-20 for what over 90 bits leave)."""
+    import math
+    from decimal import Decimal, getcontext
+
+    import numpy as np
+
+    from block_diffusion_speculative_inject_gb300 import Rope
+    f32 = lambda x: Decimal(float(np.float32(x)))  # noqa: E731
+    args = {("original_positions" if k == "original" else k): v for k, v in kw.items()}
+    t = Rope(256, rot_dim=rot, theta=theta, **args)._c
+    getcontext().prec = 60
+    pi, lt = Decimal("3.14159265358979323846264338327950288419716939937510582097494"), f32(theta).ln()
+    factor = f32(kw.get("factor", 1.0))
+    if kw.get("scaling") == "yarn":
+        dim = lambda b: rot * math.log(kw["original"] / (b * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
+        lo, hi = max(math.floor(dim(32.0)), 0), min(math.ceil(dim(1.0)), rot - 1)
+    for i in range(rot // 2):
+        f = (Decimal(-2 * i) * lt / rot).exp()
+        if kw.get("scaling") == "linear":
+            f /= factor
+        if kw.get("scaling") == "yarn":
+            g = Decimal(0) if i <= lo else Decimal(1) if i >= hi else Decimal(i - lo) / Decimal(hi - lo)
+            f = f / factor * g + f * (1 - g)
+        assert abs(Decimal(t.turn[i]) - f / (2 * pi) * 2 ** 64) <= Decimal(0.5) + Decimal(2) ** -20, i
+
+
 def test_rope_apply_refusals(lib):
     from block_diffusion_speculative_inject_gb300 import _ffi
     t = _ffi.RopeTable()
