@@ -10,7 +10,8 @@ One round of a verify loop, with nothing read back to the host:
 
 Calls run on the device of their tensors, on `stream` (default: that device's current stream), and
 allocate outputs that are not given from torch's allocator. Arguments that do not fit raise
-DFlashError before anything is launched.
+DFlashError before anything is launched. None of them records a gradient, so with grad mode on a floating-point
+tensor that requires one is refused (rope's gradient is rope with transpose=True, for a Function of the caller's).
 """
 import ctypes
 import math
@@ -82,6 +83,14 @@ def _device(first, *others):
     if i < 0:
         raise _error("tensors must be on a CUDA device")
     return i
+
+
+def _no_gradient(name, *tensors):
+    """Refuses a call whose result would silently have no history."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise _error(f"{name} records no gradients: call it under torch.no_grad(), or detach its tensors")
 
 
 def _ptr(t):
@@ -226,6 +235,7 @@ def rope(table, positions, q, k=None, transpose=False, q_out=None, k_out=None, s
             kos = _row_stride("k_out", k_out, nk, hd)
     elif k_out is not None:
         raise _error("k_out without k")
+    _no_gradient("rope", q, k, q_out, k_out)
     dev = _device(q, k, positions, q_out, k_out)
 
     def body(s):
@@ -250,6 +260,7 @@ def kv8_append(cache, k, v, slot_map, stream=None):
     ks, vs = _row_stride("k", k, heads, hd), _row_stride("v", v, heads, hd)
     _aligned_rows("k", k, ks)
     _aligned_rows("v", v, vs)
+    _no_gradient("kv8_append", k, v)
     _on(cache._device(k, v, slot_map), stream,
         lambda s: _call("dflash_kv8_append", s, cache._ref, rows, _dt(k), k.data_ptr(), ks, v.data_ptr(), vs,
                         slot_map.data_ptr()))
@@ -279,6 +290,7 @@ def kv8_attention(cache, q, cu_q, ctx_len, block_table, mask="causal", tree_mask
     else. workspace: a uint8 tensor of kv8_workspace(...) bytes; allocated for the call if None.
     Returns out [rows, heads, head_dim], or (out, lse [rows, heads] fp32) with want_lse."""
     a = _attn_args(cache, q, cu_q, ctx_len, block_table, mask, tree_mask, scale, max_q, out, lse)
+    _no_gradient("kv8_attention", q, out, lse)
     if workspace is not None:
         _tensor("workspace", workspace, _U1, (None,))
     dev = cache._device(q, cu_q, ctx_len, block_table, tree_mask, out, lse, workspace)

@@ -242,6 +242,30 @@ def test_rope_transpose_is_the_gradient():
         assert abs(float((diff * y.double()).sum()) - float(grad[at])) < 1e-4      # 128 outputs, 2 * 4e-7 * |y| each
 
 
+def test_rope_inside_a_function_of_the_caller():
+    """Autograd over both outputs through the caller's Function: the gradients are the transposed calls', bit for bit."""
+    from block_diffusion_speculative_inject_gb300 import Rope, rope
+    t = Rope(64, rot_dim=32)
+    pos = _i4([5, 0, 70000])
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k):
+            return rope(t, pos, q, k)
+
+        @staticmethod
+        def backward(ctx, gq, gk):
+            return rope(t, pos, gq.contiguous(), gk.contiguous(), transpose=True)
+
+    g = torch.Generator().manual_seed(6)
+    q, k = (torch.randn((3, h, 64), generator=g).cuda().requires_grad_() for h in (4, 2))
+    wq, wk = (torch.randn((3, h, 64), generator=g).cuda() for h in (4, 2))
+    a, b = Turn.apply(q, k)
+    ((a * wq).sum() + (b * wk).sum()).backward()
+    want = rope(t, pos, wq, wk, transpose=True)
+    assert torch.equal(q.grad, want[0]) and torch.equal(k.grad, want[1])
+
+
 # ---------------------------------------------------------------- quantised append
 def _cache_cpu(seed, n_pages, nkv, hd, poison=True):
     """A pool with finite random bytes in every page, scales 2^-8 .. 2^-4."""

@@ -228,3 +228,25 @@ def test_binding_refusals():
         pkg.kv8_attention(cache, **att)
     with pytest.raises(pkg.DFlashError, match="CUDA device"):
         pkg.page_plan(**plan)
+
+
+def test_binding_refuses_to_lose_a_gradient():
+    """A result without a history, or a cache written past autograd, is refused where gradients are recorded."""
+    import block_diffusion_speculative_inject_gb300 as pkg
+    i4 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    e4 = lambda *s: torch.zeros(s, dtype=torch.uint8).view(torch.float8_e4m3fn)  # noqa: E731
+    x = lambda grad: torch.zeros((3, 2, 64), requires_grad=grad)  # noqa: E731
+    cache = pkg.KV8Cache(e4(4, 2, 64, 64), e4(4, 2, 64, 64), torch.zeros(4, 2), torch.zeros(4, 2))
+    r, slots = pkg.Rope(64), torch.zeros(3, dtype=torch.int64)
+    att = (i4(2), i4(1), i4(1, 4))
+    calls = [lambda g: pkg.rope(r, i4(3), x(g)), lambda g: pkg.rope(r, i4(3), x(False), x(g)),
+             lambda g: pkg.rope(r, i4(3), x(False), q_out=x(g)), lambda g: pkg.kv8_append(cache, x(g), x(False), slots),
+             lambda g: pkg.kv8_append(cache, x(False), x(g), slots), lambda g: pkg.kv8_attention(cache, x(g), *att),
+             lambda g: pkg.kv8_attention(cache, x(False), *att, out=x(g))]
+    for call in calls:
+        with pytest.raises(pkg.DFlashError, match="no gradients"):
+            call(True)
+        with torch.no_grad(), pytest.raises(pkg.DFlashError, match="CUDA device"):      # taken as far as a CPU tensor goes
+            call(True)
+        with pytest.raises(pkg.DFlashError, match="CUDA device"):
+            call(False)
