@@ -740,6 +740,79 @@ def test_verify_loop(dtype, group, hd):
     assert sorted(got + lp.stack[:int(lp.free)].tolist()) == list(range(64))      # no page lost, none twice
 
 
+@pytest.mark.parametrize("budget", [11, 40])
+def test_draft_tree_round(budget):
+    """A round over draft trees: ddtree_build's masks go to the attention as they are (checked against the parents' chains),
+    ddtree_walk accepts a path, and the path's rows, which lie scattered among the tree's, are appended anew after all of
+    the tree's tokens were dropped."""
+    from block_diffusion_speculative_inject_gb300 import (ddtree_build, ddtree_walk, kv8_append, kv8_attention, page_plan,
+                                                          rope)
+    n, L, kc, nkv, dtype = 3, 7, 4, 2, torch.bfloat16
+    lp = _Loop(n, nkv, 4, 128, 40, 8, dtype, seed=3)
+    prompt = [100, 1, 63]
+    q, k, v = lp.draw(sum(prompt))
+    p, qr, kr, out = lp.device_round(_i4(prompt), sum(prompt), q.cuda(), k.cuda(), v.cuda(), max(prompt))
+    lp.check_round(p, kr, qr, v, out)
+    lp.len, lp.free = p["new_len"], p["n_free"]
+
+    logp = -torch.sort(torch.rand((n, L, kc), generator=lp.g) * 3, dim=2).values
+    tok = torch.arange(kc, dtype=torch.int32).expand(n, L, kc).contiguous()
+    tree = ddtree_build(tok.cuda(), logp.cuda(), budget)
+    assert tree["n_nodes"].tolist() == [budget] * n
+    rows = n * (budget + 1)
+    q, k, v = lp.draw(rows)
+    p = page_plan(lp.len, _i4([budget + 1] * n), lp.table, lp.stack, lp.free, rows)
+    depth = torch.cat([torch.zeros((n, 1), dtype=torch.int32, device="cuda"), tree["depth"]], 1)
+    positions = (lp.len[:, None] + depth).reshape(-1).to(torch.int32)
+    qr, kr = rope(lp.rope, positions, q.cuda(), k.cuda())
+    kv8_append(lp.cache, kr, v.cuda(), p["slot_map"])
+    out = kv8_attention(lp.cache, qr, p["cu_rows"], p["new_len"], lp.table, mask="tree",
+                        tree_mask=tree["mask"].flatten(0, 1), max_q=budget + 1)
+    R.append(lp.ref, kr.cpu(), v, p["slot_map"].tolist())
+    parent = tree["parent"].tolist()
+    chain = torch.zeros((n, budget + 1, budget + 1), dtype=torch.bool)
+    for b in range(n):
+        for i in range(budget + 1):
+            j = i
+            while j > 0:
+                chain[b, i, j] = True
+                j = parent[b][j - 1] + 1
+            chain[b, i, 0] = True
+    bits = torch.zeros((n, budget + 1, 2), dtype=torch.int64)
+    for j in range(budget + 1):
+        bits[:, :, j // 32] |= chain[:, :, j].long() << (j % 32)
+    bits = (bits - (bits >> 31 << 32)).to(torch.int32).flatten(0, 1)
+    want, _, absv, top = R.attention(lp.ref, qr.cpu(), p["cu_rows"].tolist(), p["new_len"].tolist(), lp.table.cpu(), "tree", bits)
+    tol = want.abs() * HALF[dtype] + absv * (2.0 ** -11 + 2 * (top * 2.0 ** -19 + 2.0 ** -19))[..., None]
+    assert bool(((out.cpu().double() - want).abs() <= tol).all())
+
+    target = torch.randint(0, kc, (n, budget + 1), generator=lp.g, dtype=torch.int32)
+    target[:, 0] = tree["tok"][:, 0].cpu()
+    accept, tokens, _ = ddtree_walk(tree, L, target.cuda())
+    path = []                                          # rows of the accepted path, the root first
+    for b in range(n):
+        at = 0
+        path.append(b * (budget + 1))
+        for t in tokens[b, :int(accept[b])].tolist():
+            at = next(i + 1 for i in range(budget) if parent[b][i] == at - 1 and int(tree["tok"][b, i]) == t)
+            path.append(b * (budget + 1) + at)
+    assert len(path) == int(accept.sum()) + n and int(accept.min()) >= 1
+    drop = page_plan(p["new_len"], _i4([-budget - 1] * n), lp.table, lp.stack, p["n_free"], 0)
+    assert torch.equal(drop["new_len"], lp.len)
+    kept = page_plan(drop["new_len"], accept + 1, lp.table, lp.stack, drop["n_free"], rows)
+    idx = torch.tensor(path)
+    ka, va = (torch.cat([x, torch.zeros((rows - len(path),) + x.shape[1:], dtype=dtype)]) for x in (kr.cpu()[idx], v[idx]))
+    kv8_append(lp.cache, ka.cuda(), va.cuda(), kept["slot_map"])
+    R.append(lp.ref, ka, va, kept["slot_map"].tolist())
+    assert torch.equal(kept["positions"][:len(path)].cpu(), positions.cpu()[idx])
+    q, _, _ = lp.draw(n)
+    cu, ctx = list(range(n + 1)), kept["new_len"].tolist()
+    out = kv8_attention(lp.cache, q.cuda(), _i4(cu), kept["new_len"], lp.table, max_q=1)
+    want, _, absv, top = R.attention(lp.ref, q, cu, ctx, lp.table.cpu(), "causal")
+    tol = want.abs() * HALF[dtype] + absv * (2.0 ** -11 + 2 * (top * 2.0 ** -19 + 2.0 ** -19))[..., None]
+    assert bool(((out.cpu().double() - want).abs() <= tol).all())
+
+
 def test_round_in_a_graph_and_on_another_stream():
     """A whole round captured once and replayed on new inputs equals the eager round; two graphs with their own
     workspaces run at once on two streams."""
