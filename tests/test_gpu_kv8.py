@@ -644,6 +644,58 @@ def test_attention_strided_queries():
         assert torch.equal(kv8_attention(gpu, view, *args, max_q=n_q), want)
 
 
+@pytest.mark.parametrize("n_q,hint", [(1, 1), (2, 64)])
+def test_attention_most_requests(n_q, hint):
+    """4096 requests, a fifth of them without rows, in both kernels."""
+    ctx = [(i * 37) % 130 for i in range(4096)]
+    c, table, q, cu, tree = _attn_case(15, ctx, [n_q if i % 5 else 0 for i in range(4096)], 1, 64, 1, "causal", torch.bfloat16)
+    _check_attn(c, table, q, cu, ctx, "causal", tree, torch.bfloat16, max_q=hint)
+
+
+@pytest.mark.parametrize("hint", [1, 3])
+def test_attention_most_heads_and_blocks(hint):
+    """128 kv heads of 8 query heads each; a block table of 2^24 entries."""
+    from block_diffusion_speculative_inject_gb300 import kv8_attention
+    ctx, n_q = [70, 130], [3, 1]
+    c, table, q, cu, tree = _attn_case(16, ctx, n_q, 128, 64, 1024, "causal", torch.bfloat16, extra=0)
+    _check_attn(c, table, q, cu, ctx, "causal", tree, torch.bfloat16, max_q=hint)
+    gpu, q1 = _to_gpu(c), q[:3].cuda()
+    wide = torch.full((1, 1 << 24), -1, dtype=torch.int32, device="cuda")
+    wide[0, :table.shape[1]] = table[0].cuda()
+    one = table[:1].cuda().contiguous()
+    assert torch.equal(kv8_attention(gpu, q1, _i4([0, 3]), _i4([70]), wide, max_q=hint),
+                       kv8_attention(gpu, q1, _i4([0, 3]), _i4([70]), one, max_q=hint))
+
+
+def test_append_and_plan_at_their_limits():
+    """128 kv heads; a table of 2^24 blocks and a stack of 2^24 pages; the largest and smallest slots."""
+    from block_diffusion_speculative_inject_gb300 import kv8_append, page_plan
+    n_pages, nkv, hd = 5, 128, 64
+    g = torch.Generator().manual_seed(12)
+    slots = [PAGE * 3 + 60 + i for i in range(4)] + [2 ** 63 - 1, -2 ** 63, n_pages * PAGE] + [PAGE + i for i in range(9)]
+    k, v = (torch.randn((len(slots), nkv, hd), generator=g).bfloat16() for _ in range(2))
+    want = _cache_cpu(5, n_pages, nkv, hd)
+    gpu = _to_gpu(want)
+    kv8_append(gpu, k.cuda(), v.cuda(), torch.tensor(slots, device="cuda"))
+    R.append(want, k, v, slots)
+    _same_cache(gpu, want)
+    most = 1 << 24
+    table = torch.full((1, most), -1, dtype=torch.int32, device="cuda")
+    stack = torch.arange(most, dtype=torch.int32, device="cuda")
+    full = page_plan(_i4([0]), _i4([most * PAGE]), table, stack, _i4([most]), 0)         # no room for the rows
+    assert full["refused"].tolist() == [1] and full["n_free"].tolist() == [most]
+    full = page_plan(_i4([0]), _i4([most * PAGE]), table, stack, _i4([most]), most * PAGE)
+    assert full["refused"].tolist() == [0] and full["n_free"].tolist() == [0] and full["new_len"].tolist() == [most * PAGE]
+    assert torch.equal(table[0], torch.arange(most - 1, -1, -1, dtype=torch.int32, device="cuda"))
+    p = torch.arange(most * PAGE, dtype=torch.int32, device="cuda")
+    assert torch.equal(full["positions"], p)
+    assert torch.equal(full["slot_map"], (most - 1 - p.long() // PAGE) * PAGE + p % PAGE)
+    del full, p
+    back = page_plan(_i4([most * PAGE]), _i4([-2 ** 31]), table, stack.zero_(), _i4([0]), 0)
+    assert back["n_free"].tolist() == [most] and torch.equal(stack, table[0])
+    torch.cuda.empty_cache()
+
+
 def test_far_pages_of_a_large_pool():
     """Pages whose bytes lie beyond 2^32: append, read and both attention kernels."""
     from block_diffusion_speculative_inject_gb300 import KV8Cache, kv8_append, kv8_attention, kv8_read
