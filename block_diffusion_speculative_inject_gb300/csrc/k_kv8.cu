@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
 // shared tile, since its pages are transposed: a thread holds neighbouring tokens of its dims, so that
 // the tile is written in words of four tokens.
 //
-// Bound by latency for a few rows (scale, rows and slots are dependent loads: 8 x 16 rows of 8 x 128 take 7.7 us)
+// Bound by latency for a few rows (8 x 16 rows of 8 x 128 take 7.7 us: slots, then rows and scale, then stores. Rows wait
+// for the slots because a thread's registers go by the offset in the page, not because their addresses need them)
 // and by instructions for many (8 x 4096 rows: 42.0 us, 4.8 TB/s), so the maximum is taken on pairs, bytes are
 // turned with permutes and a whole page of V is copied 16 bytes at a time (59.7 us without these). Six CTAs
 // per SM are asked for (44.5 us with five). A warp looks for a window's next run in 64 slots at once: row by
@@ -192,7 +193,8 @@ __global__ void __launch_bounds__(PP_THREADS) k_page_plan(const PlanArgs a) {
 // The slots of a run are found by every warp for itself (a run whose slots rise by one, which is what a
 // plan makes, needs no barrier); only two barriers are left, around the CTA's maximum and V's tile.
 constexpr int KA_THREADS = 256;
-constexpr int KV8_CTAS = 152 * 8;                     // CTAs of KA_THREADS that the GPU holds at once
+constexpr int KV8_CTAS = 152 * 8;                     // CTAs that a call is cut into before its windows grow: a wave of the
+                                                      // six per SM that fit, and a third of one
 
 template <typename T>
 struct AppendArgs {
@@ -430,7 +432,7 @@ cudaError_t launch_append(const dflash_kv8_cache *c, int rows, const void *k, in
   AppendArgs<T> a{rows, 1, c->n_kv_heads, c->n_pages, (const T *)k, (const T *)v, ks, vs, slot,
                   (uint8_t *)c->k_pages, (uint8_t *)c->v_pages, c->k_scale, c->v_scale};
   // Rows of a window: one, so that every row of a few may start a page of its own at once, up to a
-  // page's worth when that leaves CTAs enough for 8 per SM (half of it, for twice as many: 11.8 against 9.8 us at 33 x 8
+  // page's worth when that leaves KV8_CTAS CTAs (half of it, for twice as many: 11.8 against 9.8 us at 33 x 8
   // rows of 8 x 128, 8.4 against 5.9 us at 29 x 48 .. 96 of 1 x 64, 13.4 against 16.7 at 7849 rows of 4 x 128).
   const long ctas = (long)rows * c->n_kv_heads * 2;
   a.window = (int)(ctas / KV8_CTAS);

@@ -6,8 +6,9 @@
 //   O[128, hd] += P . V          kind::f16, A = P in tensor memory, B = V pages widened to f16
 // Q's row, scaled by a power of two so that its largest entry is in [128, 256), is the sum of an e4m3 and
 // an e5m2 part: bf16 has 8 significant bits, e4m3 takes 4, and what rounding to nearest leaves is at
-// most 8 units of the last place, which e5m2's 3 bits hold exactly. So K needs no conversion, and S is
-// exact for entries of q down to 2^-14 of the row's largest (below, q is off by at most 2^-21 of it).
+// most 8 units of the last place, which e5m2's 3 bits hold exactly. So K needs no conversion, and q is
+// exact for entries down to 2^-6 scaled, 2^-13 of the row's largest. Below, e4m3 is subnormal and leaves up to 16
+// units and more, and e5m2 rounds those by 2^-14 at most: 2^-21 of the row's largest.
 // P could not go the same way: rows with one loud token and many quiet ones need its small values, so
 // P is f16 (11 bits, largest 2^7 .. 2^15, normal to 2^-14) and two warps widen V (exact) into a second
 // pair of tiles. That costs shared-memory traffic of 3x V's bytes per tile, 176 KB in all with the MMAs'
@@ -44,8 +45,8 @@ constexpr int KT_THREADS = 384;
 constexpr int KT_WIDEN = 64;                           // threads that widen V
 constexpr int KT_STAGES = 3;
 constexpr int KT_SIDE = 8;                             // tiles whose page ids and scales are kept
-constexpr int KT_COST = 8;                             // what an item's start and end cost, in tiles (the trees
-                                                       // above: 141 us with 4, 134 with 6 and with 8, 138 with 12)
+constexpr int KT_COST = 8;                             // what an item's start and end cost, in tiles (measured on the
+                                                       // trees above alone: 141 us with 4, 134 with 6 and 8, 138 with 12)
 constexpr int KT_RING = 16;                            // pieces kept: the one found last is at most 7 ahead of the one written
 constexpr float KT_BIAS = 7.f;
 constexpr uint32_t TM_O = 384;

@@ -1,12 +1,16 @@
 """The caller-owned 8-bit paged cache and rotary positions (include/dflash.h): argument checks and
 marshalling around the library's kernels.
 
-One round of a verify loop, with nothing read back to the host:
+One round of a verify loop with blocks of `block` rows, with nothing read back to the host:
 
     plan = page_plan(ctx_len, n_new, block_table, free_list, n_free, max_rows)
     q, k = rope(rotary, plan["positions"], q, k)
     kv8_append(cache, k, v, plan["slot_map"])
-    out = kv8_attention(cache, q, plan["cu_rows"], plan["new_len"], block_table, mask="causal")
+    out = kv8_attention(cache, q, plan["cu_rows"], plan["new_len"], block_table, mask="causal", max_q=block)
+
+A draft tree's rows are planned and appended alike, but their positions are the context's length plus their
+depth, and the attention takes mask="tree" with ddtree_build's masks. The accepted path lies scattered among
+them: drop them all (page_plan with -rows), plan the path's rows and append these again from k and v.
 
 Calls run on the device of their tensors, on `stream` (default: that device's current stream), and
 allocate outputs that are not given from torch's allocator. Arguments that do not fit raise
@@ -287,7 +291,8 @@ def kv8_attention(cache, q, cu_q, ctx_len, block_table, mask="causal", tree_mask
     block_table[b] (dflash_kv8_attention). mask: "none", "causal", or "tree" with tree_mask [rows, words] int32
     (as ddtree_build's, flattened over its requests). scale: 1 / sqrt(head_dim) if None. max_q: the most rows
     of a request where the host knows it (default: q's rows), which steers the choice of kernel and nothing
-    else. workspace: a uint8 tensor of kv8_workspace(...) bytes; allocated for the call if None.
+    else; give it, for without it a batch of single tokens or short blocks goes to the kernel for many rows, which
+    takes up to 1.6 times as long there. workspace: a uint8 tensor of kv8_workspace(...) bytes; allocated for the call if None.
     Returns out [rows, heads, head_dim], or (out, lse [rows, heads] fp32) with want_lse."""
     a = _attn_args(cache, q, cu_q, ctx_len, block_table, mask, tree_mask, scale, max_q, out, lse)
     _no_gradient("kv8_attention", q, out, lse)

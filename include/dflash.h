@@ -467,10 +467,13 @@ dflash_status dflash_kv8_read(void *stream, const dflash_kv8_cache *cache, int32
  * A row that sees nothing gets out = 0 and lse = -infinity. What is stored at tokens that a row does
  * not see, NaN included, does not reach it. A row of q with an infinity or NaN gives NaN. Tokens on a
  * page outside [0, n_pages) are not seen. Rows past cu_q[n_req] stay as they were.
- * Sums, maxima and normalisers are fp32. bf16: q as it is (entries below 2^-14 of a row's largest may be off by
+ * Sums, maxima and normalisers are fp32. bf16: q as it is (entries below 2^-13 of a row's largest may be off by
  * 2^-21 of that), softmax weights rounded to 11 bits, one rounding of the output. fp32: operands split in
- * two 11-bit parts. Waits inside the kernels are bounded (2 s); rows whose wait ran out become NaN.
- *   max_q: the most rows of a request as far as the host knows; it only steers the choice of kernel.
+ * two 11-bit parts. Scores are to fit fp32, and V's scales of one request to lie within a factor 2^100 (the weights of
+ * tokens on pages of a much smaller scale would be lost). Waits inside the kernels are bounded (2 s); rows whose
+ * wait ran out become NaN.
+ *   max_q: the most rows of a request as far as the host knows; it only steers the choice of kernel (too large a
+ *   hint costs a batch of single tokens or short blocks up to 1.6 times the time).
  *   workspace: dflash_kv8_attention_workspace() bytes, 256-byte aligned; contents do not matter
  *   before or after. Calls that may overlap (two streams, two graphs) need one each.
  * Limits: n_q_heads a multiple of n_kv_heads, at most 8 per kv head; 1 <= n_req <= 4096; scale

@@ -623,6 +623,19 @@ def test_attention_zero_and_tiny_queries_over_zero_keys(dtype, mask, n_q, hint):
     _check_attn(c, table, q, cu, ctx, mask, tree, dtype, max_q=hint)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_q", [1, 20])
+def test_attention_value_scales_at_their_limit(dtype, n_q):
+    """Pages whose V scales lie a factor 2^100 apart, in either order: the small ones' tokens keep their weight."""
+    ctx = [1024, 333]
+    for order in (0, 1):
+        c, table, q, cu, tree = _attn_case(19 + order, ctx, [n_q, n_q], 1, 128, 4, "none", dtype, spread=0.5)
+        for b in range(2):
+            for i in range(R.pages_of(ctx[b])):
+                c["v_scale"][int(table[b, i])] = 2.0 ** (36 if (i + order) % 4 == 0 else -64)
+        _check_attn(c, table, q, cu, ctx, "none", tree, dtype, max_q=n_q)
+
+
 @pytest.mark.parametrize("hint", [0, 1, 16, 17, 10 ** 6])
 def test_attention_max_q_only_steers(hint):
     """Any max_q gives the rows of every request."""
