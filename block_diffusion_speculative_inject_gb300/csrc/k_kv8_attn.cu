@@ -16,7 +16,7 @@
 // V's page scale goes into the exponent (P carries s_v, the row sum divides it out again), so that
 // O of pages of very different scale adds up in one accumulator. f16 holds q exactly (bf16 times a
 // power of two per row, whose largest is at 2^14; entries below 2^-31 of it lose bits) and P to 11 bits with
-// its largest at 2^14, so P is normal down to 2^-28 of that. Rounded so, P adds half a percent to the error that the
+// its largest at 2^14, so P is normal down to 2^-28 of that. Rounded so, P adds 0.1% to the error that the
 // rounding of a bf16 output makes (1.650e-3 against 1.648e-3 of plain fp32, relative, 64 requests of one token).
 // For fp32, q and P are pairs of f16: off by 2^-23 of a value at most (2^-39 of the row's largest for small ones),
 // where fp32 itself rounds by 2^-24. Every product is two.

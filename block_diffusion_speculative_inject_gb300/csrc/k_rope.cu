@@ -150,7 +150,7 @@ cudaError_t launch_rope(const RopeArgs &a, bool inter, int width, cudaStream_t s
 using namespace dflash;
 
 namespace {
-// A double's 53 bits would leave position * 2^-54 turns, 6e-7 rad at 2^31. The table is made in sums of two doubles
+// A double's 53 bits would leave position * 2^-54 turns, 7e-7 rad at 2^31. The table is made in sums of two doubles
 // instead (over 100 bits), with error-free sums and products (Dekker 1971), the same on every host: products are
 // kept from being contracted into the sums that follow.
 struct Two {

@@ -292,7 +292,7 @@ def kv8_attention(cache, q, cu_q, ctx_len, block_table, mask="causal", tree_mask
     (as ddtree_build's, flattened over its requests). scale: 1 / sqrt(head_dim) if None. max_q: the most rows
     of a request where the host knows it (default: q's rows), which steers the choice of kernel and nothing
     else; give it, for without it a batch of single tokens or short blocks goes to the kernel for many rows, which
-    takes up to 1.6 times as long there. workspace: a uint8 tensor of kv8_workspace(...) bytes; allocated for the call if None.
+    takes 1.1 to 3 times as long there. workspace: a uint8 tensor of kv8_workspace(...) bytes; allocated for the call if None.
     Returns out [rows, heads, head_dim], or (out, lse [rows, heads] fp32) with want_lse."""
     a = _attn_args(cache, q, cu_q, ctx_len, block_table, mask, tree_mask, scale, max_q, out, lse)
     _no_gradient("kv8_attention", q, out, lse)

@@ -370,9 +370,10 @@ dflash_status dflash_ddtree_walk(void *stream, int32_t n_req, int32_t L, int32_t
  *   of tokens 64 i .. 64 i + 63; free_list [n_pages] int32, a stack whose first n_free[0] entries
  *   are the free pages (n_free [1] int32).
  * Given back pages (whole pages past the new end) are pushed in request order, as far as the stack's
- * n_pages entries go; then the requests that grow pop theirs off the top, in request order. A request is refused, and keeps its length,
- * when its new length needs more than max_blocks pages, when the pages asked for by it and the
- * requests before it are more than there are, or when their rows are more than max_rows.
+ * n_pages entries go; then the requests that grow pop theirs off the top, in request order. A request
+ * is refused, and keeps its length, when its new length needs more than max_blocks pages, when the
+ * pages asked for by it and the requests before it are more than there are, or when their rows are
+ * more than max_rows.
  *   Outputs: new_len [n_req], n_free_out [1], cu_rows [n_req + 1] (prefix sums of the rows that
  *   were granted), refused [n_req] (1 or 0), and for each new row in request order slot_map
  *   [max_rows] int64 = page * 64 + offset and positions [max_rows] int32; rows past the last
@@ -472,8 +473,8 @@ dflash_status dflash_kv8_read(void *stream, const dflash_kv8_cache *cache, int32
  * two 11-bit parts. Scores are to fit fp32, and V's scales of one request to lie within a factor 2^100 (the weights of
  * tokens on pages of a much smaller scale would be lost). Waits inside the kernels are bounded (2 s); rows whose
  * wait ran out become NaN.
- *   max_q: the most rows of a request as far as the host knows; it only steers the choice of kernel (too large a
- *   hint costs a batch of single tokens or short blocks up to 1.6 times the time).
+ *   max_q: the most rows of a request as far as the host knows; it only steers the choice of kernel (with too
+ *   large a hint a batch of single tokens or short blocks takes 1.1 to 3 times as long).
  *   workspace: dflash_kv8_attention_workspace() bytes, 256-byte aligned; contents do not matter
  *   before or after. Calls that may overlap (two streams, two graphs) need one each.
  * Limits: n_q_heads a multiple of n_kv_heads, at most 8 per kv head; 1 <= n_req <= 4096; scale
