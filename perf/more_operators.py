@@ -298,8 +298,8 @@ def prepare(case, seed):
         s.update(k_pages=pools[0], v_pages=pools[1], k_scale=pools[2], v_scale=pools[3], base_len=_i32(ctx),
                  n_keep=_i32(more), keep=_i32([p + [-1] * (width - len(p)) for p in paths]))
         if own:
-            from block_diffusion_speculative_inject_gb300 import KV8Cache
-            s["layer_caches"] = [KV8Cache(*(x[i] for x in pools)) for i in range(layers)]
+            from block_diffusion_speculative_inject_gb300 import KV8Cache, KV8Layers
+            s["layer_caches"] = KV8Layers(KV8Cache(*(x[i] for x in pools)) for i in range(layers))
         return s
     if op == "select":      # the pages themselves are not read
         kp = torch.empty((n_pages, nkv, PAGE, hd), dtype=torch.float8_e4m3fn, device=_dev())
