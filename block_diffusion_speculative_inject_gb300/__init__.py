@@ -16,7 +16,9 @@ Functions with the C names take torch tensors (device buffers) and Python ints:
 `Context` wraps the same calls as methods and allocates outputs when asked to.
 
 Without a context, for a cache that the caller owns (8-bit pages planned, written and read on
-the GPU): page_plan, Rope / rope, KV8Cache, kv8_append, kv8_read, kv8_attention.
+the GPU): page_plan, Rope / rope, qk_norm_rope (with its gradient), KV8Cache, kv8_append, kv8_read, kv8_attention;
+kv8_bounds and kv8_select choose the blocks of a long context that kv8_attention then reads alone; ddtree_path and
+kv8_compact move the accepted path of a draft tree to its place.
 """
 import ctypes
 
@@ -28,7 +30,9 @@ __all__ = ["DFlashError", "Context", "Limits", "dflash_create", "dflash_destroy"
            "dflash_inject_context", "dflash_inject_blocks", "dflash_draft_step", "dflash_verify_greedy",
            "dflash_release", "dflash_truncate", "dflash_context_len", "dflash_export_kv",
            "dflash_validate_config", "make_config", "library",
-           "KV8Cache", "Rope", "page_plan", "rope", "kv8_append", "kv8_read", "kv8_attention", "kv8_workspace"]
+           "KV8Cache", "KV8Layers", "Rope", "page_plan", "rope", "kv8_append", "kv8_read", "kv8_attention", "kv8_workspace",
+           "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_workspace", "kv8_bounds", "kv8_select",
+           "kv8_select_workspace", "kv8_compact", "ddtree_path"]
 
 
 class DFlashError(RuntimeError):
@@ -413,6 +417,26 @@ def ddtree_walk(tree, L, target_next, stream=None):
     return acc, toks, nxt
 
 
+def ddtree_path(tree, L, target_next, stream=None):
+    """The rows that ddtree_walk accepts (dflash_ddtree_path): (path [n, L + 1], n_path [n]) int32, the root's row 0 first, then
+    row j + 1 for each accepted node j, -1 after them. kv8_compact takes them as keep and n_keep."""
+    n, budget = _check("tree['tok']", tree["tok"], _I4, (None, None))
+    _check("tree['parent']", tree["parent"], _I4, (n, budget))
+    _check("tree['n_nodes']", tree["n_nodes"], _I4, (n,))
+    _check("target_next", target_next, _I4, (n, budget + 1))
+    if not (1 <= L <= 31 and 1 <= budget <= 1024):
+        raise DFlashError(-1, "L must be in [1, 31] and budget in [1, 1024]")
+    dev = _one_device(tree["tok"], tree["parent"], tree["n_nodes"], target_next)
+
+    def body(s):
+        path = torch.empty((n, L + 1), dtype=torch.int32, device=dev)
+        n_path = torch.empty((n,), dtype=torch.int32, device=dev)
+        _call("dflash_ddtree_path", s, n, L, budget, tree["tok"].data_ptr(), tree["parent"].data_ptr(),
+              tree["n_nodes"].data_ptr(), target_next.data_ptr(), path.data_ptr(), n_path.data_ptr())
+        return path, n_path
+    return _on(dev, stream, body)
+
+
 def dflash_release(ctx: Context, req_id):
     ctx.release(req_id)
 
@@ -429,5 +453,8 @@ def dflash_export_kv(ctx: Context, req_id, layer, pos0, n, stream=None):
     return ctx.export_kv(req_id, layer, pos0, n, stream=stream)
 
 
-from .kv8 import (KV8Cache, Rope, kv8_append, kv8_attention, kv8_read, kv8_workspace, page_plan,  # noqa: E402
-                  rope)
+from .kv8 import (_I4, KV8Cache, KV8Layers, Rope, _call, _on, kv8_append, kv8_attention, kv8_bounds, kv8_compact,  # noqa: E402
+                  kv8_read, kv8_select, kv8_select_workspace, kv8_workspace, page_plan, qk_norm_rope,
+                  qk_norm_rope_backward, qk_norm_rope_workspace, rope)
+from .kv8 import _device as _one_device  # noqa: E402
+from .kv8 import _tensor as _check  # noqa: E402

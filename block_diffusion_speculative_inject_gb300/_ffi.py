@@ -66,6 +66,23 @@ class KV8Attn(ctypes.Structure):
         ("workspace_bytes", ctypes.c_int64)]
 
 
+class KV8Choice(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_req", "rows", "n_q_heads", "max_blocks", "n_select", "keep_first",
+                                              "keep_last", "dtype")] + [
+        ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("cu_q", "ctx_len", "block_table", "bounds", "blocks", "workspace")] + [
+        ("workspace_bytes", ctypes.c_int64)]
+
+
+class QKNormRopeGrad(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n_q_heads", "n_k_heads", "head_dim", "dtype")] + [
+        ("eps", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("positions", "q_weight", "k_weight", "q", "k", "grad_q_out", "grad_k_out")] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "grad_q_out_stride", "grad_k_out_stride")] + [
+        (n, ctypes.c_void_p) for n in ("dq", "dk")] + [(n, ctypes.c_int64) for n in ("dq_stride", "dk_stride")] + [
+        (n, ctypes.c_void_p) for n in ("dq_weight", "dk_weight", "workspace")] + [("workspace_bytes", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -85,6 +102,7 @@ SIGNATURES = {
     "dflash_select_path": (_I32, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dflash_ddtree_build": (_I32, [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dflash_ddtree_walk": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "dflash_ddtree_path": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]),
     "dflash_verify_sample": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dflash_verify_sample_q": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dflash_select_sample": (_I32, [_P, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P, _P, _P, _P,
@@ -93,10 +111,19 @@ SIGNATURES = {
     "dflash_rope_init": (_I32, [ctypes.POINTER(RopeParams), ctypes.POINTER(RopeTable)]),
     "dflash_rope_apply": (_I32, [_P, ctypes.POINTER(RopeTable), _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _I64, _P,
                                  _I64, _P, _I64, _P, _I64]),
+    "dflash_qk_norm_rope": (_I32, [_P, ctypes.POINTER(RopeTable), _I32, _I32, _I32, _I32, _I32, _P, ctypes.c_float, _P, _P,
+                                   _P, _I64, _P, _I64, _P, _I64, _P, _I64]),
+    "dflash_qk_norm_rope_workspace": (_I64, []),
+    "dflash_qk_norm_rope_backward": (_I32, [_P, ctypes.POINTER(RopeTable), ctypes.POINTER(QKNormRopeGrad)]),
     "dflash_kv8_append": (_I32, [_P, ctypes.POINTER(KV8Cache), _I32, _I32, _P, _I64, _P, _I64, _P]),
     "dflash_kv8_read": (_I32, [_P, ctypes.POINTER(KV8Cache), _I32, _P, _P, _P]),
     "dflash_kv8_attention_workspace": (_I64, [ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Attn)]),
     "dflash_kv8_attention": (_I32, [_P, ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Attn)]),
+    "dflash_kv8_bounds": (_I32, [_P, ctypes.POINTER(KV8Cache), _P, _I32, _I32, _P, _P, _P]),
+    "dflash_kv8_select_workspace": (_I64, [ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Choice)]),
+    "dflash_kv8_select": (_I32, [_P, ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Choice)]),
+    "dflash_kv8_attention_blocks": (_I32, [_P, ctypes.POINTER(KV8Cache), ctypes.POINTER(KV8Attn), _P, _I32]),
+    "dflash_kv8_compact": (_I32, [_P, _I32, ctypes.POINTER(KV8Cache), _I32, _I32, _I32, _P, _P, _P, _P]),
     "dflash_release": (_I32, [_P, _I32]),
     "dflash_truncate": (_I32, [_P, _I32, _I32]),
     "dflash_context_len": (_I32, [_P, _I32, _I32P]),

@@ -176,19 +176,21 @@ __global__ void __launch_bounds__(DDT_THREADS) k_ddtree_build(int n, int L, int 
 
 // Greedy walk: target_next [n][budget + 1] (index 0: after the root, index i + 1: after node
 // i). Outputs accept_len [n], out_tokens [n][L + 1] (the matched tokens, the target's token
-// where the walk stopped, then -1), next_anchor [n]. One warp per request scans the nodes 32
+// where the walk stopped, then -1), next_anchor [n]; or (path not null) path [n][L + 1] (0, then
+// the accepted nodes + 1, then -1) and n_path [n] instead. One warp per request scans the nodes 32
 // at a time for the first child of the current node with the target's token.
 __global__ void __launch_bounds__(32) k_ddtree_walk(int n, int L, int budget, const int32_t *tree_tok,
                                                     const int32_t *tree_parent, const int32_t *n_nodes,
                                                     const int32_t *target_next, int32_t *accept_len,
-                                                    int32_t *out_tokens, int32_t *next_anchor) {
+                                                    int32_t *out_tokens, int32_t *next_anchor,
+                                                    int32_t *path, int32_t *n_path) {
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.x, lane = threadIdx.x;
   if (b >= n) return;
   const int32_t *tok = tree_tok + (size_t)b * budget, *par = tree_parent + (size_t)b * budget;
   const int32_t *tn = target_next + (size_t)b * (budget + 1);
-  int32_t *o = out_tokens + (size_t)b * (L + 1);
+  int32_t *o = (path ? path : out_tokens) + (size_t)b * (L + 1);
   const int nn = n_nodes[b];
   int cur = -1, a = 0;
   int32_t t = tn[0];
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(32) k_ddtree_walk(int n, int L, int budget, co
         break;
       }
     }
-    if (lane == 0) o[a] = t;
+    if (lane == 0) o[a] = path ? cur + 1 : t;
     if (child < 0 || a >= L) break;
     ++a;
     cur = child;
@@ -210,8 +212,12 @@ __global__ void __launch_bounds__(32) k_ddtree_walk(int n, int L, int budget, co
   }
   for (int j = a + 1 + lane; j <= L; j += 32) o[j] = -1;
   if (lane == 0) {
-    accept_len[b] = a;
-    next_anchor[b] = t;
+    if (path) {
+      n_path[b] = a + 1;
+    } else {
+      accept_len[b] = a;
+      next_anchor[b] = t;
+    }
   }
 }
 
@@ -274,6 +280,19 @@ extern "C" dflash_status dflash_ddtree_walk(void *stream, int32_t n_req, int32_t
     return DFLASH_ERR_INVALID_ARG;
   cudaError_t e = launch_pdl(k_ddtree_walk, dim3(n_req), dim3(32), 0, (cudaStream_t)stream,
                              (int)n_req, (int)L, (int)budget, tree_tok, tree_parent, n_nodes, target_next,
-                             accept_len, out_tokens, next_anchor);
+                             accept_len, out_tokens, next_anchor, (int32_t *)nullptr, (int32_t *)nullptr);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+extern "C" dflash_status dflash_ddtree_path(void *stream, int32_t n_req, int32_t L, int32_t budget,
+                                            const int32_t *tree_tok, const int32_t *tree_parent,
+                                            const int32_t *n_nodes, const int32_t *target_next, int32_t *path,
+                                            int32_t *n_path) {
+  if (n_req < 0 || L < 1 || L > 31 || budget < 1 || budget > DDT_MAX_BUDGET) return DFLASH_ERR_INVALID_ARG;
+  if (n_req == 0) return DFLASH_OK;
+  if (!tree_tok || !tree_parent || !n_nodes || !target_next || !path || !n_path) return DFLASH_ERR_INVALID_ARG;
+  cudaError_t e = launch_pdl(k_ddtree_walk, dim3(n_req), dim3(32), 0, (cudaStream_t)stream,
+                             (int)n_req, (int)L, (int)budget, tree_tok, tree_parent, n_nodes, target_next,
+                             (int32_t *)nullptr, (int32_t *)nullptr, (int32_t *)nullptr, path, n_path);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }

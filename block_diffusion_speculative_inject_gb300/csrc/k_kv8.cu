@@ -206,14 +206,6 @@ struct AppendArgs {
   float *kscale, *vscale;
 };
 
-// smallest e >= KV8_MIN_EXP with amax <= 448 * 2^e = 1.75 * 2^(e + 8), from amax's own bits
-__device__ __forceinline__ int scale_exp(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return max(e, KV8_MIN_EXP);
-}
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
 // The largest |x| of 16 bytes, NaN left out; and with infinities left out too.
 template <typename T>
 __device__ __forceinline__ float largest(const uint4 &q) {
@@ -236,12 +228,6 @@ __device__ __forceinline__ float largest_finite(const uint4 &q) {
     if (x <= 3.402823466e38f) big = fmaxf(big, x);
   }
   return big;
-}
-
-// four e4m3 bytes times a factor, rounded again
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
-  const float2 a = e4m3x2_to_f32(w), b = e4m3x2_to_f32(w >> 16);
-  return f32_to_e4m3x2(a.x * f, a.y * f) | f32_to_e4m3x2(b.x * f, b.y * f) << 16;
 }
 
 template <typename T, int HD>

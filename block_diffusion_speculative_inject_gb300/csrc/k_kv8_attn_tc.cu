@@ -67,6 +67,7 @@ struct KtLayout {
 
 struct KtSide {
   int page[2];                                         // -1: not there, nothing of it is seen
+  int block[2];                                        // of the context, where blocks are listed
   float ks[2], ev[2], iv[2];                           // K's scale, log2 of V's and 1 over it
 };
 
@@ -150,10 +151,10 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t *w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
-template <int HD>
+template <int HD, bool SEL>
 __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_constant__ KtParams p) {
   typedef KtLayout<HD> Lay;
-  typedef Kv8Tiles<KT_TOKENS, KT_ROWS, KT_COST> Tiles;
+  typedef Kv8Tiles<KT_TOKENS, KT_ROWS, KT_COST, SEL> Tiles;
   const Kv8AttnArgs &a = p.a;
   extern __shared__ uint8_t kt_raw[];
   const uint32_t raw = smem_u32(kt_raw), base = (raw + 1023u) & ~1023u;
@@ -193,11 +194,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
   pdl_wait();
   long long chunk, item_begin;
   Kv8Piece pc;
-  if (!kv8_start<KT_TOKENS, KT_ROWS, KT_COST>(a, sh.grp, blockIdx.x, gridDim.x, pc, chunk, item_begin)) {   // uniform for the CTA
+  if (!kv8_start<KT_TOKENS, KT_ROWS, KT_COST, SEL>(a, sh.grp, blockIdx.x, gridDim.x, pc, chunk, item_begin)) {   // uniform for the CTA
     if (threadIdx.x == 0) a.desc[blockIdx.x].pieces = 0;
     return;
   }
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = kv8_desc<KT_TOKENS, KT_ROWS, KT_COST>(a, pc, blockIdx.x, chunk, item_begin);
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = kv8_desc<KT_TOKENS, KT_ROWS, KT_COST, SEL>(a, pc, blockIdx.x, chunk, item_begin);
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
@@ -223,9 +224,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
     };
     // lane x: page x (and its scales) of 16 tiles of a piece, and of the 16 after them (of the next
     // piece's first), whose table entries and then scales are fetched while these are used
-    auto table = [&](const Kv8Piece &x, int from) {
+    auto table = [&](const Kv8Piece &x, int from, int &block) {
       const int pg = 2 * from + lane;
-      return (long long)pg * KV_PAGE < Tiles(a).limit(x.r, x.qt) && pg < 2 * x.u1 ? a.table[(size_t)x.b * a.width + pg] : -1;
+      if (!((long long)pg * KV_PAGE < Tiles(a).limit(x.r, x.qt) && pg < 2 * x.u1)) return -1;
+      if constexpr (SEL) return kv8_listed(a, x.r, x.b, x.h, pg, block);
+      return a.table[(size_t)x.b * a.width + pg];
     };
     auto scales = [&](int h, int &pg, float &k, float &v) {
       if (pg < 0 || pg >= a.n_pages) pg = -1;
@@ -236,7 +239,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       }
     };
     float ks, vs, next_ks = 1.f, next_vs = 1.f, piece_ks = 1.f, piece_vs = 1.f;
-    int page = table(pc, pc.u0), next_page = -1, piece_page = -1;
+    int block = 0, next_block = 0, piece_block = 0;
+    int page = table(pc, pc.u0, block), next_page = -1, piece_page = -1;
     publish(pc, 0);
     scales(pc.h, page, ks, vs);
     Kv8Piece nx = pc;
@@ -247,11 +251,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         if (u == tab_u + 16) {
           tab_u = u;
           page = next_page;
+          if constexpr (SEL) block = next_block;
           ks = next_ks;
           ev = log2f(next_vs);
           iv = 1.f / next_vs;
         }
-        if (u == tab_u + 4) next_page = table(pc, tab_u + 16);
+        if (u == tab_u + 4) next_page = table(pc, tab_u + 16, next_block);
         if (u == tab_u + 10) scales(pc.h, next_page, next_ks, next_vs);
         const int at = 2 * (u - tab_u), stg = i % KT_STAGES;
         const uint32_t use = i / KT_STAGES;
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         if (x == 0 || x == 1) {
           KtSide &sd = sh.side[i % KT_SIDE];
           sd.page[x] = page;
+          if constexpr (SEL) sd.block[x] = block;
           sd.ks[x] = ks;
           sd.ev[x] = ev;
           sd.iv[x] = iv;
@@ -284,9 +290,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         }
         if (pc.left > 0) {
           if (u == pc.u0) {
-            kv8_next_piece<KT_TOKENS, KT_ROWS, KT_COST>(a, nx);
+            kv8_next_piece<KT_TOKENS, KT_ROWS, KT_COST, SEL>(a, nx);
             publish(nx, pn + 1);
-            piece_page = table(nx, nx.u0);
+            piece_page = table(nx, nx.u0, piece_block);
           }
           if (u == min(pc.u0 + 1, pc.u1 - 1)) scales(nx.h, piece_page, piece_ks, piece_vs);
         }
@@ -294,6 +300,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
       if (!go || pc.left <= 0) break;
       pc = nx;
       page = piece_page;
+      if constexpr (SEL) block = piece_block;
       ks = piece_ks;
       vs = piece_vs;
     }
@@ -465,14 +472,15 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         // zero keys (scale 2^-64) would underflow. |S| is below 2^24, so a score moves by 2^-102 at most. (A maximum in
         // place of the sum, an instruction more on the way to P, cost 1% of the time.)
         const float c = fmaf(fac, sd.ks[half], 1.17549435e-38f), ev = sd.ev[half];
-        const bool partial = sd.page[half] < 0 || 2 * u + half >= open;
+        const int block = SEL ? sd.block[half] : 2 * u + half;     // of the context
+        const bool partial = sd.page[half] < 0 || block >= open;
         // S of my tokens, without what the row does not see
         auto load_s = [&](float *sc) {
           tmem_ld32(sa, sc);
           tmem_ld32(sa + 32, sc + 32);
           tmem_ld_wait();
           if (partial) {
-            const uint64_t see = live && sd.page[half] >= 0 ? kv8_visible(a, mine.r, tk, 2 * u + half) : 0;
+            const uint64_t see = live && sd.page[half] >= 0 ? kv8_visible(a, mine.r, tk, block) : 0;
             const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -616,10 +624,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
           uint32_t hit = 0;
           const int lim = Tiles(a).limit(pc.r, pc.qt);
 #pragma unroll 1
-          for (int x = max(2 * pc.u0, open); x < 2 * pc.u1 && (long long)x * KV_PAGE < lim; ++x) {
-            const int page = a.table[(size_t)pc.b * a.width + x];
-            if (page < 0 || page >= a.n_pages) continue;
-            const uint64_t see = kv8_visible(a, pc.r, tk, x);
+          for (int x = SEL ? 2 * pc.u0 : max(2 * pc.u0, open); x < 2 * pc.u1 && (long long)x * KV_PAGE < lim; ++x) {
+            int block = x;
+            const int page = SEL ? kv8_listed(a, pc.r, pc.b, pc.h, x, block) : a.table[(size_t)pc.b * a.width + x];
+            if (page < 0 || page >= a.n_pages || block < open) continue;
+            const uint64_t see = kv8_visible(a, pc.r, tk, block);
             const uint8_t *vb = a.vp + kv8_block(page, pc.h, a.nkv, HD);
 #pragma unroll 1
             for (int z = 0; z < 16 * KV_PAGE; ++z)
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
         keep(sh.ring[(pn + 1) % KT_RING]);
       } else {                                         // a wait ran out: the rows left become NaN all the same
         Kv8Piece nx = pc;
-        kv8_next_piece<KT_TOKENS, KT_ROWS, KT_COST>(a, nx);
+        kv8_next_piece<KT_TOKENS, KT_ROWS, KT_COST, SEL>(a, nx);
         keep(nx);
       }
       first = false;
@@ -686,10 +695,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
 #pragma unroll
           for (int j = 0; j < N; ++j) v[j] = lds128(src + KT_WIDEN * 16 * j);
           const int page = sh.side[i % KT_SIDE].page[x];
-          const long long end = (long long)(2 * u + x + 1) * KV_PAGE;
+          const int block = SEL ? sh.side[i % KT_SIDE].block[x] : 2 * u + x;
+          const long long end = (long long)(block + 1) * KV_PAGE;
           if (page < 0 || end > open) {
             // tokens that exist, from this thread's 16: the rest may be anything
-            const int tail = page < 0 ? 0 : pc.r.len - (2 * u + x) * KV_PAGE - 16 * (tid & 3);
+            const int tail = page < 0 ? 0 : pc.r.len - block * KV_PAGE - 16 * (tid & 3);
             uint32_t any = 0;                          // some row does not see some token: a NaN must not meet its zero weight
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -741,10 +751,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) k_kv8_attn_tiles(const __grid_c
 }
 
 namespace {
-template <int HD>
+template <int HD, bool SEL>
 cudaError_t launch(const KtParams &p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kt_smem<HD>());
-  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_tiles<HD>, dim3(KV8_SMS), dim3(KT_THREADS), kt_smem<HD>(), s, p);
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tiles<HD, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kt_smem<HD>());
+  if (e == cudaSuccess) e = launch_pdl(k_kv8_attn_tiles<HD, SEL>, dim3(KV8_SMS), dim3(KT_THREADS), kt_smem<HD>(), s, p);
   if (e == cudaSuccess)
     e = launch_pdl(k_kv8_combine<bf16, HD, KT_ROWS>, dim3(KV8_SMS - 1, 16), dim3(128), 0, s, p.a);
   return e;
@@ -770,7 +780,8 @@ cudaError_t launch_kv8_tiles(const Kv8AttnArgs &a, int hd, cudaStream_t s) {
                                   hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  return hd == 128 ? launch<128>(p, s) : launch<64>(p, s);
+  if (a.blocks) return hd == 128 ? launch<128, true>(p, s) : launch<64, true>(p, s);
+  return hd == 128 ? launch<128, false>(p, s) : launch<64, false>(p, s);
 }
 
 }  // namespace dflash

@@ -1,0 +1,420 @@
+// The choice of blocks for attention over a part of a long context (8-bit paged cache): bounds of a page's keys
+// (dflash_kv8_bounds) and the choice by the score that they give (dflash_kv8_select).
+#include "kv8_sched.cuh"
+
+namespace dflash {
+
+// ---------------------------------------------------------------- bounds
+// A warp per (page, kv head): lanes read 16 bytes of a row each, several rows at a time, and keep the least and the
+// largest of their 16 dims as f16 pairs (exact). Bound by the read of the pages.
+constexpr int KB_THREADS = 256;
+constexpr int KB_CTAS = 152 * 4;
+
+struct BoundsArgs {
+  int n_req, width, n_pages, nkv;
+  const int32_t *old_len, *new_len, *table;
+  const uint8_t *kp;
+  int8_t *bounds;
+};
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *(const __half2 *)&x; }
+
+template <int HD>
+__global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
+  extern __shared__ long long kb_pre[];               // [n_req + 1]: pages touched by the requests before
+  __shared__ long long warp_tot[KB_THREADS / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long cap = (long long)a.width * KV_PAGE;
+  auto lens = [&](int b, int &first, int &end) {      // rows [first, end) of request b
+    first = (int)max(0ll, min((long long)a.old_len[b], cap));
+    end = (int)max(0ll, min((long long)a.new_len[b], cap));
+  };
+  const int ipt = (a.n_req + KB_THREADS - 1) / KB_THREADS;
+  long long mine = 0;
+  for (int i = 0; i < ipt; ++i) {
+    const int b = tid * ipt + i;
+    if (b >= a.n_req) break;
+    int s, e;
+    lens(b, s, e);
+    if (e > s) mine += (e + KV_PAGE - 1) / KV_PAGE - s / KV_PAGE;
+  }
+  long long inc = warp_scan_ll(mine);
+  if (lane == 31) warp_tot[warp] = inc;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) inc += warp_tot[i];
+  long long run = inc - mine;
+  for (int i = 0; i < ipt; ++i) {
+    const int b = tid * ipt + i;
+    if (b >= a.n_req) break;
+    int s, e;
+    lens(b, s, e);
+    kb_pre[b] = run;
+    if (e > s) run += (e + KV_PAGE - 1) / KV_PAGE - s / KV_PAGE;
+  }
+  if (tid == KB_THREADS - 1) kb_pre[a.n_req] = inc;
+  __syncthreads();
+  const long long tasks = kb_pre[a.n_req] * a.nkv, step = (long long)gridDim.x * (KB_THREADS / 32);
+  constexpr int LPR = HD / 16, RPI = 32 / LPR;        // lanes of a row, rows at a time
+  for (long long t = (long long)blockIdx.x * (KB_THREADS / 32) + warp; t < tasks; t += step) {
+    const long long pg = t / a.nkv;
+    const int h = (int)(t - pg * a.nkv);
+    int lo = 0, hi = a.n_req - 1;                      // the last request whose pages begin at or before pg
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (kb_pre[m] <= pg) lo = m;
+      else hi = m - 1;
+    }
+    int s, e;
+    lens(lo, s, e);
+    const int blk = s / KV_PAGE + (int)(pg - kb_pre[lo]);
+    const int page = a.table[(size_t)lo * a.width + blk];
+    if (page < 0 || page >= a.n_pages) continue;
+    const int rows = min(KV_PAGE, e - blk * KV_PAGE);
+    const uint8_t *src = a.kp + kv8_block(page, h, a.nkv, HD) + lane * 16;
+    __half2 least[8], most[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      least[j] = as_half2(0x7c007c00u);
+      most[j] = as_half2(0xfc00fc00u);
+    }
+#pragma unroll 8
+    for (int r = 0; r < KV_PAGE; r += RPI) {
+      if (r + lane / LPR >= rows) continue;
+      const uint4 w = *(const uint4 *)(src + r * HD);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t p0, p1;
+        e4m3x4_to_f16(v[j], p0, p1);
+        least[2 * j] = __hmin2(least[2 * j], as_half2(p0));
+        most[2 * j] = __hmax2(most[2 * j], as_half2(p0));
+        least[2 * j + 1] = __hmin2(least[2 * j + 1], as_half2(p1));
+        most[2 * j + 1] = __hmax2(most[2 * j + 1], as_half2(p1));
+      }
+    }
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        least[j] = __hmin2(least[j], __shfl_xor_sync(0xffffffffu, least[j], o));
+        most[j] = __hmax2(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+      }
+    if (lane < 2 * LPR) {                              // the first row's lanes write the least, the second's the largest
+      const bool up = lane >= LPR;
+      uint32_t out[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 l = __half22float2(least[j]), m = __half22float2(most[j]);
+        const int x = l.x > m.x ? 0 : (int)(up ? ceilf(m.x * 0.25f) : floorf(l.x * 0.25f));
+        const int y = l.y > m.y ? 0 : (int)(up ? ceilf(m.y * 0.25f) : floorf(l.y * 0.25f));
+        out[j / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 8) << 16 * (j & 1);
+      }
+      *(uint4 *)(a.bounds + ((size_t)page * a.nkv + h) * (2 * HD) + lane * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- scores
+// score[block] = max over rows of (q+ . hi + q- . lo) unit * 4 scale, q+ = max(q, 0) and q- = min(q, 0) in whole
+// numbers of at most 1024: two m16n8k16 products of 16 blocks with 8 rows, in f16 with fp32 sums. Products are at most
+// 2^17 and the sums of a row at most 2^24, so every partial sum is a whole number that fp32 (and an accumulator that
+// truncates) holds. Contraction indices are permuted as in the attention for few rows: a lane's 16 bytes are the dims of
+// four steps.
+constexpr int KS_THREADS = 128;
+constexpr int KS_ROWS = 128;                          // rows of q staged at once
+
+struct SelectArgs {
+  Kv8AttnArgs a;
+  int n_select, first, last;
+  const int8_t *bounds;
+  float *score;                                       // [n_req][nkv][width]
+  int32_t *blocks;
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four signed bytes as two f16 pairs: byte + 128 in the low bits of 1024 + .., less 1152
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+  hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(KS_THREADS) k_kv8_scores(const SelectArgs x) {
+  constexpr int KS = HD / 16, C = HD / 64;
+  __shared__ uint2 qf[KS_ROWS / 8][KS][32];            // fragments of q
+  __shared__ float unit[KS_ROWS];                      // 0: a row that has no say
+  const Kv8AttnArgs &a = x.a;
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const Kv8Req r = kv8_req(a, b);
+  const int blocks = (r.len + KV_PAGE - 1) / KV_PAGE, group = a.nq / a.nkv;
+  if (r.n == 0 || blocks <= x.n_select || blockIdx.x * 64 >= blocks) return;
+  const long long rows = (long long)r.n * group;
+  float *score = x.score + ((size_t)b * a.nkv + h) * a.width;
+  for (long long r0 = 0; r0 < rows; r0 += KS_ROWS) {
+    // q in whole numbers: HD / 4 lanes a row, four dims each
+    constexpr int LPR = HD / 4;
+    const int here = (int)min((long long)KS_ROWS, rows - r0), tiles = (here + 7) / 8;
+    __syncthreads();
+    for (int i0 = 0; i0 < tiles * 8; i0 += KS_THREADS / LPR) {
+      const int i = i0 + threadIdx.x / LPR, l = threadIdx.x % LPR;
+      const bool live = i < here;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        const long long row = r0 + i;
+        const T *src = (const T *)a.q + (r.row0 + row / group) * a.q_stride + (int64_t)(h * group + row % group) * HD + 4 * l;
+        if constexpr (sizeof(T) == 2) {
+          const uint2 w = *(const uint2 *)src;
+          v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+          v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+          const float4 w = *(const float4 *)src;
+          v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        }
+      }
+      uint32_t top = 0;                               // bits of the largest magnitude: NaN and infinity are the largest
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool fin = top < 0x7f800000u;
+      // top = m 2^k, m in [1/2, 1): unit 2^(k - 10)
+      const int k = max((int)(top >> 23) - 126, -100);
+      const float up = __uint_as_float((uint32_t)(137 - k) << 23);
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const __half2 y = __floats2half2_rn(fin ? rintf(v[2 * j] * up) : 0.f, fin ? rintf(v[2 * j + 1] * up) : 0.f);
+        w[j] = *(const uint32_t *)&y;
+      }
+      // dims 4 l .. + 3 are word l & 3 of lane l / 4 & 3's 16 bytes in chunk l / 16
+      if (i < tiles * 8) {
+        qf[i / 8][l / 16 * 4 + (l & 3)][(i & 7) * 4 + (l >> 2 & 3)] = make_uint2(w[0], w[1]);
+        if (l == 0) unit[i] = live && fin ? __uint_as_float((uint32_t)(117 + k) << 23) : 0.f;
+      }
+    }
+    __syncthreads();
+    for (int p0 = blockIdx.x * 64 + warp * 16; p0 < blocks; p0 += gridDim.x * 64) {
+      int page[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int p = p0 + g + 8 * y;
+        page[y] = p < blocks ? a.table[(size_t)b * a.width + p] : -1;
+        if (page[y] >= a.n_pages) page[y] = -1;
+      }
+      uint32_t lo[KS][4], hi[KS][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int8_t *src = x.bounds + ((size_t)max(page[y], 0) * a.nkv + h) * (2 * HD) + 16 * t;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const uint4 l4 = page[y] >= 0 ? *(const uint4 *)(src + 64 * c) : make_uint4(0, 0, 0, 0);
+          const uint4 h4 = page[y] >= 0 ? *(const uint4 *)(src + HD + 64 * c) : make_uint4(0, 0, 0, 0);
+          const uint32_t lw[4] = {l4.x, l4.y, l4.z, l4.w}, hw[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            s8x4_to_f16(lw[s], lo[4 * c + s][y], lo[4 * c + s][2 + y]);
+            s8x4_to_f16(hw[s], hi[4 * c + s][y], hi[4 * c + s][2 + y]);
+          }
+        }
+      }
+      float best[2] = {-INFINITY, -INFINITY};
+      for (int n = 0; n < tiles; ++n) {
+        float up[4] = {0.f, 0.f, 0.f, 0.f}, dn[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint2 q = qf[n][k][lane];
+          const __half2 zero = as_half2(0);
+          const __half2 p0h = __hmax2(as_half2(q.x), zero), p1h = __hmax2(as_half2(q.y), zero);
+          const __half2 n0h = __hmin2(as_half2(q.x), zero), n1h = __hmin2(as_half2(q.y), zero);
+          mma_16816(up, hi[k], *(const uint32_t *)&p0h, *(const uint32_t *)&p1h);
+          mma_16816(dn, lo[k], *(const uint32_t *)&n0h, *(const uint32_t *)&n1h);
+        }
+        const float u0 = unit[8 * n + 2 * t], u1 = unit[8 * n + 2 * t + 1];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (u0 > 0.f) best[y] = fmaxf(best[y], (up[2 * y] + dn[2 * y]) * u0);
+          if (u1 > 0.f) best[y] = fmaxf(best[y], (up[2 * y + 1] + dn[2 * y + 1]) * u1);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        best[y] = fmaxf(best[y], __shfl_xor_sync(0xffffffffu, best[y], 1));
+        best[y] = fmaxf(best[y], __shfl_xor_sync(0xffffffffu, best[y], 2));
+        const int p = p0 + g + 8 * y;
+        if (t || p >= blocks) continue;
+        float v = page[y] < 0 ? -INFINITY : best[y] * (4.f * x.a.ks[(size_t)page[y] * a.nkv + h]);
+        if (!(v == v)) v = -INFINITY;
+        score[p] = r0 ? fmaxf(score[p], v) : v;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the n_select best
+// A CTA per (request, kv head). Keys rank as the scores do (fixed blocks above all); four passes over the keys' bytes,
+// each a histogram of the keys that agree with the threshold so far, find the last key that is taken and how many of
+// those equal to it; the chosen ones are then written in order.
+constexpr int KC_THREADS = 256;
+
+__global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
+  __shared__ int hist[256], warp_tot[KC_THREADS / 32 + 1];
+  __shared__ int s_bin, s_left;
+  const Kv8AttnArgs &a = x.a;
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Kv8Req r = kv8_req(a, b);
+  const int blocks = r.n ? (r.len + KV_PAGE - 1) / KV_PAGE : 0;
+  int32_t *out = x.blocks + ((size_t)b * a.nkv + h) * x.n_select;
+  if (blocks <= x.n_select) {
+    for (int i = tid; i < x.n_select; i += KC_THREADS) out[i] = i < blocks ? i : -1;
+    return;
+  }
+  const float *score = x.score + ((size_t)b * a.nkv + h) * a.width;
+  // floor((len - n) / 64) - last; the rows may be more than the context
+  const int d = r.len - r.n, own = (d >= 0 ? d / KV_PAGE : -((-d + KV_PAGE - 1) / KV_PAGE)) - x.last;
+  auto key = [&](int j) {
+    if (j < x.first || j >= own) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(score[j] + 0.f);                 // (-0 as 0)
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+  };
+  uint32_t prefix = 0;
+  int left = x.n_select;                               // of the keys that begin with prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += KC_THREADS) hist[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < blocks; j += KC_THREADS) {
+      const uint32_t k = key(j);
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[k >> shift & 255], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {                                   // from the top: the bin where the count passes left
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+      int inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      int before = inc - sum;
+      if (before < left && inc >= left) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < left && before + c[i] >= left) {
+            s_bin = 255 - 8 * lane - i;
+            s_left = left - before;
+          }
+          before += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)s_bin << shift;
+    left = s_left;
+    __syncthreads();
+  }
+  // keys above prefix, and the first `left` equal to it
+  int done = 0, equal = 0;
+  for (int j0 = 0; j0 < blocks; j0 += KC_THREADS) {
+    const int j = j0 + tid;
+    const uint32_t k = j < blocks ? key(j) : 0;
+    const bool eq = j < blocks && k == prefix, over = j < blocks && k > prefix;
+    const unsigned be = __ballot_sync(0xffffffffu, eq), bo = __ballot_sync(0xffffffffu, over), lt = (1u << lane) - 1;
+    if (lane == 0) warp_tot[warp] = __popc(be) | __popc(bo) << 16;
+    __syncthreads();
+    int tot = 0, mine = 0;
+#pragma unroll
+    for (int i = 0; i < KC_THREADS / 32; ++i) {
+      if (i == warp) mine = tot;
+      tot += warp_tot[i];
+    }
+    const int e = equal + (mine & 0xffff) + __popc(be & lt), o = (mine >> 16) + __popc(bo & lt);
+    // equal ones before this one that are taken
+    if (over || (eq && e < left)) out[done + o + min(e, left) - min(equal, left)] = j;
+    const int all = equal + (tot & 0xffff);
+    done += (tot >> 16) + min(all, left) - min(equal, left);
+    equal = all;
+    __syncthreads();
+  }
+}
+
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" dflash_status dflash_kv8_bounds(void *stream, const dflash_kv8_cache *c, int8_t *bounds, int32_t n_req,
+                                           int32_t max_blocks, const int32_t *old_len, const int32_t *new_len,
+                                           const int32_t *block_table) {
+  if (!kv8_cache_ok(c) || n_req < 1 || n_req > KV8_MAX_REQ || max_blocks < 1 || max_blocks > (1 << 24) || !bounds ||
+      !aligned(bounds, 16) || !old_len || !new_len || !block_table || !aligned(old_len, 4) || !aligned(new_len, 4) ||
+      !aligned(block_table, 4))
+    return DFLASH_ERR_INVALID_ARG;
+  const BoundsArgs a{n_req, max_blocks, c->n_pages, c->n_kv_heads, old_len, new_len, block_table,
+                     (const uint8_t *)c->k_pages, bounds};
+  const int64_t most = ((int64_t)n_req * max_blocks * c->n_kv_heads + KB_THREADS / 32 - 1) / (KB_THREADS / 32);
+  const dim3 g((unsigned)(most < KB_CTAS ? most : KB_CTAS)), t(KB_THREADS);
+  const size_t sm = (size_t)(n_req + 1) * sizeof(long long);
+  const cudaError_t e = c->head_dim == 128 ? launch_pdl(k_kv8_bounds<128>, g, t, sm, (cudaStream_t)stream, a)
+                                           : launch_pdl(k_kv8_bounds<64>, g, t, sm, (cudaStream_t)stream, a);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+namespace {
+bool choice_ok(const dflash_kv8_cache *c, const dflash_kv8_choice *x) {
+  constexpr int most = 1 << 24;
+  if (!c || !x || c->n_pages < 1 || c->n_pages > most || c->n_kv_heads < 1 || c->n_kv_heads > 128 ||
+      (c->head_dim != 64 && c->head_dim != 128) || x->n_req < 1 || x->n_req > KV8_MAX_REQ || x->rows < 0 ||
+      x->n_q_heads < 1 || x->n_q_heads % c->n_kv_heads || x->n_q_heads / c->n_kv_heads > 8 || x->max_blocks < 1 ||
+      x->max_blocks > most || x->n_select < 1 || x->n_select > most || x->keep_first < 0 || x->keep_first > most ||
+      x->keep_last < 0 || x->keep_last > most || (x->dtype != DFLASH_F32 && x->dtype != DFLASH_BF16))
+    return false;
+  return (int64_t)x->n_req * c->n_kv_heads * x->n_select < (1ll << 31) &&
+         x->q_stride >= (int64_t)x->n_q_heads * c->head_dim && x->q_stride % (16 / dtype_bytes(x->dtype)) == 0;
+}
+template <typename T>
+cudaError_t launch_select(const SelectArgs &x, int hd, cudaStream_t s) {
+  // CTAs of a (request, kv head), which take 64 blocks at a time in turn
+  const long items = (long)x.a.n_req * x.a.nkv, want = (152 * 4 + items - 1) / items;
+  const long most = ((long)x.a.width + 63) / 64;
+  const dim3 g((unsigned)(want < most ? want : most), x.a.nkv, x.a.n_req), t(KS_THREADS);
+  cudaError_t e = cudaSuccess;
+  if (x.a.width > x.n_select)
+    e = hd == 128 ? launch_pdl(k_kv8_scores<T, 128>, g, t, 0, s, x) : launch_pdl(k_kv8_scores<T, 64>, g, t, 0, s, x);
+  if (e == cudaSuccess) e = launch_pdl(k_kv8_choose, dim3(x.a.nkv, x.a.n_req), dim3(KC_THREADS), 0, s, x);
+  return e;
+}
+}  // namespace
+
+extern "C" int64_t dflash_kv8_select_workspace(const dflash_kv8_cache *c, const dflash_kv8_choice *x) {
+  if (!choice_ok(c, x)) return -1;
+  return (int64_t)x->n_req * c->n_kv_heads * x->max_blocks * (int64_t)sizeof(float);
+}
+
+extern "C" dflash_status dflash_kv8_select(void *stream, const dflash_kv8_cache *c, const dflash_kv8_choice *x) {
+  if (!choice_ok(c, x) || !c->k_scale || !aligned(c->k_scale, 4)) return DFLASH_ERR_INVALID_ARG;
+  if (!x->cu_q || !x->ctx_len || !x->block_table || !x->bounds || !x->blocks || !x->workspace || (x->rows && !x->q) ||
+      !aligned(x->cu_q, 4) || !aligned(x->ctx_len, 4) || !aligned(x->block_table, 4) || !aligned(x->bounds, 16) ||
+      !aligned(x->blocks, 4) || !aligned(x->workspace, 256) || !aligned(x->q, 16) ||
+      x->workspace_bytes < dflash_kv8_select_workspace(c, x))
+    return DFLASH_ERR_INVALID_ARG;
+  SelectArgs s{};
+  s.a.n_req = x->n_req, s.a.rows = x->rows, s.a.nq = x->n_q_heads, s.a.nkv = c->n_kv_heads, s.a.width = x->max_blocks;
+  s.a.n_pages = c->n_pages, s.a.q = x->q, s.a.q_stride = x->q_stride;
+  s.a.cu_q = x->cu_q, s.a.ctx_len = x->ctx_len, s.a.table = x->block_table, s.a.ks = c->k_scale;
+  s.n_select = x->n_select, s.first = x->keep_first, s.last = x->keep_last;
+  s.bounds = x->bounds, s.score = (float *)x->workspace, s.blocks = x->blocks;
+  const cudaError_t e = x->dtype == DFLASH_BF16 ? launch_select<bf16>(s, c->head_dim, (cudaStream_t)stream)
+                                                : launch_select<float>(s, c->head_dim, (cudaStream_t)stream);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}

@@ -9,7 +9,7 @@
 // row's pairs (at most 128) are computed once in shared memory and used by all of its heads.
 #include <cmath>
 
-#include "kv8.cuh"
+#include "rope.cuh"
 
 namespace dflash {
 
@@ -23,31 +23,6 @@ struct RopeArgs {
   const void *q, *k;
   void *qo, *ko;
   int64_t qs, ks, qos, kos;
-};
-
-// (cos, sin) of a phase in units of 2^-64 turns: the nearest quarter turn is split off exactly,
-// the rest, at most an eighth of a turn, goes to sincospif
-__device__ __forceinline__ float2 phase_cs(uint64_t ph) {
-  const uint32_t quarter = (uint32_t)((ph + (1ull << 61)) >> 62);
-  const int64_t rest = (int64_t)(ph - ((uint64_t)quarter << 62));
-  float s, c;
-  sincospif((float)rest * 0x1p-63f, &s, &c);
-  if (quarter & 1) {
-    const float t = c;
-    c = -s;
-    s = t;
-  }
-  return (quarter & 2) ? make_float2(-c, -s) : make_float2(c, s);
-}
-
-// the turned pair; one contraction for every instance, so that all of them give the same bits
-__device__ __forceinline__ float2 turned(float x, float y, float2 k) {
-  return make_float2(fmaf(x, k.x, -__fmul_rn(y, k.y)), fmaf(y, k.x, __fmul_rn(x, k.y)));
-}
-
-template <typename T, int N>
-struct alignas(N * sizeof(T)) Vec {
-  T v[N];
 };
 
 // A CTA turns one row; V elements per access (16 or 8 bytes, or two elements or one where a row, a

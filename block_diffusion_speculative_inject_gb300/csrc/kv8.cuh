@@ -57,6 +57,20 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// smallest e >= KV8_MIN_EXP with amax <= 448 * 2^e = 1.75 * 2^(e + 8), from amax's own bits
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, KV8_MIN_EXP);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// four e4m3 bytes times a factor, rounded again
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+  const float2 a = e4m3x2_to_f32(w), b = e4m3x2_to_f32(w >> 16);
+  return f32_to_e4m3x2(a.x * f, a.y * f) | f32_to_e4m3x2(b.x * f, b.y * f) << 16;
+}
+
 inline bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 inline int dtype_bytes(int dtype) { return dtype == DFLASH_BF16 ? 2 : 4; }
 

@@ -117,5 +117,7 @@ __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile
 // The kernel for many query rows (bf16): tiles of 128 rows, one worker per SM.
 constexpr int KT_ROWS = 128;
 cudaError_t launch_kv8_tiles(const Kv8AttnArgs &a, int hd, cudaStream_t s);
+// The kernel for few rows over listed blocks (rows: 8 or 16 of a tile; wide: bf16).
+cudaError_t launch_kv8_rows_listed(const Kv8AttnArgs &a, bool wide, int hd, int rows, cudaStream_t s);
 
 }  // namespace dflash

@@ -34,6 +34,9 @@ struct Kv8AttnArgs {
   // workspace: one descriptor per worker, then two partial results per worker
   struct Kv8Desc *desc;
   float *part_o, *part_ml;     // [2 workers][M][hd], [2 workers][M][2] (max in log2 units, sum)
+  // attention over listed blocks: [n_req][nkv][n_blocks] indices into a request's table row
+  const int32_t *blocks;
+  int n_blocks;
 };
 
 // What the merge needs to know of a worker's first piece: 0 pieces unless it continues an item that the worker
@@ -79,15 +82,19 @@ __device__ __forceinline__ Kv8Req kv8_req(const Kv8AttnArgs &a, int b) {
   return r;
 }
 
-// Tokens of a tile, tokens it may see, units: M rows of a tile hold M / group tokens.
-template <int U, int M, int C>
+// Tokens of a tile, tokens it may see, units: M rows of a tile hold M / group tokens. SEL: over listed blocks. A request
+// has as many as its context, n_blocks at most, and every tile walks all of its list, whose entries take the place of
+// the context's pages.
+template <int U, int M, int C, bool SEL = false>
 struct Kv8Tiles {
-  int tpt, nkv, causal;
+  int tpt, nkv, causal, n_blocks;
   __device__ __forceinline__ Kv8Tiles(const Kv8AttnArgs &a)
-      : tpt(M / (a.nq / a.nkv)), nkv(a.nkv), causal(a.mask == DFLASH_MASK_CAUSAL) {}
+      : tpt(M / (a.nq / a.nkv)), nkv(a.nkv), causal(!SEL && a.mask == DFLASH_MASK_CAUSAL), n_blocks(SEL ? a.n_blocks : 0) {}
   __device__ __forceinline__ int tiles(const Kv8Req &r) const { return (r.n + tpt - 1) / tpt; }
   // the tokens [0, limit) hold all that some row of the tile sees
+  // (SEL: as many tokens as the list's entries hold)
   __device__ __forceinline__ int limit(const Kv8Req &r, int qt) const {
+    if constexpr (SEL) return min((r.len + KV_PAGE - 1) / KV_PAGE, n_blocks) * KV_PAGE;
     return causal ? max(0, (int)min((long long)r.len, (long long)r.len - r.n + min((long long)(qt + 1) * tpt, (long long)r.n)))
                   : r.len;
   }
@@ -132,10 +139,10 @@ __device__ __forceinline__ long long warp_scan_ll(long long x) {       // inclus
 // The start of worker `me` of `workers`: false if it has nothing to do. The whole CTA calls it (s_grp is for more
 // than 32 requests only); chunk gets a worker's length of the line, item_begin where the first
 // piece's item begins. For up to 32 requests every warp sums them up by itself, without a barrier.
-template <int U, int M, int C>
+template <int U, int M, int C, bool SEL = false>
 __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp, int me, int workers, Kv8Piece &p,
                                           long long &chunk, long long &item_begin) {
-  const Kv8Tiles<U, M, C> tl(a);
+  const Kv8Tiles<U, M, C, SEL> tl(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (a.n_req + 31) / 32;
   long long total = 0;
@@ -237,13 +244,13 @@ __device__ __forceinline__ bool kv8_start(const Kv8AttnArgs &a, long long *s_grp
 }
 
 // The descriptor of worker `me`, whose first piece is p.
-template <int U, int M, int C>
+template <int U, int M, int C, bool SEL = false>
 __device__ __forceinline__ Kv8Desc kv8_desc(const Kv8AttnArgs &a, const Kv8Piece &p, int me, long long chunk, long long item_begin) {
   Kv8Desc d{0, 0, 0, 0, 0, {0, 0, 0}};
   const long long pos = me * chunk;
   const long long begin = item_begin + C;              // the item's first unit
   if (begin < pos && begin >= pos - chunk) {
-    const Kv8Tiles<U, M, C> tl(a);
+    const Kv8Tiles<U, M, C, SEL> tl(a);
     d.pieces = (int)div_ll(begin + p.units - 1, chunk) - me + 2;       // up to the worker of the last unit
     d.slot0 = 2 * (me - 1) + (item_begin <= pos - chunk ? 0 : 1);
     d.row0 = p.r.row0 + p.qt * tl.tpt;
@@ -254,9 +261,9 @@ __device__ __forceinline__ Kv8Desc kv8_desc(const Kv8AttnArgs &a, const Kv8Piece
 }
 
 // The next piece of the same worker; p.left > 0.
-template <int U, int M, int C>
+template <int U, int M, int C, bool SEL = false>
 __device__ __forceinline__ void kv8_next_piece(const Kv8AttnArgs &a, Kv8Piece &p) {
-  const Kv8Tiles<U, M, C> tl(a);
+  const Kv8Tiles<U, M, C, SEL> tl(a);
   if (++p.h == a.nkv) {
     p.h = 0;
     if (++p.qt == tl.tiles(p.r)) {
@@ -276,6 +283,16 @@ __device__ __forceinline__ void kv8_next_piece(const Kv8AttnArgs &a, Kv8Piece &p
   p.u1 = (int)min((long long)p.units, p.left - C);
   p.left -= C + p.u1;
   if (p.left <= C) p.left = 0;
+}
+
+// The page that entry u of the list of (request b, kv head h) names, -1 if none, and its block in `block`.
+__device__ __forceinline__ int kv8_listed(const Kv8AttnArgs &a, const Kv8Req &r, int b, int h, int u, int &block) {
+  block = a.blocks[((size_t)b * a.nkv + h) * a.n_blocks + u];
+  if (block < 0 || (long long)block * KV_PAGE >= r.len) {
+    block = 0;
+    return -1;
+  }
+  return a.table[(size_t)b * a.width + block];
 }
 
 // Which of the 64 tokens of page `page_no` the row of `token` (index among the request's rows) sees,

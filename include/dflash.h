@@ -356,6 +356,14 @@ dflash_status dflash_ddtree_walk(void *stream, int32_t n_req, int32_t L, int32_t
                                  const int32_t *n_nodes, const int32_t *target_next,
                                  int32_t *accept_len, int32_t *out_tokens, int32_t *next_anchor);
 
+/* The rows that dflash_ddtree_walk accepts, for dflash_kv8_compact: path [n_req, L+1] holds 0 (the root), then
+ * j + 1 for each accepted node j in order (rising), then -1; n_path [n_req] how many there are, accept_len + 1.
+ * Inputs, limits and errors as dflash_ddtree_walk's. */
+dflash_status dflash_ddtree_path(void *stream, int32_t n_req, int32_t L, int32_t budget,
+                                 const int32_t *tree_tok, const int32_t *tree_parent,
+                                 const int32_t *n_nodes, const int32_t *target_next,
+                                 int32_t *path, int32_t *n_path);
+
 /* ---- The 8-bit paged cache: caller-owned pages, planned, written and read on the GPU ----
  * The context above owns its cache and plans its pages on the host. The calls below serve a
  * cache that the caller owns (a target model's, or a draft's of its own): block tables and slot
@@ -427,6 +435,41 @@ dflash_status dflash_rope_apply(void *stream, const dflash_rope *rope, int32_t r
                                 int32_t n_k_heads, int32_t head_dim, dflash_dtype dtype, const int32_t *positions,
                                 int32_t transpose, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                                 void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride);
+
+/* Per-head RMSNorm of queries and keys with the rotary positions in the same pass: every head x [head_dim] of q
+ * and of k becomes the rotation of x / sqrt(mean(x^2) + eps) * weight by its row's position. Arguments as
+ * dflash_rope_apply's (q_out / k_out may be q / k themselves, with the same stride; k may be NULL, and k_weight then is not
+ * read), q_weight and k_weight [head_dim] of `dtype`, eps > 0. Computed in fp32 from the stored values, rounded
+ * once; the squares of a head are to fit fp32.
+ *
+ * dflash_qk_norm_rope_backward: the gradients of q, k and of both weights from those of q_out and k_out. q, k are the
+ * call's inputs before it (an in-place call has overwritten them). With y the gradient of a head's output, R its rotation,
+ *   n = R^T y, g = n * weight, r = 1 / sqrt(mean(x^2) + eps):
+ *   dx = r (g - x r^2 mean(g x)), dweight = sum over rows and heads of n x r.
+ *   grad_q_out / grad_k_out, dq / dk: of dtype, rows of their own strides; dq / dk may be grad_q_out / grad_k_out (same stride).
+ *   dq_weight, dk_weight [head_dim] fp32 (dk_weight untouched without k): overwritten, the same bits for the same inputs.
+ *   workspace: dflash_qk_norm_rope_workspace() bytes, 256-byte aligned; calls that may overlap need one each. */
+dflash_status dflash_qk_norm_rope(void *stream, const dflash_rope *rope, int32_t rows, int32_t n_q_heads,
+                                  int32_t n_k_heads, int32_t head_dim, dflash_dtype dtype, const int32_t *positions,
+                                  float eps, const void *q_weight, const void *k_weight, const void *q,
+                                  int64_t q_stride, const void *k, int64_t k_stride, void *q_out,
+                                  int64_t q_out_stride, void *k_out, int64_t k_out_stride);
+typedef struct {
+  int32_t rows, n_q_heads, n_k_heads, head_dim;
+  dflash_dtype dtype;
+  float eps;
+  const int32_t *positions;
+  const void *q_weight, *k_weight;
+  const void *q, *k, *grad_q_out, *grad_k_out;
+  int64_t q_stride, k_stride, grad_q_out_stride, grad_k_out_stride;
+  void *dq, *dk;
+  int64_t dq_stride, dk_stride;
+  float *dq_weight, *dk_weight;
+  void *workspace;
+  int64_t workspace_bytes;
+} dflash_qk_norm_rope_grad;
+int64_t dflash_qk_norm_rope_workspace(void);
+dflash_status dflash_qk_norm_rope_backward(void *stream, const dflash_rope *rope, const dflash_qk_norm_rope_grad *args);
 
 /* A cache in 8 bits (e4m3), one scale per page of 64 tokens and kv head for K and for V:
  *   k_pages [n_pages, n_kv_heads, 64, head_dim], v_pages [n_pages, n_kv_heads, head_dim, 64] (V is
@@ -502,6 +545,75 @@ typedef struct {
  * Pointers are not looked at. */
 int64_t dflash_kv8_attention_workspace(const dflash_kv8_cache *cache, const dflash_kv8_attn *args);
 dflash_status dflash_kv8_attention(void *stream, const dflash_kv8_cache *cache, const dflash_kv8_attn *args);
+
+/* ---- Attention over chosen blocks of a long context: bounds of each page's keys, a choice of blocks by a score that
+ * the bounds give, and the attention over the chosen blocks alone.
+ *
+ * Bounds: int8 [n_pages, n_kv_heads, 2, head_dim], the caller's. For a page and head, with b the stored bytes' values
+ * (|b| <= 448) of its rows, [0][d] = floor(min b_d / 4) and [1][d] = ceil(max b_d / 4): 4 * bound * k_scale bounds
+ * the keys. NaN bytes are left out (a dim of nothing else: 0 and 0).
+ * dflash_kv8_bounds: makes those of every page that holds a token of [old_len[b], new_len[b]) of request b anew, from
+ * its rows below new_len[b] (so: after an append of those tokens, with dflash_page_plan's lengths; old_len 0 for the
+ * whole context). Tokens that a request gives up leave bounds that are still bounds until the next append there.
+ * old_len, new_len [n_req] int32, read as within [0, 64 max_blocks]; pages outside [0, n_pages) are skipped. Requests that share
+ * a page must agree on its rows. bounds 16-byte aligned. */
+dflash_status dflash_kv8_bounds(void *stream, const dflash_kv8_cache *cache, int8_t *bounds, int32_t n_req,
+                                int32_t max_blocks, const int32_t *old_len, const int32_t *new_len,
+                                const int32_t *block_table);
+
+/* Chooses blocks of 64 tokens for each request and kv head: blocks [n_req, n_kv_heads, n_select] int32, indices into the
+ * request's row of block_table, rising, then -1. A request of `len` tokens has P = ceil(len / 64) blocks and min(P, n_select)
+ * of them are chosen (none where it has no rows):
+ *   first those with index < keep_first or >= floor((len - n) / 64) - keep_last, n its rows: those that hold its own rows (the
+ *   context's last n tokens) and keep_last before them;
+ *   then by falling score; ties, and more of the first kind than n_select, go to the lowest index.
+ * The score of a block is the largest over the request's rows and the kv head's query heads of
+ *   sum_d max(x_d lo_d, x_d hi_d) * unit * 4 * k_scale,
+ * x = round(q / unit) (to even), unit the power of two with 512 <= max |x| <= 1024 (2^-110 at least): with bounds as
+ * dflash_kv8_bounds makes them the largest product q k that the block can hold, up to q's rounding to 11 bits. The sum is an integer
+ * of at most 2^24 and exact, so the choice depends on nothing but the inputs. Rows with an infinity or NaN have no
+ * say; a block whose page is outside [0, n_pages) scores -infinity. Scores are to fit fp32's normal range or be zero.
+ * Only cache->k_scale is read of the cache.
+ *   workspace: dflash_kv8_select_workspace() bytes, 256-byte aligned; contents do not matter before or after. Calls that may
+ *   overlap need one each.
+ * Limits: as dflash_kv8_attention's for n_req, max_blocks, heads and q; n_select in [1, 2^24], keep_first and keep_last in
+ * [0, 2^24]; the blocks hold fewer than 2^31 entries. */
+typedef struct {
+  int32_t n_req, rows, n_q_heads, max_blocks, n_select, keep_first, keep_last;
+  dflash_dtype dtype;
+  const void *q;
+  int64_t q_stride;
+  const int32_t *cu_q, *ctx_len, *block_table;
+  const int8_t *bounds;
+  int32_t *blocks;
+  void *workspace;
+  int64_t workspace_bytes;
+} dflash_kv8_choice;
+/* Bytes of workspace for these arguments (host only; -1: invalid arguments). Pointers are not looked at. */
+int64_t dflash_kv8_select_workspace(const dflash_kv8_cache *cache, const dflash_kv8_choice *args);
+dflash_status dflash_kv8_select(void *stream, const dflash_kv8_cache *cache, const dflash_kv8_choice *args);
+
+/* dflash_kv8_attention over the listed blocks only: a token is seen if the mask lets it be seen and its block is among
+ * the first min(n_blocks, ceil(ctx_len[b] / 64)) entries of blocks[b][kv head] ([n_req, n_kv_heads, n_blocks] int32, as
+ * dflash_kv8_select makes them; entries outside [0, ceil(ctx_len[b] / 64)) name nothing). A block is to be listed once: twice, it
+ * counts twice. Everything else, the workspace too, is dflash_kv8_attention's. n_blocks in [1, 2^24]. */
+dflash_status dflash_kv8_attention_blocks(void *stream, const dflash_kv8_cache *cache, const dflash_kv8_attn *args,
+                                          const int32_t *blocks, int32_t n_blocks);
+
+/* Moves the kept rows of each request's end down over the others, in place, in n_layers caches at once (the layers of a
+ * model: caches of the same n_pages, n_kv_heads and head_dim, a HOST array, that share the block table): token
+ * base_len[b] + keep[b][j] goes to base_len[b] + j, for j < n_keep[b], as if its rows were read (dflash_kv8_read) and
+ * then appended there (dflash_kv8_append): values move exactly but where a page's larger scale rounds small ones anew. After a draft
+ * tree of which the path keep (dflash_ddtree_path) is accepted, base_len is the length before the tree; dflash_page_plan
+ * with n_new = n_keep - rows then gives the rest back, and dflash_kv8_bounds from base_len to base_len + n_keep brings the
+ * bounds up to date.
+ *   base_len, n_keep [n_req], keep [n_req, max_keep] int32, rising, 0 <= keep[b][j] (else the rows' order is
+ *   not defined); n_keep is read as within [0, max_keep]. Rows whose token or place lies past the table or on a page outside
+ *   [0, n_pages) are skipped. The pages written must belong to one request.
+ * Limits: 1 <= n_layers <= 128, 1 <= n_req <= 4096, max_keep in [1, 2^24], max_blocks in [1, 2^24]. */
+dflash_status dflash_kv8_compact(void *stream, int32_t n_layers, const dflash_kv8_cache *caches, int32_t n_req,
+                                 int32_t max_blocks, int32_t max_keep, const int32_t *base_len, const int32_t *keep,
+                                 const int32_t *n_keep, const int32_t *block_table);
 
 /* Forgets a request and returns its pages to the pool (host only). Work already
  * enqueued that reads those pages must precede any later call in stream order. */
