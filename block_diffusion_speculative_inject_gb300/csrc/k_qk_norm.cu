@@ -5,8 +5,7 @@
 //
 // Every element is read and written once, which bounds both. A head belongs to G lanes of a warp (the smallest
 // power of two that its chunks need, at most 32), which hold it in registers between the sum of squares and the
-// rotation; a chunk is V dims and, in the half layout, their partners, or the V dims that follow. Sines and
-// cosines of a row are made once, in shared memory, for all of its heads.
+// rotation; a chunk is V dims and, in the half layout, their partners, or the V dims that follow.
 #include <cmath>
 
 #include "rope.cuh"
@@ -14,13 +13,16 @@
 namespace dflash {
 
 constexpr int QN_THREADS = 256;
-constexpr int QN_CTAS = 152 * 4;                      // CTAs of the gradient, one partial sum of the weights' each
+constexpr int QN_CTAS = 152 * 3, QN_CTAS_GRAD = 152 * 2;      // most CTAs: as many as are resident
+constexpr int QN_DEPTH = 5, QN_DEPTH_GRAD = 4;        // heads of a lane that are held or on their way
 
 struct NormArgs {
   uint64_t turn[128];
   float magnitude, eps;
   int rot, inter, rows, nq, nk, hd;
-  int chunks, lanes, tile;                            // chunks of a head, lanes of a head, rows of a CTA's tile
+  int chunks, lanes;                                  // chunks of a head, lanes of a head
+  int step;                                           // groups of lanes that share a row
+  unsigned by_pairs;                                  // 2^20 / pairs, rounded up
   const int32_t *positions;
   const void *qw, *kw;
   const void *q, *k, *gq, *gk;                        // inputs; gradients of the outputs (backward)
@@ -29,11 +31,27 @@ struct NormArgs {
   float *part;                                        // [CTAs][2][hd] partial sums of the weights' gradients
 };
 
-// Chunk c of a head: dims lo .. lo + V - 1 and hi .. hi + V - 1 (none where hi >= hd), turned if c is below the rotated ones.
+// Two fp32 at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n fma.rn.f32x2 x, x, y, z;\n"
+      " mov.b64 {%0, %1}, x;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Chunk c of a head: dims lo .. lo + V - 1 and hi .. hi + V - 1 (none from hd on), turned if c is below the rotated ones.
 template <int V>
 struct Chunk {
   int lo, hi;
   bool turns;
+  Chunk() = default;
   __device__ __forceinline__ Chunk(const NormArgs &a, int c) {
     const int rot_chunks = a.rot / (2 * V);
     turns = c < rot_chunks;
@@ -43,43 +61,121 @@ struct Chunk {
   }
 };
 
+// 2 V stored values of a chunk, V of each half, as V pairs: neighbours of a half (V = 1: the two).
 template <typename T, int V>
-__device__ __forceinline__ void load_dims(const T *p, int d, int hd, float *x) {
-  if (d < hd) {
-    const Vec<T, V> v = *(const Vec<T, V> *)(p + d);
-#pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = to_f(v.v[j]);
+__device__ __forceinline__ void unpack(const Vec<T, V> &lo, const Vec<T, V> &hi, float2 (&x)[V]) {
+  if constexpr (V == 1) {
+    x[0] = make_float2(to_f(lo.v[0]), to_f(hi.v[0]));
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = 0.f;
+    for (int j = 0; j < V / 2; ++j) {
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t a = ((const uint32_t *)&lo)[j], b = ((const uint32_t *)&hi)[j];
+        x[j] = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+        x[V / 2 + j] = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+      } else {
+        x[j] = make_float2(to_f(lo.v[2 * j]), to_f(lo.v[2 * j + 1]));
+        x[V / 2 + j] = make_float2(to_f(hi.v[2 * j]), to_f(hi.v[2 * j + 1]));
+      }
+    }
   }
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_dims(T *p, int d, int hd, const float *x) {
-  if (d >= hd) return;
-  Vec<T, V> v;
+__device__ __forceinline__ void pack(const float2 *x, Vec<T, V> &v) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) v.v[j] = from_f<T>(x[j]);
-  *(Vec<T, V> *)(p + d) = v;
+  for (int j = 0; j < V / 2; ++j) {
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[j].x, x[j].y);
+      ((uint32_t *)&v)[j] = *(const uint32_t *)&b;
+    } else {
+      v.v[2 * j] = from_f<T>(x[j].x);
+      v.v[2 * j + 1] = from_f<T>(x[j].y);
+    }
+  }
 }
 
-// the chunk's 2 V values turned in place by cs (its row's pairs)
-template <int V>
-__device__ __forceinline__ void turn_chunk(const NormArgs &a, const Chunk<V> &c, const float2 *cs, float *x) {
-  if (!c.turns) return;
-  if (a.inter) {
+// A lane's part of a head as stored: R chunks, zeros past the head's end. FULL: no lane has a place past it.
+template <typename T, int V, int R, bool FULL>
+struct Part {
+  typedef Vec<T, V> VT;
+  VT v[2 * R];
+  static __device__ __forceinline__ int dim(const Chunk<V> (&c)[R], int i) { return i & 1 ? c[i / 2].hi : c[i / 2].lo; }
+  __device__ __forceinline__ void zero(int i) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float2 z = turned(x[2 * j], x[2 * j + 1], cs[c.lo / 2 + j]);
-      x[2 * j] = z.x;
-      x[2 * j + 1] = z.y;
+    for (int j = 0; j < V; ++j) v[i].v[j] = from_f<T>(0.f);
+  }
+  __device__ __forceinline__ void load(const T *p, const Chunk<V> (&c)[R], int hd) {
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) {
+      if (FULL || dim(c, i) < hd) v[i] = *(const VT *)(p + dim(c, i));
+      else zero(i);
     }
+  }
+  __device__ __forceinline__ void chunk(int i, float2 (&x)[V]) const { unpack<T, V>(v[2 * i], v[2 * i + 1], x); }
+};
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void store_chunk(T *p, const Chunk<V> &c, int hd, const float2 (&x)[V]) {
+  Vec<T, V> lo, hi;
+  if constexpr (V == 1) {
+    lo.v[0] = from_f<T>(x[0].x);
+    hi.v[0] = from_f<T>(x[0].y);
+  } else {
+    pack<T, V>(x, lo);
+    pack<T, V>(x + V / 2, hi);
+  }
+  if (FULL || c.lo < hd) *(Vec<T, V> *)(p + c.lo) = lo;
+  if (FULL || c.hi < hd) *(Vec<T, V> *)(p + c.hi) = hi;
+}
+
+// Copies ahead: every thread's own ring of DEPTH parts (of OPS operands) in shared memory, which no other reads.
+template <typename T, int V, int R, int OPS, int DEPTH, bool FULL>
+struct Ring {
+  typedef Vec<T, V> VT;
+  typedef Part<T, V, R, FULL> P;
+  static constexpr size_t BYTES = sizeof(VT) * 2 * R * OPS * DEPTH * QN_THREADS;
+  VT *mine;
+  __device__ __forceinline__ Ring(void *base) : mine((VT *)base + threadIdx.x) {}
+  __device__ __forceinline__ VT *at(int slot, int op, int i) const { return mine + ((slot * OPS + op) * 2 * R + i) * QN_THREADS; }
+  __device__ __forceinline__ void fetch(int slot, int op, const T *p, const Chunk<V> (&c)[R], int hd) const {
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) {
+      const int d = P::dim(c, i);
+      if (!FULL && d >= hd) continue;
+      VT *to = at(slot, op, i);
+      if constexpr (sizeof(VT) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p + d) : "memory");
+      else if constexpr (sizeof(VT) >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p + d), "n"(sizeof(VT)) : "memory");
+      else
+        *to = *(const VT *)(p + d);
+    }
+  }
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // the oldest of DEPTH - 1 groups has arrived
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory"); }
+  __device__ __forceinline__ void take(int slot, int op, P &x, const Chunk<V> (&c)[R], int hd) const {
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) {
+      if (FULL || P::dim(c, i) < hd) x.v[i] = *at(slot, op, i);
+      else x.zero(i);
+    }
+  }
+};
+
+// the chunk's 2 V values turned in place by its pairs' cosines and sines
+template <int V>
+__device__ __forceinline__ void turn_chunk(bool inter, bool turns, const float *cos, const float *sin, float2 (&x)[V]) {
+  if (!turns) return;
+  if (inter || V == 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = turned(x[j].x, x[j].y, make_float2(cos[j], sin[j]));
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float2 z = turned(x[j], x[V + j], cs[c.lo + j]);
-      x[j] = z.x;
-      x[V + j] = z.y;
+    for (int j = 0; j < V / 2; ++j) {
+      const float2 c = make_float2(cos[2 * j], cos[2 * j + 1]), s = make_float2(sin[2 * j], sin[2 * j + 1]);
+      const float2 l = x[j], h = x[V / 2 + j], m = mul2(h, s);
+      x[j] = make_float2(fmaf(l.x, c.x, -m.x), fmaf(l.y, c.y, -m.y));
+      x[V / 2 + j] = fma2(h, c, mul2(l, s));
     }
   }
 }
@@ -88,179 +184,197 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// cos and sin of the tile's rows; sign -1: the transposed rotation
-__device__ __forceinline__ void tile_angles(const NormArgs &a, int row0, int rows, float sign, float2 *cs) {
-  const int pairs = a.rot / 2;
-  for (int i = threadIdx.x; i < rows * pairs; i += QN_THREADS) {
-    const int r = i / pairs, p = i - r * pairs;
-    float2 t = phase_cs((uint64_t)(int64_t)a.positions[row0 + r] * a.turn[p]);
-    t.x *= a.magnitude;
-    t.y *= sign * a.magnitude;
-    cs[i] = t;
-  }
+// 1 / sqrt(x): the approximation and a step of Newton's method
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
 }
 
-// R: chunks of a lane
-template <typename T, int V, int R>
-__global__ void __launch_bounds__(QN_THREADS) k_qk_norm(const __grid_constant__ NormArgs a) {
-  extern __shared__ float2 cs[];                      // [tile][pairs]
+// Forward and gradient. A CTA takes a share of the rows, a tile at a time. A group of lanes stays with a row of the tile
+// for all of its heads there (every a.step-th of q's and k's), so that sines and cosines are in registers; those of the
+// next tile are made while this one is worked on. Heads to come are copied ahead.
+template <typename T, int V, int R, bool FULL, bool GRAD>
+__global__ void __launch_bounds__(QN_THREADS, GRAD ? 2 : 3) k_qk_norm(const __grid_constant__ NormArgs a) {
+  constexpr int OPS = GRAD ? 2 : 1, DEPTH = GRAD ? QN_DEPTH_GRAD : QN_DEPTH;
+  typedef Ring<T, V, R, OPS, DEPTH, FULL> Copies;
+  extern __shared__ __align__(16) uint8_t qn_smem[];
+  __shared__ uint64_t s_turn[128];
+  const Copies ring(qn_smem);
+  float *cs = (float *)(qn_smem + Copies::BYTES);      // [2][cosines, sines][tile][pairs]
   pdl_trigger();
+  const int pairs = a.rot / 2, heads = a.nq + a.nk;
+  for (int i = threadIdx.x; i < pairs; i += QN_THREADS) s_turn[i] = a.turn[i];
+  const int first = (int)((int64_t)a.rows * blockIdx.x / gridDim.x), end = (int)((int64_t)a.rows * (blockIdx.x + 1) / gridDim.x);
+  const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
+  const int tile = QN_THREADS / a.lanes / a.step;
+  const int my_row = group / a.step, my_head = group % a.step, per_tile = (heads + a.step - 1) / a.step;
+  Chunk<V> c[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) c[i] = Chunk<V>(a, lane + i * a.lanes);
   pdl_wait();
-  const int row0 = blockIdx.x * a.tile, rows = min(a.tile, a.rows - row0), heads = a.nq + a.nk;
-  const int per = QN_THREADS / a.lanes, lane = threadIdx.x % a.lanes, total = rows * heads;
-  tile_angles(a, row0, rows, 1.f, cs);
-  __syncthreads();
-  for (int s0 = 0; s0 < total; s0 += per) {           // (all lanes of a warp stay for the sums)
-    const int s = s0 + threadIdx.x / a.lanes;
-    const bool live = s < total;
-    const int r = live ? s / heads : 0;
-    int h = live ? s - r * heads : 0;
-    const bool isk = h >= a.nq;
-    if (isk) h -= a.nq;
-    const size_t row = row0 + r;
-    const T *src = (isk ? (const T *)a.k + row * a.ks : (const T *)a.q + row * a.qs) + (size_t)h * a.hd;
-    T *dst = (isk ? (T *)a.ko + row * a.kos : (T *)a.qo + row * a.qos) + (size_t)h * a.hd;
-    const T *w = (const T *)(isk ? a.kw : a.qw);
-    float x[R][2 * V];
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const Chunk<V> c(a, lane + i * a.lanes);
-      load_dims<T, V>(src, live ? c.lo : a.hd, a.hd, x[i]);
-      load_dims<T, V>(src, live ? c.hi : a.hd, a.hd, x[i] + V);
-#pragma unroll
-      for (int j = 0; j < 2 * V; ++j) ss = fmaf(x[i][j], x[i][j], ss);
+  // the copies: DEPTH - 1 steps ahead
+  int f_row = first + my_row, f_head = my_head, f_slot = 0;
+  auto fetch = [&]() {
+    if (f_row < end && f_head < heads) {
+      const bool isk = f_head >= a.nq;
+      const int64_t from = (int64_t)(isk ? f_head - a.nq : f_head) * a.hd;
+      ring.fetch(f_slot, 0, (const T *)(isk ? a.k : a.q) + f_row * (isk ? a.ks : a.qs) + from, c, a.hd);
+      if constexpr (GRAD) ring.fetch(f_slot, 1, (const T *)(isk ? a.gk : a.gq) + f_row * (isk ? a.gks : a.gqs) + from, c, a.hd);
     }
-    const float inv = __frsqrt_rn(head_sum(ss, a.lanes) / (float)a.hd + a.eps);
-    if (!live) continue;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const Chunk<V> c(a, lane + i * a.lanes);
-      float y[2 * V];
-      load_dims<T, V>(w, c.lo, a.hd, y);
-      load_dims<T, V>(w, c.hi, a.hd, y + V);
-#pragma unroll
-      for (int j = 0; j < 2 * V; ++j) y[j] *= x[i][j] * inv;
-      turn_chunk<V>(a, c, cs + r * (a.rot / 2), y);
-      store_dims<T, V>(dst, c.lo, a.hd, y);
-      store_dims<T, V>(dst, c.hi, a.hd, y + V);
+    ring.commit();
+    f_slot = f_slot + 1 == DEPTH ? 0 : f_slot + 1;
+    f_head += a.step;
+    if (f_head >= per_tile * a.step) {
+      f_head = my_head;
+      f_row += tile;
     }
+  };
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) fetch();
+  __syncthreads();                                    // s_turn is there
+  auto angles = [&](int row0, float *to) {
+    const int n = min(tile, end - row0) * pairs;
+    for (int i = threadIdx.x; i < n; i += QN_THREADS) {
+      const int r = (int)(i * a.by_pairs >> 20);       // i / pairs: i is below 2048 where pairs is above 1
+      const float2 t = phase_cs((uint64_t)(int64_t)a.positions[row0 + r] * s_turn[i - r * pairs]);
+      to[i] = t.x * a.magnitude;
+      to[tile * pairs + i] = t.y * (GRAD ? -a.magnitude : a.magnitude);        // (the gradient turns back)
+    }
+  };
+  Part<T, V, R, FULL> qw, kw;
+  qw.load((const T *)a.qw, c, a.hd);
+  if (a.nk) kw.load((const T *)a.kw, c, a.hd);
+  else kw = qw;
+  const float inv_hd = 1.f / (float)a.hd;
+  float2 wsum[2][GRAD ? R : 1][V];
+  if constexpr (GRAD) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) wsum[k][i][j] = make_float2(0.f, 0.f);
   }
-}
-
-// The gradient: CTAs walk the tiles, q's heads and then k's, each lane with the same chunks of every head, whose sums
-// of n' x r it keeps; they are added up over the CTA at the end, in a fixed order.
-template <typename T, int V, int R>
-__global__ void __launch_bounds__(QN_THREADS) k_qk_norm_grad(const __grid_constant__ NormArgs a) {
-  extern __shared__ float2 cs[];                      // [tile][pairs], then [warps][hd] sums
-  pdl_trigger();
-  pdl_wait();
-  const int per = QN_THREADS / a.lanes, lane = threadIdx.x % a.lanes;
-  float wsum[2][R][2 * V];
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
+  if (first < end) angles(first, cs);
+  int slot = 0;
+  for (int row0 = first, buf = 0; row0 < end; row0 += tile, buf ^= 1) {
+    __syncthreads();                                  // this tile's angles are there, the last one's are done with
+    if (row0 + tile < end) angles(row0 + tile, cs + 2 * (buf ^ 1) * tile * pairs);
+    const int row = row0 + my_row;
+    float cosine[R][V], sine[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i)
+      if (c[i].turns) {
+        const float *from = cs + (2 * buf * tile + my_row) * pairs + (a.inter ? c[i].lo / 2 : c[i].lo);
 #pragma unroll
-      for (int j = 0; j < 2 * V; ++j) wsum[k][i][j] = 0.f;
-  const int tiles = (a.rows + a.tile - 1) / a.tile;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int row0 = t * a.tile, rows = min(a.tile, a.rows - row0);
-    tile_angles(a, row0, rows, -1.f, cs);
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int heads = k ? a.nk : a.nq, total = rows * heads;
-      const T *w = (const T *)(k ? a.kw : a.qw);
-      const int64_t xs = k ? a.ks : a.qs, gs = k ? a.gks : a.gqs, os = k ? a.kos : a.qos;
-      for (int s0 = 0; s0 < total; s0 += per) {
-        const int s = s0 + threadIdx.x / a.lanes;
-        const bool live = s < total;
-        const int r = live ? s / heads : 0, h = live ? s - r * heads : 0;
-        const size_t row = row0 + r;
-        const T *src = (const T *)(k ? a.k : a.q) + row * xs + (size_t)h * a.hd;
-        const T *up = (const T *)(k ? a.gk : a.gq) + row * gs + (size_t)h * a.hd;
-        T *dst = (T *)(k ? a.ko : a.qo) + row * os + (size_t)h * a.hd;
-        float x[R][2 * V], g[R][2 * V];
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const Chunk<V> c(a, lane + i * a.lanes);
-          load_dims<T, V>(src, live ? c.lo : a.hd, a.hd, x[i]);
-          load_dims<T, V>(src, live ? c.hi : a.hd, a.hd, x[i] + V);
-          load_dims<T, V>(up, live ? c.lo : a.hd, a.hd, g[i]);
-          load_dims<T, V>(up, live ? c.hi : a.hd, a.hd, g[i] + V);
+        for (int j = 0; j < V; ++j) {
+          cosine[i][j] = from[j];
+          sine[i][j] = from[tile * pairs + j];
         }
+      }
+    for (int h = my_head, n = 0; n < per_tile; ++n, h += a.step) {     // (all lanes of a warp stay for the sums)
+      ring.wait();
+      Part<T, V, R, FULL> x, g;
+      ring.take(slot, 0, x, c, a.hd);
+      if constexpr (GRAD) ring.take(slot, 1, g, c, a.hd);
+      fetch();
+      slot = slot + 1 == DEPTH ? 0 : slot + 1;
+      const bool isk = h >= a.nq;
+      float2 u[R][V], z[R][V], w[R][V];
+      float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const Chunk<V> c(a, lane + i * a.lanes);
-          turn_chunk<V>(a, c, cs + r * (a.rot / 2), g[i]);
-          float y[2 * V];
-          load_dims<T, V>(w, c.lo, a.hd, y);
-          load_dims<T, V>(w, c.hi, a.hd, y + V);
+      for (int i = 0; i < R; ++i) {
+        x.chunk(i, u[i]);
 #pragma unroll
-          for (int j = 0; j < 2 * V; ++j) {
-            ss = fmaf(x[i][j], x[i][j], ss);
-            dot = fmaf(g[i][j] * y[j], x[i][j], dot);
+        for (int j = 0; j < V; ++j) ss = fma2(u[i][j], u[i][j], ss);
+        Part<T, V, 1, FULL> both_w;
+        both_w.v[0] = isk ? kw.v[2 * i] : qw.v[2 * i];
+        both_w.v[1] = isk ? kw.v[2 * i + 1] : qw.v[2 * i + 1];
+        both_w.chunk(0, w[i]);
+        if constexpr (GRAD) {
+          g.chunk(i, z[i]);
+          turn_chunk<V>(a.inter, c[i].turns, cosine[i], sine[i], z[i]);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            w[i][j] = mul2(z[i][j], w[i][j]);
+            dot = fma2(w[i][j], u[i][j], dot);
           }
         }
-        ss = head_sum(ss, a.lanes);
-        dot = head_sum(dot, a.lanes);
-        const float inv = __frsqrt_rn(ss / (float)a.hd + a.eps), m = dot * inv / (float)a.hd;   // r mean(g x)
-        if (!live) continue;
+      }
+      const float inv = inv_sqrt(fmaf(head_sum(ss.x + ss.y, a.lanes), inv_hd, a.eps));
+      float m = 0.f;
+      if constexpr (GRAD) m = head_sum(dot.x + dot.y, a.lanes) * inv * inv_hd;       // r mean(g x)
+      if (row >= end || h >= heads) continue;
+      const int64_t to = (int64_t)(isk ? h - a.nq : h) * a.hd;
+      T *dst = (T *)(isk ? a.ko : a.qo) + row * (isk ? a.kos : a.qos) + to;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const Chunk<V> c(a, lane + i * a.lanes);
-          float y[2 * V];
-          load_dims<T, V>(w, c.lo, a.hd, y);
-          load_dims<T, V>(w, c.hi, a.hd, y + V);
+      for (int i = 0; i < R; ++i) {
+        float2 y[V];
 #pragma unroll
-          for (int j = 0; j < 2 * V; ++j) {
-            const float u = x[i][j] * inv;
-            wsum[k][i][j] = fmaf(g[i][j], u, wsum[k][i][j]);
-            y[j] = inv * fmaf(g[i][j], y[j], -u * m);
-          }
-          store_dims<T, V>(dst, c.lo, a.hd, y);
-          store_dims<T, V>(dst, c.hi, a.hd, y + V);
+        for (int j = 0; j < V; ++j) {
+          u[i][j] = mul2(u[i][j], both(inv));
+          if constexpr (GRAD) y[j] = mul2(fma2(u[i][j], both(-m), w[i][j]), both(inv));
+          else y[j] = mul2(u[i][j], w[i][j]);
+        }
+        if constexpr (!GRAD) turn_chunk<V>(a.inter, c[i].turns, cosine[i], sine[i], y);
+        store_chunk<T, V, FULL>(dst, c[i], a.hd, y);
+      }
+      if constexpr (GRAD) {
+        if (isk) {
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) wsum[1][i][j] = fma2(z[i][j], u[i][j], wsum[1][i][j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) wsum[0][i][j] = fma2(z[i][j], u[i][j], wsum[0][i][j]);
         }
       }
     }
-    __syncthreads();                                  // the angles are done with
   }
-  float *sums = (float *)cs;
-  const int warp = threadIdx.x >> 5;
-  for (int k = 0; k < 2; ++k) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const Chunk<V> c(a, lane + i * a.lanes);
-#pragma unroll
-      for (int j = 0; j < 2 * V; ++j) {
-        float v = k ? wsum[1][i][j] : wsum[0][i][j];
-        for (int o = a.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int first = j < V ? c.lo : c.hi, d = first + j % V;
-        if ((threadIdx.x & 31) < a.lanes && first < a.hd) sums[warp * a.hd + d] = v;
-      }
-    }
+  if constexpr (GRAD) {
+    // the weights' gradients over the CTA, in a fixed order
     __syncthreads();
-    for (int d = threadIdx.x; d < a.hd; d += QN_THREADS) {
+    float *sums = (float *)qn_smem;                   // [warps][2][hd]
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          float2 v = wsum[k][i][j];
+          for (int o = a.lanes; o < 32; o <<= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+          }
+          // (V = 1: the two halves; else neighbours, the first half's and then the other's)
+          const int d0 = V == 1 ? c[i].lo : j < V / 2 ? c[i].lo + 2 * j : c[i].hi + 2 * j - V, d1 = V == 1 ? c[i].hi : d0 + 1;
+          if ((threadIdx.x & 31) < a.lanes) {
+            if (d0 < a.hd) sums[(2 * warp + k) * a.hd + d0] = v.x;
+            if (d1 < a.hd) sums[(2 * warp + k) * a.hd + d1] = v.y;
+          }
+        }
+    __syncthreads();
+    for (int d = threadIdx.x; d < 2 * a.hd; d += QN_THREADS) {
       float v = 0.f;
-      for (int x = 0; x < QN_THREADS / 32; ++x) v += sums[x * a.hd + d];
-      a.part[((size_t)blockIdx.x * 2 + k) * a.hd + d] = v;
+      for (int x = 0; x < QN_THREADS / 32; ++x) v += sums[2 * x * a.hd + d];
+      a.part[(size_t)blockIdx.x * 2 * a.hd + d] = v;
     }
-    __syncthreads();
   }
 }
 
-// dweight[d] = sum of n partial sums: 32 dims of a CTA, 32 threads each
-__global__ void __launch_bounds__(1024) k_qk_norm_weights(int n, int hd, const float *part, float *dqw, float *dkw) {
+// dweight[d] = the sum of the CTAs' partial sums: 32 dims of a CTA, 32 threads each
+__global__ void __launch_bounds__(1024) k_qk_norm_weights(int ctas, int hd, const float *part, float *dqw, float *dkw) {
   __shared__ float s[32][33];
   pdl_trigger();
   pdl_wait();
   const int k = blockIdx.y, d = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
   float v = 0.f;
   if (d < hd)
-    for (int i = y; i < n; i += 32) v += part[((size_t)i * 2 + k) * hd + d];
+    for (int i = y; i < ctas; i += 32) v += part[((size_t)i * 2 + k) * hd + d];
   s[y][threadIdx.x] = v;
   __syncthreads();
   v = warp_sum(s[threadIdx.x][y]);
@@ -268,29 +382,35 @@ __global__ void __launch_bounds__(1024) k_qk_norm_weights(int n, int hd, const f
   if (threadIdx.x == 0 && dim < hd) (k ? dkw : dqw)[dim] = v;
 }
 
-template <typename T, int V, int R>
-cudaError_t launch_norm(const NormArgs &a, int *parts, cudaStream_t s) {
-  const size_t angles = (size_t)a.tile * (a.rot / 2) * sizeof(float2);
-  const int tiles = (a.rows + a.tile - 1) / a.tile;
-  if (!parts) return launch_pdl(k_qk_norm<T, V, R>, dim3(tiles), dim3(QN_THREADS), angles, s, a);
-  const size_t sums = (size_t)QN_THREADS / 32 * a.hd * sizeof(float);
-  *parts = tiles < QN_CTAS ? tiles : QN_CTAS;
-  return launch_pdl(k_qk_norm_grad<T, V, R>, dim3(*parts), dim3(QN_THREADS), angles > sums ? angles : sums, s, a);
+template <typename T, int V, int R, bool FULL, bool GRAD>
+cudaError_t launch_norm(const NormArgs &a, int ctas, cudaStream_t s) {
+  const int tile = QN_THREADS / a.lanes / a.step;
+  size_t sm = Ring<T, V, R, GRAD ? 2 : 1, GRAD ? QN_DEPTH_GRAD : QN_DEPTH, FULL>::BYTES + 4ull * tile * (a.rot / 2) * sizeof(float);
+  const size_t sums = (size_t)QN_THREADS / 32 * 2 * a.hd * sizeof(float);
+  sm = GRAD && sm < sums ? sums : sm;
+  const cudaError_t e = cudaFuncSetAttribute(k_qk_norm<T, V, R, FULL, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 << 10);
+  return e != cudaSuccess ? e : launch_pdl(k_qk_norm<T, V, R, FULL, GRAD>, dim3(ctas), dim3(QN_THREADS), sm, s, a);
 }
 
-// width: elements of an access; parts: gets the number of partial sums of the gradient (null: forward)
-template <typename T>
-cudaError_t launch_norm(NormArgs a, int width, int *parts, cudaStream_t s) {
+// width: elements of an access. Returns the CTAs in *ctas.
+template <typename T, bool GRAD>
+cudaError_t launch_norm(NormArgs &a, int width, int *ctas, cudaStream_t s) {
   constexpr int W = 16 / sizeof(T);
   a.chunks = (a.hd + 2 * width - 1) / (2 * width);
   a.lanes = 1;
   while (a.lanes < a.chunks && a.lanes < 32) a.lanes *= 2;
-  // a tile of rows has as many heads as the CTA takes at once, but no more than 8 rows
-  const int per = QN_THREADS / a.lanes, heads = parts ? (a.nk ? a.nk : a.nq) : a.nq + a.nk;
-  a.tile = (per + heads - 1) / heads;
-  a.tile = a.tile > 8 ? 8 : a.tile;
-  if (width == W) return launch_norm<T, W, 1>(a, parts, s);
-  return width == 2 ? launch_norm<T, 2, 2>(a, parts, s) : launch_norm<T, 1, 4>(a, parts, s);
+  const int per = QN_THREADS / a.lanes, heads = a.nq + a.nk;
+  a.by_pairs = ((1u << 20) + a.rot / 2 - 1) / (a.rot / 2);
+  constexpr int most = GRAD ? QN_CTAS_GRAD : QN_CTAS;
+  // Groups of lanes that share a row: 8, for more than one row's angles at a time; all of them where that
+  // leaves too few CTAs, and no more than there are heads.
+  a.step = 1;
+  while (a.step < per && a.step < heads && (a.step < 8 || (int64_t)a.rows * a.step < (int64_t)most * per)) a.step *= 2;
+  const int tile = per / a.step, tiles = (a.rows + tile - 1) / tile;
+  *ctas = tiles < most ? tiles : most;
+  if (width == W && a.lanes == a.chunks && a.hd % (2 * W) == 0) return launch_norm<T, W, 1, true, GRAD>(a, *ctas, s);
+  if (width == W) return launch_norm<T, W, 1, false, GRAD>(a, *ctas, s);
+  return width == 2 ? launch_norm<T, 2, 2, false, GRAD>(a, *ctas, s) : launch_norm<T, 1, 4, false, GRAD>(a, *ctas, s);
 }
 
 }  // namespace dflash
@@ -357,11 +477,12 @@ extern "C" dflash_status dflash_qk_norm_rope(void *stream, const dflash_rope *ro
   a.qs = q_stride, a.ks = k_stride, a.qos = q_out_stride, a.kos = k_out_stride;
   const int w = access_width(a, es, f, n);
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = dtype == DFLASH_BF16 ? launch_norm<bf16>(a, w, nullptr, s) : launch_norm<float>(a, w, nullptr, s);
+  int ctas;
+  const cudaError_t e = dtype == DFLASH_BF16 ? launch_norm<bf16, false>(a, w, &ctas, s) : launch_norm<float, false>(a, w, &ctas, s);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
-extern "C" int64_t dflash_qk_norm_rope_workspace(void) { return (int64_t)QN_CTAS * 2 * 256 * sizeof(float); }
+extern "C" int64_t dflash_qk_norm_rope_workspace(void) { return (int64_t)QN_CTAS_GRAD * 2 * 256 * sizeof(float); }
 
 extern "C" dflash_status dflash_qk_norm_rope_backward(void *stream, const dflash_rope *rope,
                                                       const dflash_qk_norm_rope_grad *x) {
@@ -395,13 +516,13 @@ extern "C" dflash_status dflash_qk_norm_rope_backward(void *stream, const dflash
   a.part = (float *)x->workspace;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  int parts = 0;
+  int ctas = 0;
   if (x->rows) {
     const int w = access_width(a, es, f, n);
-    e = x->dtype == DFLASH_BF16 ? launch_norm<bf16>(a, w, &parts, s) : launch_norm<float>(a, w, &parts, s);
+    e = x->dtype == DFLASH_BF16 ? launch_norm<bf16, true>(a, w, &ctas, s) : launch_norm<float, true>(a, w, &ctas, s);
   }
   if (e == cudaSuccess)
-    e = launch_pdl(k_qk_norm_weights, dim3((hd + 31) / 32, nk ? 2 : 1), dim3(32, 32), 0, s, parts, hd,
+    e = launch_pdl(k_qk_norm_weights, dim3((hd + 31) / 32, nk ? 2 : 1), dim3(32, 32), 0, s, ctas, hd,
                    (const float *)a.part, x->dq_weight, x->dk_weight);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
