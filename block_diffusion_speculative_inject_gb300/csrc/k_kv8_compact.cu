@@ -9,7 +9,7 @@
 
 namespace dflash {
 
-constexpr int KP_THREADS = 256;
+constexpr int KP_THREADS = 128;
 constexpr int KP_LAYERS = 128;
 
 struct CompactArgs {
@@ -42,13 +42,13 @@ __global__ void __launch_bounds__(KP_THREADS) k_kv8_compact(const __grid_constan
   const int32_t *table = a.table + (size_t)b * a.width;
   for (long long blk = base / KV_PAGE; blk * KV_PAGE < end; ++blk) {
     const int page = table[blk];
+    const long long to = blk * KV_PAGE + tid;
+    const int k = tid < KV_PAGE && to >= base && to < end ? a.keep[(size_t)b * a.max_keep + (to - base)] : -1;
     if (page < 0 || page >= a.n_pages) continue;       // (the same for the CTA)
     if (tid < KV_PAGE) {
-      const long long to = blk * KV_PAGE + tid;
       int slot = -1;
       float sc = 0.f;
-      if (to >= base && to < end) {
-        const int k = a.keep[(size_t)b * a.max_keep + (to - base)];
+      {
         const long long src = base + k;
         if (k >= 0 && src < cap) {
           const int sp = table[src / KV_PAGE];
@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(KP_THREADS) k_kv8_compact(const __grid_constan
     }
     __syncthreads();
     const uint64_t owned = (uint64_t)s_owned[1] << 32 | s_owned[0];
+    const int o0 = owned ? __ffsll((long long)owned) - 1 : 0, last = owned ? 63 - __clzll(owned) : -1;
+    const int w0 = o0 / 4, words = last < 0 ? 0 : last / 4 - w0 + 1;   // of V's places
     // the rows' bytes, and the largest value among them (NaN and what passes fp32 left out)
     float big = 0.f;
     auto largest = [&](uint32_t m, float sc) {
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(KP_THREADS) k_kv8_compact(const __grid_constan
       for (int j = 0; j < 4; ++j) largest(w >> 8 * j & 0x7f, sc);
     };
     if (!isv) {
-      for (int i = tid; i < KV_PAGE * HD / 16; i += KP_THREADS) {
+      for (int i = o0 * (HD / 16) + tid; i < (last + 1) * (HD / 16); i += KP_THREADS) {
         const int o = i / (HD / 16), c = i % (HD / 16);
         if (!(owned >> o & 1)) continue;
         const uint4 w = *(const uint4 *)(pages + kv8_block(from[o] / KV_PAGE, h, a.nkv, HD) + (from[o] % KV_PAGE) * HD + 16 * c);
@@ -84,15 +86,15 @@ __global__ void __launch_bounds__(KP_THREADS) k_kv8_compact(const __grid_constan
         take(w.x, from_scale[o]), take(w.y, from_scale[o]), take(w.z, from_scale[o]), take(w.w, from_scale[o]);
       }
     } else {
-      for (int i = tid; i < HD * (KV_PAGE / 4); i += KP_THREADS) {
-        const int d = i / (KV_PAGE / 4), o = i % (KV_PAGE / 4) * 4;
+      for (int x = tid; x < HD * words; x += KP_THREADS) {
+        const int d = x / words, i = d * (KV_PAGE / 4) + w0 + x - d * words, o = i % (KV_PAGE / 4) * 4;
         uint32_t w = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (owned >> (o + j) & 1) {
-            const uint32_t x = pages[kv8_block(from[o + j] / KV_PAGE, h, a.nkv, HD) + d * KV_PAGE + from[o + j] % KV_PAGE];
-            w |= x << 8 * j;
-            largest(x & 0x7f, from_scale[o + j]);
+            const uint32_t y = pages[kv8_block(from[o + j] / KV_PAGE, h, a.nkv, HD) + d * KV_PAGE + from[o + j] % KV_PAGE];
+            w |= y << 8 * j;
+            largest(y & 0x7f, from_scale[o + j]);
           }
         *(uint32_t *)(tile + 4 * i) = w;
       }
@@ -109,7 +111,6 @@ __global__ void __launch_bounds__(KP_THREADS) k_kv8_compact(const __grid_constan
       float scale = pow2f(scale_exp(big)), again = 1.f;
       if (old >= scale) scale = old;
       else if (!fresh) again = old / scale;
-      const int last = 63 - __clzll(owned);
       const uint64_t kept = fresh || again == 1.f ? 0 : (last == 63 ? ~0ull : (2ull << last) - 1) & ~owned;
       const float inv = 1.f / scale;
       if (tid == 0) *sp = scale;
@@ -118,16 +119,18 @@ __global__ void __launch_bounds__(KP_THREADS) k_kv8_compact(const __grid_constan
         const float2 x = e4m3x2_to_f32(w), y = e4m3x2_to_f32(w >> 16);
         return f32_to_e4m3x2(x.x * sc * inv, x.y * sc * inv) | f32_to_e4m3x2(y.x * sc * inv, y.y * sc * inv) << 16;
       };
+      const int from0 = kept ? 0 : o0;                 // the first place that is written
       if (!isv) {
-        for (int i = tid; i < KV_PAGE * HD / 4; i += KP_THREADS) {
+        for (int i = from0 * (HD / 4) + tid; i < (last + 1) * (HD / 4); i += KP_THREADS) {
           const int o = i / (HD / 4);
           uint32_t *dst = (uint32_t *)(blkp + 4 * i);
           if (owned >> o & 1) *dst = moved(*(const uint32_t *)(tile + 4 * i), from_scale[o]);
           else if (kept >> o & 1) *dst = rescale4(*dst, again);
         }
       } else {
-        for (int i = tid; i < HD * (KV_PAGE / 4); i += KP_THREADS) {
-          const int o = i % (KV_PAGE / 4) * 4;
+        const int f0 = from0 / 4, n = last / 4 - f0 + 1;
+        for (int z = tid; z < HD * n; z += KP_THREADS) {
+          const int d = z / n, i = d * (KV_PAGE / 4) + f0 + z - d * n, o = i % (KV_PAGE / 4) * 4;
           const uint32_t mo = (uint32_t)(owned >> o) & 15, mk = (uint32_t)(kept >> o) & 15;
           if (!(mo | mk)) continue;
           uint32_t *dst = (uint32_t *)(blkp + 4 * i);

@@ -79,21 +79,28 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
       least[j] = as_half2(0x7c007c00u);
       most[j] = as_half2(0xfc00fc00u);
     }
-#pragma unroll 8
-    for (int r = 0; r < KV_PAGE; r += RPI) {
-      if (r + lane / LPR >= rows) continue;
-      const uint4 w = *(const uint4 *)(src + r * HD);
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+    for (int r0 = lane / LPR; r0 < rows; r0 += 8 * RPI) {
+      uint4 w[8];                                      // (rows past the end: NaN, which the smaller and the larger both leave out)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t p0, p1;
-        e4m3x4_to_f16(v[j], p0, p1);
-        least[2 * j] = __hmin2(least[2 * j], as_half2(p0));
-        most[2 * j] = __hmax2(most[2 * j], as_half2(p0));
-        least[2 * j + 1] = __hmin2(least[2 * j + 1], as_half2(p1));
-        most[2 * j + 1] = __hmax2(most[2 * j + 1], as_half2(p1));
+      for (int i = 0; i < 8; ++i)
+        w[i] = r0 + i * RPI < rows ? *(const uint4 *)(src + (size_t)(r0 - lane / LPR + i * RPI) * HD)
+                                   : make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p0, p1;
+          e4m3x4_to_f16(v[j], p0, p1);
+          least[2 * j] = __hmin2(least[2 * j], as_half2(p0));
+          most[2 * j] = __hmax2(most[2 * j], as_half2(p0));
+          least[2 * j + 1] = __hmin2(least[2 * j + 1], as_half2(p1));
+          most[2 * j + 1] = __hmax2(most[2 * j + 1], as_half2(p1));
+        }
       }
     }
+    __syncwarp();
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
@@ -122,8 +129,9 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
 // 2^17 and the sums of a row at most 2^24, so every partial sum is a whole number that fp32 (and an accumulator that
 // truncates) holds. Contraction indices are permuted as in the attention for few rows: a lane's 16 bytes are the dims of
 // four steps.
-constexpr int KS_THREADS = 128;
-constexpr int KS_ROWS = 128;                          // rows of q staged at once
+constexpr int KS_THREADS = 256;
+constexpr int KS_TILE = KS_THREADS / 2;               // blocks of a CTA at once: 16 of a warp
+constexpr int KS_ROWS = 80;                           // rows of q staged at once: 40 KB
 
 struct SelectArgs {
   Kv8AttnArgs a;
@@ -145,10 +153,26 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &
   hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
 }
 
+template <typename T>
+struct Vec4;
+template <>
+struct Vec4<bf16> {
+  uint2 w;
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+  }
+};
+template <>
+struct Vec4<float> {
+  float4 w;
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w; }
+};
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(KS_THREADS) k_kv8_scores(const SelectArgs x) {
+__global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x) {
   constexpr int KS = HD / 16, C = HD / 64;
-  __shared__ uint2 qf[KS_ROWS / 8][KS][32];            // fragments of q
+  __shared__ uint4 qf[KS_ROWS / 8][KS][32];            // fragments of q+ and of q-
   __shared__ float unit[KS_ROWS];                      // 0: a row that has no say
   const Kv8AttnArgs &a = x.a;
   pdl_trigger();
@@ -156,30 +180,29 @@ __global__ void __launch_bounds__(KS_THREADS) k_kv8_scores(const SelectArgs x) {
   const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Kv8Req r = kv8_req(a, b);
   const int blocks = (r.len + KV_PAGE - 1) / KV_PAGE, group = a.nq / a.nkv;
-  if (r.n == 0 || blocks <= x.n_select || blockIdx.x * 64 >= blocks) return;
+  if (r.n == 0 || blocks <= x.n_select || blockIdx.x * KS_TILE >= blocks) return;
   const long long rows = (long long)r.n * group;
   float *score = x.score + ((size_t)b * a.nkv + h) * a.width;
   for (long long r0 = 0; r0 < rows; r0 += KS_ROWS) {
     // q in whole numbers: HD / 4 lanes a row, four dims each
-    constexpr int LPR = HD / 4;
+    constexpr int LPR = HD / 4, N = KS_ROWS * LPR / KS_THREADS;
     const int here = (int)min((long long)KS_ROWS, rows - r0), tiles = (here + 7) / 8;
+    const int i0 = threadIdx.x / LPR, l = threadIdx.x % LPR;
+    typedef Vec4<T> Q4;
+    Q4 in[N];                                         // all loads first
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = i0 + n * (KS_THREADS / LPR);
+      const long long row = r0 + i;
+      in[n] = i < here ? *(const Q4 *)((const T *)a.q + (r.row0 + row / group) * a.q_stride + (int64_t)(h * group + row % group) * HD + 4 * l)
+                       : Q4{};
+    }
     __syncthreads();
-    for (int i0 = 0; i0 < tiles * 8; i0 += KS_THREADS / LPR) {
-      const int i = i0 + threadIdx.x / LPR, l = threadIdx.x % LPR;
-      const bool live = i < here;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (live) {
-        const long long row = r0 + i;
-        const T *src = (const T *)a.q + (r.row0 + row / group) * a.q_stride + (int64_t)(h * group + row % group) * HD + 4 * l;
-        if constexpr (sizeof(T) == 2) {
-          const uint2 w = *(const uint2 *)src;
-          v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
-          v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
-          const float4 w = *(const float4 *)src;
-          v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-        }
-      }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = i0 + n * (KS_THREADS / LPR);
+      float v[4];
+      in[n].get(v);
       uint32_t top = 0;                               // bits of the largest magnitude: NaN and infinity are the largest
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
@@ -189,20 +212,20 @@ __global__ void __launch_bounds__(KS_THREADS) k_kv8_scores(const SelectArgs x) {
       // top = m 2^k, m in [1/2, 1): unit 2^(k - 10)
       const int k = max((int)(top >> 23) - 126, -100);
       const float up = __uint_as_float((uint32_t)(137 - k) << 23);
-      uint32_t w[2];
+      uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const __half2 y = __floats2half2_rn(fin ? rintf(v[2 * j] * up) : 0.f, fin ? rintf(v[2 * j + 1] * up) : 0.f);
-        w[j] = *(const uint32_t *)&y;
+        const __half2 p = __hmax2(y, as_half2(0)), m = __hmin2(y, as_half2(0));
+        w[j] = *(const uint32_t *)&p;
+        w[2 + j] = *(const uint32_t *)&m;
       }
       // dims 4 l .. + 3 are word l & 3 of lane l / 4 & 3's 16 bytes in chunk l / 16
-      if (i < tiles * 8) {
-        qf[i / 8][l / 16 * 4 + (l & 3)][(i & 7) * 4 + (l >> 2 & 3)] = make_uint2(w[0], w[1]);
-        if (l == 0) unit[i] = live && fin ? __uint_as_float((uint32_t)(117 + k) << 23) : 0.f;
-      }
+      qf[i / 8][l / 16 * 4 + (l & 3)][(i & 7) * 4 + (l >> 2 & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
+      if (l == 0) unit[i] = i < here && fin ? __uint_as_float((uint32_t)(117 + k) << 23) : 0.f;
     }
     __syncthreads();
-    for (int p0 = blockIdx.x * 64 + warp * 16; p0 < blocks; p0 += gridDim.x * 64) {
+    for (int p0 = blockIdx.x * KS_TILE + warp * 16; p0 < blocks; p0 += gridDim.x * KS_TILE) {
       int page[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -231,12 +254,9 @@ __global__ void __launch_bounds__(KS_THREADS) k_kv8_scores(const SelectArgs x) {
         float up[4] = {0.f, 0.f, 0.f, 0.f}, dn[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const uint2 q = qf[n][k][lane];
-          const __half2 zero = as_half2(0);
-          const __half2 p0h = __hmax2(as_half2(q.x), zero), p1h = __hmax2(as_half2(q.y), zero);
-          const __half2 n0h = __hmin2(as_half2(q.x), zero), n1h = __hmin2(as_half2(q.y), zero);
-          mma_16816(up, hi[k], *(const uint32_t *)&p0h, *(const uint32_t *)&p1h);
-          mma_16816(dn, lo[k], *(const uint32_t *)&n0h, *(const uint32_t *)&n1h);
+          const uint4 q = qf[n][k][lane];
+          mma_16816(up, hi[k], q.x, q.y);
+          mma_16816(dn, lo[k], q.z, q.w);
         }
         const float u0 = unit[8 * n + 2 * t], u1 = unit[8 * n + 2 * t + 1];
 #pragma unroll
@@ -263,10 +283,12 @@ __global__ void __launch_bounds__(KS_THREADS) k_kv8_scores(const SelectArgs x) {
 // A CTA per (request, kv head). Keys rank as the scores do (fixed blocks above all); four passes over the keys' bytes,
 // each a histogram of the keys that agree with the threshold so far, find the last key that is taken and how many of
 // those equal to it; the chosen ones are then written in order.
-constexpr int KC_THREADS = 256;
+constexpr int KC_THREADS = 512;
+constexpr int KC_HELD = 4096;                         // keys that are kept in shared memory
 
 __global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
-  __shared__ int hist[256], warp_tot[KC_THREADS / 32 + 1];
+  __shared__ int hist[256], warp_tot[KC_THREADS / 32];
+  __shared__ uint32_t held[KC_HELD];
   __shared__ int s_bin, s_left;
   const Kv8AttnArgs &a = x.a;
   pdl_trigger();
@@ -282,11 +304,15 @@ __global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
   const float *score = x.score + ((size_t)b * a.nkv + h) * a.width;
   // floor((len - n) / 64) - last; the rows may be more than the context
   const int d = r.len - r.n, own = (d >= 0 ? d / KV_PAGE : -((-d + KV_PAGE - 1) / KV_PAGE)) - x.last;
-  auto key = [&](int j) {
+  auto key_of = [&](int j) {
     if (j < x.first || j >= own) return 0xffffffffu;
     const uint32_t u = __float_as_uint(score[j] + 0.f);                 // (-0 as 0)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
   };
+  const bool fits = blocks <= KC_HELD;
+  if (fits)
+    for (int j = tid; j < blocks; j += KC_THREADS) held[j] = key_of(j);        // (read by the thread that wrote it)
+  auto key = [&](int j) { return fits ? held[j] : key_of(j); };
   uint32_t prefix = 0;
   int left = x.n_select;                               // of the keys that begin with prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
@@ -384,9 +410,9 @@ bool choice_ok(const dflash_kv8_cache *c, const dflash_kv8_choice *x) {
 }
 template <typename T>
 cudaError_t launch_select(const SelectArgs &x, int hd, cudaStream_t s) {
-  // CTAs of a (request, kv head), which take 64 blocks at a time in turn
-  const long items = (long)x.a.n_req * x.a.nkv, want = (152 * 4 + items - 1) / items;
-  const long most = ((long)x.a.width + 63) / 64;
+  // CTAs of a (request, kv head), which take KS_TILE blocks at a time in turn: as many as are resident
+  const long items = (long)x.a.n_req * x.a.nkv, want = items < 304 ? 304 / items : 1;
+  const long most = ((long)x.a.width + KS_TILE - 1) / KS_TILE;
   const dim3 g((unsigned)(want < most ? want : most), x.a.nkv, x.a.n_req), t(KS_THREADS);
   cudaError_t e = cudaSuccess;
   if (x.a.width > x.n_select)
