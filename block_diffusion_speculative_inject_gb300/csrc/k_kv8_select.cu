@@ -8,7 +8,7 @@ namespace dflash {
 // A warp per (page, kv head): lanes read 16 bytes of a row each, several rows at a time, and keep the least and the
 // largest of their 16 dims as f16 pairs (exact). Bound by the read of the pages.
 constexpr int KB_THREADS = 256;
-constexpr int KB_CTAS = 152 * 4;
+constexpr int KB_CTAS = 152 * 5;
 
 struct BoundsArgs {
   int n_req, width, n_pages, nkv;
@@ -73,50 +73,75 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
     if (page < 0 || page >= a.n_pages) continue;
     const int rows = min(KV_PAGE, e - blk * KV_PAGE);
     const uint8_t *src = a.kp + kv8_block(page, h, a.nkv, HD) + lane * 16;
+    // Per word of four bytes the pairs (0, 2) and (1, 3). A byte moved into the place of f16's exponent is its value times
+    // 2^-8, in four instructions for a pair where a conversion is two slow ones; but NaN is 480 then, and where that is the
+    // least or the largest the scan is made again with NaN left out.
     __half2 least[8], most[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      least[j] = as_half2(0x7c007c00u);
-      most[j] = as_half2(0xfc00fc00u);
-    }
-#pragma unroll 1
-    for (int r0 = lane / LPR; r0 < rows; r0 += 8 * RPI) {
-      uint4 w[8];                                      // (rows past the end: NaN, which the smaller and the larger both leave out)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = r0 + i * RPI < rows ? *(const uint4 *)(src + (size_t)(r0 - lane / LPR + i * RPI) * HD)
-                                   : make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t p0, p1;
-          e4m3x4_to_f16(v[j], p0, p1);
-          least[2 * j] = __hmin2(least[2 * j], as_half2(p0));
-          most[2 * j] = __hmax2(most[2 * j], as_half2(p0));
-          least[2 * j + 1] = __hmin2(least[2 * j + 1], as_half2(p1));
-          most[2 * j + 1] = __hmax2(most[2 * j + 1], as_half2(p1));
-        }
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1)
+    auto scan = [&](bool nan) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        least[j] = __hmin2(least[j], __shfl_xor_sync(0xffffffffu, least[j], o));
-        most[j] = __hmax2(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+        least[j] = as_half2(0x7c007c00u);
+        most[j] = as_half2(0xfc00fc00u);
       }
+#pragma unroll 1
+      for (int r0 = lane / LPR; r0 < rows; r0 += 8 * RPI) {
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // (past the end: the first row again)
+          const int r = r0 + i * RPI < rows ? r0 + i * RPI : r0;
+          w[i] = *(const uint4 *)(src + (size_t)(r - lane / LPR) * HD);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t e, o;
+            if (nan) {
+              uint32_t p0, p1;
+              e4m3x4_to_f16(v[j], p0, p1);             // times 2^-8: exact, the smallest is 2^-17
+              const __half2 h0 = __hmul2(as_half2(p0), as_half2(0x1c001c00u)), h1 = __hmul2(as_half2(p1), as_half2(0x1c001c00u));
+              e = __byte_perm(*(const uint32_t *)&h0, *(const uint32_t *)&h1, 0x5410);
+              o = __byte_perm(*(const uint32_t *)&h0, *(const uint32_t *)&h1, 0x7632);
+            } else {
+              const uint32_t s = v[j] << 8;
+              e = (s >> 1 & 0x3f803f80u) | (s & 0x80008000u);
+              o = (v[j] >> 1 & 0x3f803f80u) | (v[j] & 0x80008000u);
+            }
+            least[2 * j] = __hmin2(least[2 * j], as_half2(e));
+            most[2 * j] = __hmax2(most[2 * j], as_half2(e));
+            least[2 * j + 1] = __hmin2(least[2 * j + 1], as_half2(o));
+            most[2 * j + 1] = __hmax2(most[2 * j + 1], as_half2(o));
+          }
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          least[j] = __hmin2(least[j], __shfl_xor_sync(0xffffffffu, least[j], o));
+          most[j] = __hmax2(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+        }
+    };
+    scan(false);
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 l = __half22float2(least[j]), m = __half22float2(most[j]);
+      nan = nan || fminf(l.x, l.y) < -1.8f || fmaxf(m.x, m.y) > 1.8f;    // 480 2^-8, where 448 2^-8 is 1.75
+    }
+    if (__any_sync(0xffffffffu, nan)) scan(true);
     if (lane < 2 * LPR) {                              // the first row's lanes write the least, the second's the largest
       const bool up = lane >= LPR;
       uint32_t out[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 l = __half22float2(least[j]), m = __half22float2(most[j]);
-        const int x = l.x > m.x ? 0 : (int)(up ? ceilf(m.x * 0.25f) : floorf(l.x * 0.25f));
-        const int y = l.y > m.y ? 0 : (int)(up ? ceilf(m.y * 0.25f) : floorf(l.y * 0.25f));
-        out[j / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 8) << 16 * (j & 1);
+        const int x = l.x > m.x ? 0 : (int)(up ? ceilf(m.x * 64.f) : floorf(l.x * 64.f));
+        const int y = l.y > m.y ? 0 : (int)(up ? ceilf(m.y * 64.f) : floorf(l.y * 64.f));
+        out[j / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 16) << 8 * (j & 1);
       }
       *(uint4 *)(a.bounds + ((size_t)page * a.nkv + h) * (2 * HD) + lane * 16) = make_uint4(out[0], out[1], out[2], out[3]);
     }
@@ -201,6 +226,7 @@ __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int i = i0 + n * (KS_THREADS / LPR);
+      if (n * (KS_THREADS / LPR) >= tiles * 8) break;  // (the same for the CTA)
       float v[4];
       in[n].get(v);
       uint32_t top = 0;                               // bits of the largest magnitude: NaN and infinity are the largest
