@@ -27,6 +27,7 @@ tensor that requires one is refused (rope's gradient is rope with transpose=True
 qk_norm_rope_backward, for a Function of the caller's).
 """
 import ctypes
+import functools
 import math
 
 import torch
@@ -298,9 +299,14 @@ def _norm_args(table, positions, q, k, q_weight, k_weight, eps):
     if nq < 1 or nq + nk > 1 << 20:
         raise _error("1 to 2^20 heads")
     eps = float(eps)
-    if not (ctypes.c_float(eps).value > 0 and math.isfinite(ctypes.c_float(eps).value)):
+    if not 2.0 ** -150 < eps < 3.4028235e38:           # (positive and finite in fp32)
         raise _error("eps must be positive and finite")
     return rows, nq, _row_stride("q", q, nq, hd), nk, ks, eps
+
+
+def _new_like(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _like(name, t, ref, own):
@@ -330,15 +336,16 @@ def qk_norm_rope(table, positions, q, k, q_weight, k_weight, eps=1e-6, q_out=Non
     def body(s):
         qo, ko, qo_s, ko_s = q_out, k_out, qos, kos
         if qo is None:
-            qo, qo_s = torch.empty((rows, nq, hd), dtype=q.dtype, device=dev), nq * hd
+            qo, qo_s = _new_like(q), nq * hd
         if k is not None and ko is None:
-            ko, ko_s = torch.empty((rows, nk, hd), dtype=q.dtype, device=dev), nk * hd
+            ko, ko_s = _new_like(k), nk * hd
         _call("dflash_qk_norm_rope", s, table._ref, rows, nq, nk, hd, _dt(q), positions.data_ptr(), eps, q_weight.data_ptr(),
               _ptr(k_weight), q.data_ptr(), qs, _ptr(k), ks, qo.data_ptr(), qo_s, _ptr(ko), ko_s)
         return qo, ko
     return _on(dev, stream, body)
 
 
+@functools.cache
 def qk_norm_rope_workspace():
     """Bytes of workspace that qk_norm_rope_backward needs."""
     return _ffi.load().dflash_qk_norm_rope_workspace()
@@ -356,9 +363,10 @@ def qk_norm_rope_backward(table, positions, q, k, q_weight, k_weight, grad_q_out
         raise _error("grad_q_out goes with q and grad_k_out with k")
     gqs, gks = _like("grad_q_out", grad_q_out, q, None), _like("grad_k_out", grad_k_out, k, None)
     dqs, dks = _like("dq", dq, q, grad_q_out), _like("dk", dk, k, grad_k_out)
-    for x, y, name in ((dq, q, "dq"), (dk, k, "dk")):
-        if x is not None and rows and x.data_ptr() == y.data_ptr():
-            raise _error(f"{name} must not be {name[1:]}, which is read for the weight's gradient")
+    if rows and (dq is not None or dk is not None):
+        for x, y, name in ((dq, q, "dq"), (dk, k, "dk")):
+            if x is not None and x.data_ptr() == y.data_ptr():
+                raise _error(f"{name} must not be {name[1:]}, which is read for the weight's gradient")
     if workspace is not None:
         _tensor("workspace", workspace, _U1, (None,))
     _no_gradient("qk_norm_rope_backward", q, k, q_weight, k_weight, grad_q_out, grad_k_out, dq, dk)
@@ -368,13 +376,14 @@ def qk_norm_rope_backward(table, positions, q, k, q_weight, k_weight, grad_q_out
         a, b, w = dq, dk, workspace
         a_s, b_s = dqs, dks
         if a is None:
-            a, a_s = torch.empty((rows, nq, hd), dtype=q.dtype, device=dev), nq * hd
+            a, a_s = _new_like(q), nq * hd
         if k is not None and b is None:
-            b, b_s = torch.empty((rows, nk, hd), dtype=q.dtype, device=dev), nk * hd
+            b, b_s = _new_like(k), nk * hd
         if w is None:
             w = torch.empty((qk_norm_rope_workspace(),), dtype=torch.uint8, device=dev)
-        qw = torch.empty((hd,), dtype=torch.float32, device=dev)
-        kw = None if k is None else torch.empty((hd,), dtype=torch.float32, device=dev)
+        # one allocation for both weights' gradients
+        qw, kw = torch.empty((2, hd), dtype=torch.float32, device=dev).unbind()
+        kw = None if k is None else kw
         x = _ffi.QKNormRopeGrad(rows, nq, nk, hd, _dt(q), eps, positions.data_ptr(), q_weight.data_ptr(), _ptr(k_weight),
                                 q.data_ptr(), _ptr(k), grad_q_out.data_ptr(), _ptr(grad_k_out), qs, ks, gqs, gks, a.data_ptr(),
                                 _ptr(b), a_s, b_s, qw.data_ptr(), _ptr(kw), w.data_ptr(), w.numel())
