@@ -204,7 +204,9 @@ __global__ void __launch_bounds__(QN_THREADS, GRAD ? 2 : 3) k_qk_norm(const __gr
   pdl_trigger();
   const int pairs = a.rot / 2, heads = a.nq + a.nk;
   for (int i = threadIdx.x; i < pairs; i += QN_THREADS) s_turn[i] = a.turn[i];
-  const int first = (int)((int64_t)a.rows * blockIdx.x / gridDim.x), end = (int)((int64_t)a.rows * (blockIdx.x + 1) / gridDim.x);
+  // rows from `first` on, counted from there (that of many rows has many CTAs: no sum below passes 2^31)
+  const int first = (int)((int64_t)a.rows * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)a.rows * (blockIdx.x + 1) / gridDim.x) - first;
   const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
   const int tile = QN_THREADS / a.lanes / a.step;
   const int my_row = group / a.step, my_head = group % a.step, per_tile = (heads + a.step - 1) / a.step;
@@ -213,13 +215,13 @@ __global__ void __launch_bounds__(QN_THREADS, GRAD ? 2 : 3) k_qk_norm(const __gr
   for (int i = 0; i < R; ++i) c[i] = Chunk<V>(a, lane + i * a.lanes);
   pdl_wait();
   // the copies: DEPTH - 1 steps ahead
-  int f_row = first + my_row, f_head = my_head, f_slot = 0;
+  int f_row = my_row, f_head = my_head, f_slot = 0;
   auto fetch = [&]() {
     if (f_row < end && f_head < heads) {
       const bool isk = f_head >= a.nq;
       const int64_t from = (int64_t)(isk ? f_head - a.nq : f_head) * a.hd;
-      ring.fetch(f_slot, 0, (const T *)(isk ? a.k : a.q) + f_row * (isk ? a.ks : a.qs) + from, c, a.hd);
-      if constexpr (GRAD) ring.fetch(f_slot, 1, (const T *)(isk ? a.gk : a.gq) + f_row * (isk ? a.gks : a.gqs) + from, c, a.hd);
+      ring.fetch(f_slot, 0, (const T *)(isk ? a.k : a.q) + (first + f_row) * (isk ? a.ks : a.qs) + from, c, a.hd);
+      if constexpr (GRAD) ring.fetch(f_slot, 1, (const T *)(isk ? a.gk : a.gq) + (first + f_row) * (isk ? a.gks : a.gqs) + from, c, a.hd);
     }
     ring.commit();
     f_slot = f_slot + 1 == DEPTH ? 0 : f_slot + 1;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(QN_THREADS, GRAD ? 2 : 3) k_qk_norm(const __gr
     const int n = min(tile, end - row0) * pairs;
     for (int i = threadIdx.x; i < n; i += QN_THREADS) {
       const int r = (int)(i * a.by_pairs >> 20);       // i / pairs: i is below 2048 where pairs is above 1
-      const float2 t = phase_cs((uint64_t)(int64_t)a.positions[row0 + r] * s_turn[i - r * pairs]);
+      const float2 t = phase_cs((uint64_t)(int64_t)a.positions[first + row0 + r] * s_turn[i - r * pairs]);
       to[i] = t.x * a.magnitude;
       to[tile * pairs + i] = t.y * (GRAD ? -a.magnitude : a.magnitude);        // (the gradient turns back)
     }
@@ -255,9 +257,9 @@ __global__ void __launch_bounds__(QN_THREADS, GRAD ? 2 : 3) k_qk_norm(const __gr
 #pragma unroll
         for (int j = 0; j < V; ++j) wsum[k][i][j] = make_float2(0.f, 0.f);
   }
-  if (first < end) angles(first, cs);
+  if (end > 0) angles(0, cs);
   int slot = 0;
-  for (int row0 = first, buf = 0; row0 < end; row0 += tile, buf ^= 1) {
+  for (int row0 = 0, buf = 0; row0 < end; row0 += tile, buf ^= 1) {
     __syncthreads();                                  // this tile's angles are there, the last one's are done with
     if (row0 + tile < end) angles(row0 + tile, cs + 2 * (buf ^ 1) * tile * pairs);
     const int row = row0 + my_row;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(QN_THREADS, GRAD ? 2 : 3) k_qk_norm(const __gr
       if constexpr (GRAD) m = head_sum(dot.x + dot.y, a.lanes) * inv * inv_hd;       // r mean(g x)
       if (row >= end || h >= heads) continue;
       const int64_t to = (int64_t)(isk ? h - a.nq : h) * a.hd;
-      T *dst = (T *)(isk ? a.ko : a.qo) + row * (isk ? a.kos : a.qos) + to;
+      T *dst = (T *)(isk ? a.ko : a.qo) + (first + row) * (isk ? a.kos : a.qos) + to;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         float2 y[V];
@@ -406,8 +408,9 @@ cudaError_t launch_norm(NormArgs &a, int width, int *ctas, cudaStream_t s) {
   // leaves too few CTAs, and no more than there are heads.
   a.step = 1;
   while (a.step < per && a.step < heads && (a.step < 8 || (int64_t)a.rows * a.step < (int64_t)most * per)) a.step *= 2;
-  const int tile = per / a.step, tiles = (a.rows + tile - 1) / tile;
-  *ctas = tiles < most ? tiles : most;
+  const int tile = per / a.step;
+  const int64_t tiles = ((int64_t)a.rows + tile - 1) / tile;
+  *ctas = tiles < most ? (int)tiles : most;
   if (width == W && a.lanes == a.chunks && a.hd % (2 * W) == 0) return launch_norm<T, W, 1, true, GRAD>(a, *ctas, s);
   if (width == W) return launch_norm<T, W, 1, false, GRAD>(a, *ctas, s);
   return width == 2 ? launch_norm<T, 2, 2, false, GRAD>(a, *ctas, s) : launch_norm<T, 1, 4, false, GRAD>(a, *ctas, s);
