@@ -8,7 +8,7 @@ namespace dflash {
 // A warp per (page, kv head): lanes read 16 bytes of a row each, several rows at a time, and keep the least and the
 // largest of their 16 dims as f16 pairs (exact). Bound by the read of the pages.
 constexpr int KB_THREADS = 256;
-constexpr int KB_CTAS = 152 * 5;
+constexpr int KB_CTAS = 152 * 4;
 
 struct BoundsArgs {
   int n_req, width, n_pages, nkv;
@@ -251,13 +251,15 @@ __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x
       if (l == 0) unit[i] = i < here && fin ? __uint_as_float((uint32_t)(117 + k) << 23) : 0.f;
     }
     __syncthreads();
-    for (int p0 = blockIdx.x * KS_TILE + warp * 16; p0 < blocks; p0 += gridDim.x * KS_TILE) {
+    auto page_at = [&](int p) { return p < blocks ? a.table[(size_t)b * a.width + p] : -1; };
+    const int p_first = blockIdx.x * KS_TILE + warp * 16, p_step = gridDim.x * KS_TILE;
+    int ahead[2] = {page_at(p_first + g), page_at(p_first + g + 8)};
+    for (int p0 = p_first; p0 < blocks; p0 += p_step) {
       int page[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int p = p0 + g + 8 * y;
-        page[y] = p < blocks ? a.table[(size_t)b * a.width + p] : -1;
-        if (page[y] >= a.n_pages) page[y] = -1;
+        page[y] = ahead[y] >= a.n_pages ? -1 : ahead[y];
+        ahead[y] = page_at(p0 + p_step + g + 8 * y);
       }
       uint32_t lo[KS][4], hi[KS][4];
 #pragma unroll
@@ -276,19 +278,30 @@ __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x
         }
       }
       float best[2] = {-INFINITY, -INFINITY};
-      for (int n = 0; n < tiles; ++n) {
-        float up[4] = {0.f, 0.f, 0.f, 0.f}, dn[4] = {0.f, 0.f, 0.f, 0.f};
+      // two tiles of rows at a time, whose chains of sums interleave (an odd last one is its own partner)
+      for (int n = 0; n < tiles; n += 2) {
+        const int at[2] = {n, min(n + 1, tiles - 1)};
+        float up[2][4], dn[2][4];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint4 q = qf[n][k][lane];
-          mma_16816(up, hi[k], q.x, q.y);
-          mma_16816(dn, lo[k], q.z, q.w);
-        }
-        const float u0 = unit[8 * n + 2 * t], u1 = unit[8 * n + 2 * t + 1];
+        for (int z = 0; z < 2; ++z)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          if (u0 > 0.f) best[y] = fmaxf(best[y], (up[2 * y] + dn[2 * y]) * u0);
-          if (u1 > 0.f) best[y] = fmaxf(best[y], (up[2 * y + 1] + dn[2 * y + 1]) * u1);
+          for (int i = 0; i < 4; ++i) up[z][i] = dn[z][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint4 q = qf[at[z]][k][lane];
+            mma_16816(up[z], hi[k], q.x, q.y);
+            mma_16816(dn[z], lo[k], q.z, q.w);
+          }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float u0 = unit[8 * at[z] + 2 * t], u1 = unit[8 * at[z] + 2 * t + 1];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (u0 > 0.f) best[y] = fmaxf(best[y], (up[z][2 * y] + dn[z][2 * y]) * u0);
+            if (u1 > 0.f) best[y] = fmaxf(best[y], (up[z][2 * y + 1] + dn[z][2 * y + 1]) * u1);
+          }
         }
       }
 #pragma unroll
@@ -315,7 +328,7 @@ constexpr int KC_HELD = 4096;                         // keys that are kept in s
 __global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
   __shared__ int hist[256], warp_tot[KC_THREADS / 32];
   __shared__ uint32_t held[KC_HELD];
-  __shared__ int s_bin, s_left;
+  __shared__ int s_bin, s_left, s_all;
   const Kv8AttnArgs &a = x.a;
   pdl_trigger();
   pdl_wait();
@@ -366,6 +379,7 @@ __global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
           if (before < left && before + c[i] >= left) {
             s_bin = 255 - 8 * lane - i;
             s_left = left - before;
+            s_all = c[i] == left - before;
           }
           before += c[i];
         }
@@ -374,7 +388,13 @@ __global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
     __syncthreads();
     prefix |= (uint32_t)s_bin << shift;
     left = s_left;
+    const bool all = s_all;
     __syncthreads();
+    if (all) {                                         // every key that begins so is taken: none is below prefix
+      --prefix;                                        // (a bin of keys, none of them 0: score -NaN is none)
+      left = 0;
+      break;
+    }
   }
   // keys above prefix, and the first `left` equal to it
   int done = 0, equal = 0;
