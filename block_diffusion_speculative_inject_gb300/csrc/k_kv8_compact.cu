@@ -3,8 +3,9 @@
 // A CTA per (request, kv head, layer, K or V) takes the pages that rows go to one after another, from the first: a row
 // goes to its own place or below, so a page's rows come from that page or later ones, and none that is still to
 // be read has been written. Per page: the rows' bytes go to shared memory with their pages' scales, the largest
-// value gives the page's scale as the append's does, and the bytes are written anew. It is all latency: a few
-// rows per CTA.
+// value gives the page's scale as the append's does, and the bytes are written anew. It is all latency (lengths, the rows'
+// places, their pages, their bytes): 4.6 us for 8 rows of one layer of 8 x 128, 24 us for 8 paths of 1 .. 16 rows in 32 layers,
+// whose 4096 CTAs are not quite two waves (49 us with 256 threads a CTA that went over the whole page).
 #include "kv8.cuh"
 
 namespace dflash {

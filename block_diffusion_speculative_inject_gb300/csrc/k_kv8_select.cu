@@ -6,7 +6,9 @@ namespace dflash {
 
 // ---------------------------------------------------------------- bounds
 // A warp per (page, kv head): lanes read 16 bytes of a row each, several rows at a time, and keep the least and the
-// largest of their 16 dims as f16 pairs (exact). Bound by the read of the pages.
+// largest of their 16 dims. The read of the pages and the instructions (two minima and two maxima a word) bound it about
+// alike: 47 us for 8 prompts of 16384 .. 32768 tokens of 8 x 128 (201 MB of keys, 4.6 TB/s); 65 with a conversion of every
+// pair to f16, 56 with shifts and masks in its place.
 constexpr int KB_THREADS = 256;
 constexpr int KB_CTAS = 152 * 4;
 
@@ -18,6 +20,9 @@ struct BoundsArgs {
 };
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *(const __half2 *)&x; }
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *(const __nv_bfloat162 *)&x; }
+// bytes 0x7f / 0xff of a word, as 0x80 in each
+__device__ __forceinline__ uint32_t nan_bytes_of(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 template <int HD>
 __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
@@ -73,77 +78,101 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
     if (page < 0 || page >= a.n_pages) continue;
     const int rows = min(KV_PAGE, e - blk * KV_PAGE);
     const uint8_t *src = a.kp + kv8_block(page, h, a.nkv, HD) + lane * 16;
-    // Per word of four bytes the pairs (0, 2) and (1, 3). A byte moved into the place of f16's exponent is its value times
-    // 2^-8, in four instructions for a pair where a conversion is two slow ones; but NaN is 480 then, and where that is the
-    // least or the largest the scan is made again with NaN left out.
-    __half2 least[8], most[8];
-    auto scan = [&](bool nan) {
+    // Per word of four bytes the pairs (0, 2) and (1, 3). Read as bf16, a pair with its values in the high bytes is in their
+    // order whatever the low bytes hold (they only decide between equals), so that a word takes one shift and no
+    // conversion. NaN passes every value or is left out; where it shows (0x7f in the result), or nothing does, the scan is
+    // made again in f16, which leaves NaN out.
+    auto load = [&](int r0, uint4 (&w)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // (past the end: the first row again)
+        const int r = r0 + i * RPI < rows ? r0 + i * RPI : r0;
+        w[i] = *(const uint4 *)(src + (size_t)(r - lane / LPR) * HD);
+      }
+    };
+    __nv_bfloat162 least[8], most[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      least[j] = as_bf162(0x7f7f7f7fu);
+      most[j] = as_bf162(0xff7fff7fu);
+    }
+#pragma unroll 1
+    for (int r0 = lane / LPR; r0 < rows; r0 += 8 * RPI) {
+      uint4 w[8];
+      load(r0, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 e = as_bf162(v[j] << 8), o = as_bf162(v[j]);
+          least[2 * j] = __hmin2(least[2 * j], e);
+          most[2 * j] = __hmax2(most[2 * j], e);
+          least[2 * j + 1] = __hmin2(least[2 * j + 1], o);
+          most[2 * j + 1] = __hmax2(most[2 * j + 1], o);
+        }
+      }
+    }
+    __syncwarp();
+    uint32_t nan = 0;
+    uint32_t out[8];                                   // the least (the largest) of dims 2 j and 2 j + 1 in the second (fourth) byte
+    const bool up = lane >= LPR;                       // the first row's lanes write the least, the second's the largest
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) {
+        least[j] = __hmin2(least[j], __shfl_xor_sync(0xffffffffu, least[j], o));
+        most[j] = __hmax2(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+      }
+      const uint32_t l = *(const uint32_t *)&least[j], m = *(const uint32_t *)&most[j];
+      nan |= nan_bytes_of(l) | nan_bytes_of(m);
+      out[j] = up ? m : l;
+    }
+    if (__any_sync(0xffffffffu, (nan & 0x80008000u) != 0)) {
+      __half2 lh[8], mh[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        least[j] = as_half2(0x7c007c00u);
-        most[j] = as_half2(0xfc00fc00u);
+        lh[j] = as_half2(0x7c007c00u);
+        mh[j] = as_half2(0xfc00fc00u);
       }
 #pragma unroll 1
-      for (int r0 = lane / LPR; r0 < rows; r0 += 8 * RPI) {
-        uint4 w[8];
+      for (int r = lane / LPR; r < rows; r += RPI) {
+        const uint4 w = *(const uint4 *)(src + (size_t)(r - lane / LPR) * HD);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // (past the end: the first row again)
-          const int r = r0 + i * RPI < rows ? r0 + i * RPI : r0;
-          w[i] = *(const uint4 *)(src + (size_t)(r - lane / LPR) * HD);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t e, o;
-            if (nan) {
-              uint32_t p0, p1;
-              e4m3x4_to_f16(v[j], p0, p1);             // times 2^-8: exact, the smallest is 2^-17
-              const __half2 h0 = __hmul2(as_half2(p0), as_half2(0x1c001c00u)), h1 = __hmul2(as_half2(p1), as_half2(0x1c001c00u));
-              e = __byte_perm(*(const uint32_t *)&h0, *(const uint32_t *)&h1, 0x5410);
-              o = __byte_perm(*(const uint32_t *)&h0, *(const uint32_t *)&h1, 0x7632);
-            } else {
-              const uint32_t s = v[j] << 8;
-              e = (s >> 1 & 0x3f803f80u) | (s & 0x80008000u);
-              o = (v[j] >> 1 & 0x3f803f80u) | (v[j] & 0x80008000u);
-            }
-            least[2 * j] = __hmin2(least[2 * j], as_half2(e));
-            most[2 * j] = __hmax2(most[2 * j], as_half2(e));
-            least[2 * j + 1] = __hmin2(least[2 * j + 1], as_half2(o));
-            most[2 * j + 1] = __hmax2(most[2 * j + 1], as_half2(o));
-          }
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p0, p1;
+          e4m3x4_to_f16(v[j], p0, p1);
+          const __half2 e = as_half2(__byte_perm(p0, p1, 0x5410)), o = as_half2(__byte_perm(p0, p1, 0x7632));
+          lh[2 * j] = __hmin2(lh[2 * j], e);
+          mh[2 * j] = __hmax2(mh[2 * j], e);
+          lh[2 * j + 1] = __hmin2(lh[2 * j + 1], o);
+          mh[2 * j + 1] = __hmax2(mh[2 * j + 1], o);
         }
       }
       __syncwarp();
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1)
+      for (int j = 0; j < 8; ++j) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          least[j] = __hmin2(least[j], __shfl_xor_sync(0xffffffffu, least[j], o));
-          most[j] = __hmax2(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+        for (int o = LPR; o < 32; o <<= 1) {
+          lh[j] = __hmin2(lh[j], __shfl_xor_sync(0xffffffffu, lh[j], o));
+          mh[j] = __hmax2(mh[j], __shfl_xor_sync(0xffffffffu, mh[j], o));
         }
-    };
-    scan(false);
-    bool nan = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 l = __half22float2(least[j]), m = __half22float2(most[j]);
-      nan = nan || fminf(l.x, l.y) < -1.8f || fmaxf(m.x, m.y) > 1.8f;    // 480 2^-8, where 448 2^-8 is 1.75
+        // back to bytes (exact); a dim of nothing but NaN: 0
+        const float2 l = __half22float2(lh[j]), m = __half22float2(mh[j]);
+        const uint32_t x = f32_to_e4m3x2(l.x > m.x ? 0.f : up ? m.x : l.x, l.y > m.y ? 0.f : up ? m.y : l.y);
+        out[j] = __byte_perm(x, 0, 0x1404);
+      }
     }
-    if (__any_sync(0xffffffffu, nan)) scan(true);
-    if (lane < 2 * LPR) {                              // the first row's lanes write the least, the second's the largest
-      const bool up = lane >= LPR;
-      uint32_t out[4] = {0, 0, 0, 0};
+    if (lane < 2 * LPR) {
+      uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 l = __half22float2(least[j]), m = __half22float2(most[j]);
-        const int x = l.x > m.x ? 0 : (int)(up ? ceilf(m.x * 64.f) : floorf(l.x * 64.f));
-        const int y = l.y > m.y ? 0 : (int)(up ? ceilf(m.y * 64.f) : floorf(l.y * 64.f));
-        out[j / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 16) << 8 * (j & 1);
+        const float2 v = e4m3x2_to_f32(__byte_perm(out[j], 0, 0x4431));
+        const int x = (int)(up ? ceilf(v.x * 0.25f) : floorf(v.x * 0.25f)), y = (int)(up ? ceilf(v.y * 0.25f) : floorf(v.y * 0.25f));
+        b[j / 2] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 16) << 8 * (j & 1);
       }
-      *(uint4 *)(a.bounds + ((size_t)page * a.nkv + h) * (2 * HD) + lane * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+      *(uint4 *)(a.bounds + ((size_t)page * a.nkv + h) * (2 * HD) + lane * 16) = make_uint4(b[0], b[1], b[2], b[3]);
     }
   }
 }
@@ -154,6 +183,11 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
 // 2^17 and the sums of a row at most 2^24, so every partial sum is a whole number that fp32 (and an accumulator that
 // truncates) holds. Contraction indices are permuted as in the attention for few rows: a lane's 16 bytes are the dims of
 // four steps.
+//
+// The bounds are few bytes (26 MB for 8 x 16 rows of 40 heads over 1024 .. 2049 blocks, 4 us), and what takes 26 us there are
+// the latencies of a round (table, bounds, the products' chains of sums) with 16 warps per SM, and the reads of q's
+// fragments from shared memory. Both halves of q are kept there (46 us when they were made at every use), and all
+// of a CTA's rows are loaded at once.
 constexpr int KS_THREADS = 256;
 constexpr int KS_TILE = KS_THREADS / 2;               // blocks of a CTA at once: 16 of a warp
 constexpr int KS_ROWS = 80;                           // rows of q staged at once: 40 KB
@@ -321,7 +355,8 @@ __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x
 // ---------------------------------------------------------------- the n_select best
 // A CTA per (request, kv head). Keys rank as the scores do (fixed blocks above all); four passes over the keys' bytes,
 // each a histogram of the keys that agree with the threshold so far, find the last key that is taken and how many of
-// those equal to it; the chosen ones are then written in order.
+// those equal to it; the passes end where all keys of the last bin are taken, and the chosen ones are then written in
+// order. It is latency: 9 us for 2049 keys, most of it barriers.
 constexpr int KC_THREADS = 512;
 constexpr int KC_HELD = 4096;                         // keys that are kept in shared memory
 
@@ -391,7 +426,7 @@ __global__ void __launch_bounds__(KC_THREADS) k_kv8_choose(const SelectArgs x) {
     const bool all = s_all;
     __syncthreads();
     if (all) {                                         // every key that begins so is taken: none is below prefix
-      --prefix;                                        // (a bin of keys, none of them 0: score -NaN is none)
+      --prefix;                                        // (never below 0: then all keys would be taken, which are more)
       left = 0;
       break;
     }
@@ -456,7 +491,8 @@ bool choice_ok(const dflash_kv8_cache *c, const dflash_kv8_choice *x) {
 }
 template <typename T>
 cudaError_t launch_select(const SelectArgs &x, int hd, cudaStream_t s) {
-  // CTAs of a (request, kv head), which take KS_TILE blocks at a time in turn: as many as are resident
+  // CTAs of a (request, kv head), which take KS_TILE blocks at a time in turn: as many as are resident (64 items over
+  // 1024 .. 2049 blocks with 2 each 43.5 us, 4 34.4, 5 36.2, 8 37.2, 17 40.8: each makes q's whole numbers for itself)
   const long items = (long)x.a.n_req * x.a.nkv, want = items < 304 ? 304 / items : 1;
   const long most = ((long)x.a.width + KS_TILE - 1) / KS_TILE;
   const dim3 g((unsigned)(want < most ? want : most), x.a.nkv, x.a.n_req), t(KS_THREADS);

@@ -73,6 +73,8 @@ def _tensor(name, t, dtypes, shape, contiguous=True):
 def _row_stride(name, t, heads, hd):
     """Row stride of [rows, heads, hd] whose heads are contiguous."""
     least = heads * hd
+    if t.is_contiguous():
+        return least
     rows, by_head, by_dim = t.stride()
     if (by_dim != 1 and hd > 1) or (by_head != hd and heads > 1):
         raise _error(f"{name}: the heads of a row must be contiguous")
@@ -315,9 +317,11 @@ def _like(name, t, ref, own):
         return 0
     if ref is None:
         raise _error(f"{name} without k")
-    _, heads, hd = _tensor(name, t, (ref.dtype,), ref.shape, False)
+    rows, heads, hd = ref.shape
+    if not isinstance(t, torch.Tensor) or t.dtype != ref.dtype or t.shape != ref.shape:
+        _tensor(name, t, (ref.dtype,), ref.shape, False)
     stride = _row_stride(name, t, heads, hd)
-    if own is not None and t.shape[0] > 1 and t.data_ptr() == own.data_ptr() and stride != own.stride(0):
+    if own is not None and rows > 1 and t.data_ptr() == own.data_ptr() and stride != own.stride(0):
         raise _error(f"{name}: in place only with the same strides")
     return stride
 
@@ -381,9 +385,8 @@ def qk_norm_rope_backward(table, positions, q, k, q_weight, k_weight, grad_q_out
             b, b_s = _new_like(k), nk * hd
         if w is None:
             w = torch.empty((qk_norm_rope_workspace(),), dtype=torch.uint8, device=dev)
-        # one allocation for both weights' gradients
-        qw, kw = torch.empty((2, hd), dtype=torch.float32, device=dev).unbind()
-        kw = None if k is None else kw
+        qw = torch.empty((hd,), dtype=torch.float32, device=dev)
+        kw = None if k is None else torch.empty_like(qw)
         x = _ffi.QKNormRopeGrad(rows, nq, nk, hd, _dt(q), eps, positions.data_ptr(), q_weight.data_ptr(), _ptr(k_weight),
                                 q.data_ptr(), _ptr(k), grad_q_out.data_ptr(), _ptr(grad_k_out), qs, ks, gqs, gks, a.data_ptr(),
                                 _ptr(b), a_s, b_s, qw.data_ptr(), _ptr(kw), w.data_ptr(), w.numel())
