@@ -7,12 +7,13 @@
 // power of two that its chunks need, at most 32), which hold it in registers between the sum of squares and the
 // rotation; a chunk is V dims and, in the half layout, their partners, or the V dims that follow.
 //
-// 32768 rows of 48 x 128 bf16 take 140 us (805 MB, 5.8 TB/s; ncu: 72% of the issue slots), the gradient of 16384 rows of
-// 40 x 128 106 us with the sum over its CTAs (503 MB, 4.7 TB/s, 56%). What paid, in the forward pass: sines in registers
-// for all heads of a row (219 us when every head read them from shared memory, four lanes to a bank), copies ahead
-// through shared memory, paired arithmetic and packed conversions (248 without these two), as many CTAs as are
-// resident (146 with a third more). The gradient keeps both weights' sums, 128 registers for two CTAs per SM (110 us at 154
-// registers and one CTA).
+// 32768 rows of 48 x 128 bf16 take 128 us (805 MB, 6.3 TB/s), the gradient of 16384 rows of 40 x 128 98 us with the sum over
+// its CTAs (503 MB, 5.1 TB/s; latencies at two CTAs per SM). What paid, in the forward pass: sines in registers for all heads
+// of a row (219 us when every head read them from shared memory, four lanes to a bank), copies ahead through shared memory,
+// paired arithmetic and packed conversions (248 without these two), as many CTAs as are resident (146 with a third more), and
+// no more copies ahead than two (142 with one, 138 with four: the shared memory is the first-level cache's). The gradient
+// keeps both weights' sums, 128 registers for two CTAs per SM (110 us at 154 registers and one CTA; 105 with three copies
+// ahead, 101 with two, 98 with half as many groups to a row).
 #include <cmath>
 
 #include "rope.cuh"
@@ -21,7 +22,7 @@ namespace dflash {
 
 constexpr int QN_THREADS = 256;
 constexpr int QN_CTAS = 152 * 3, QN_CTAS_GRAD = 152 * 2;      // most CTAs: as many as are resident
-constexpr int QN_DEPTH = 5, QN_DEPTH_GRAD = 4;        // heads of a lane that are held or on their way
+constexpr int QN_DEPTH = 3, QN_DEPTH_GRAD = 3;        // heads of a lane that are held or on their way
 
 struct NormArgs {
   uint64_t turn[128];
@@ -411,11 +412,11 @@ cudaError_t launch_norm(NormArgs &a, int width, int *ctas, cudaStream_t s) {
   const int per = QN_THREADS / a.lanes, heads = a.nq + a.nk;
   a.by_pairs = ((1u << 20) + a.rot / 2 - 1) / (a.rot / 2);
   constexpr int most = GRAD ? QN_CTAS_GRAD : QN_CTAS;
-  // Groups of lanes that share a row: 8, for more than one row's angles at a time (forward and gradient above with 4:
-  // 155 and 128 us, 8: 147 and 123, 16: 141 and 140, all with 608 CTAs); all of them where that leaves too few CTAs, and
-  // no more than there are heads.
+  // Groups of lanes that share a row: 8, for more than one row's angles at a time, 4 in the gradient (forward and gradient
+  // above with 4 129 and 98 us, with 8 128 and 101); all of them where that leaves too few CTAs, and no more than there
+  // are heads.
   a.step = 1;
-  while (a.step < per && a.step < heads && (a.step < 8 || (int64_t)a.rows * a.step < (int64_t)most * per)) a.step *= 2;
+  while (a.step < per && a.step < heads && (a.step < (GRAD ? 4 : 8) || (int64_t)a.rows * a.step < (int64_t)most * per)) a.step *= 2;
   const int tile = per / a.step;
   const int64_t tiles = ((int64_t)a.rows + tile - 1) / tile;
   *ctas = tiles < most ? (int)tiles : most;

@@ -103,7 +103,7 @@ def test_norm_and_gradient(dtype, rows, nq, nk, hd, rot, inter, scaling):
     dq, dk, dqw, dkw = qk_norm_rope_backward(table, pos.cuda(), d["q"], k[0], d["wq"], k[1], d["dq"], k[2], eps=eps)
     args = (pos, rot, freq, mag, inter, eps)
     _check_norm(q, x["q"], x["wq"], *args)
-    # a lane adds a term for each of its heads in a tile of at most 8 rows; 152 * 4 CTAs share the tiles
+    # a lane adds at most 8 terms for each head here, then 8 warps and 5 shuffles, 19 CTAs' sums and 5 shuffles
     chain = 8 * max(nq, nk) + 8 + 5 + 19 + 5
     _check_grad(dq, dqw, x["q"], x["wq"], x["dq"], *args, chain)
     if nk:
