@@ -205,6 +205,32 @@ def test_norm_many_rows_repeat_and_no_rows():
     assert bool((z[2] == 0).all()) and bool((z[3] == 0).all()) and z[0].shape == (0, nq, hd)
 
 
+def test_norm_most_rows():
+    """The largest number of rows, in place: a CTA's last rows are near 2^31."""
+    from block_diffusion_speculative_inject_gb300 import Rope, qk_norm_rope
+    rows = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator().manual_seed(4)
+    at = [0, 1, 255, 256, 2 ** 30 + 77, rows - 257, rows - 2, rows - 1]
+    pos = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    q = torch.ones((rows, 1, 2), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn((len(at), 1, 2), generator=g).to(torch.bfloat16)
+    p = torch.randint(0, 9999, (len(at),), generator=g, dtype=torch.int32)
+    w = torch.randn(2, generator=g).to(torch.bfloat16)
+    for i, r in enumerate(at):
+        q[r], pos[r] = x[i].cuda(), int(p[i])
+    qk_norm_rope(Rope(2), pos, q, None, w.cuda(), None, q_out=q)
+    got = torch.stack([q[r] for r in at])
+    _check_norm(got, x, w, p, 2, *R.rope_freq(2, 1e6), False, 1e-6)
+    for start in range(2, rows, 1 << 28):              # position 0, all ones: the weights, to within one rounding
+        part = q[start:start + (1 << 28), 0]
+        same = (part == part[100]).all(1)
+        assert int((~same).sum()) <= len(at)
+    del q, pos, part, same
+    torch.cuda.empty_cache()
+
+
 def test_norm_inside_a_function_of_the_caller():
     """Autograd over both outputs through the caller's Function: the gradients are the backward call's, bit for bit."""
     from block_diffusion_speculative_inject_gb300 import Rope, qk_norm_rope, qk_norm_rope_backward
