@@ -138,6 +138,19 @@ def _dt(t):
     return _ffi.BF16 if t.dtype is torch.bfloat16 else _ffi.F32
 
 
+class _LaidOut:
+    """Attributes can be set until `_sealed` is: the library is given what was laid out from them."""
+    _sealed = False
+
+    def __setattr__(self, name, value):
+        if self._sealed:
+            raise _error(f"{type(self).__name__}: {name} cannot be changed, make a new one")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise _error(f"{type(self).__name__}: {name} cannot be taken away")
+
+
 class KV8Cache:
     """An 8-bit paged cache: k_pages [n_pages, kv heads, 64, head dim] and v_pages [n_pages, kv heads,
     head dim, 64] float8_e4m3fn, k_scale / v_scale [n_pages, kv heads] fp32, powers of two. The tensors are
@@ -179,11 +192,12 @@ class KV8Cache:
         return dev
 
 
-class KV8Layers:
-    """The caches of a model's layers (1 to 128, of one shape, on one GPU), checked and laid out once for kv8_compact."""
+class KV8Layers(_LaidOut):
+    """The caches of a model's layers (1 to 128, of one shape, on one GPU), checked and laid out once for kv8_compact; `caches`
+    is the tuple of them."""
 
     def __init__(self, caches):
-        self.caches = caches = list(caches)
+        self.caches = caches = tuple(caches)
         if not 1 <= len(caches) <= 128 or not all(isinstance(c, KV8Cache) for c in caches):
             raise _error("1 to 128 KV8Cache")
         c = caches[0]
@@ -194,6 +208,7 @@ class KV8Layers:
                 raise _error("a cache is given twice")
         self._array = (_ffi.KV8Cache * len(caches))(*(x._c for x in caches))
         self._dev = c._dev if all(x._dev == c._dev for x in caches) else None
+        self._sealed = True
 
 
 def page_plan(ctx_len, n_new, block_table, free_list, n_free, max_rows, stream=None):
@@ -569,7 +584,7 @@ def kv8_compact(caches, block_table, base_len, keep, n_keep, stream=None):
     dev = _device(block_table, base_len, keep, n_keep)
     if dev != caches._dev:
         raise _error(f"the caches' tensors are not all on cuda:{dev}")
-    _on(dev, stream, lambda s: _call("dflash_kv8_compact", s, len(caches.caches), caches._array, n, width, most,
+    _on(dev, stream, lambda s: _call("dflash_kv8_compact", s, len(caches._array), caches._array, n, width, most,
                                      base_len.data_ptr(), keep.data_ptr(), n_keep.data_ptr(), block_table.data_ptr()))
 
 

@@ -221,3 +221,30 @@ def test_binding_refuses_to_lose_a_gradient():
     # the choice is whole numbers: a q that requires a gradient loses none
     with pytest.raises(pkg.DFlashError, match="CUDA device"):
         pkg.kv8_select(cache(), torch.zeros((4, 2, 2, 64), dtype=torch.int8), x(2, True), i4(2), i4(1), i4(1, 4), 2)
+
+
+def test_layers_stay_as_they_were_laid_out(monkeypatch):
+    """What kv8_compact hands to the library is the array that was checked: its caches can be neither added to nor replaced."""
+    import block_diffusion_speculative_inject_gb300.kv8 as kv8
+    pkg, i4, e4, bf, cache = _things()
+    given = [cache(), cache()]
+    layers = pkg.KV8Layers(given)
+    seen = []
+    monkeypatch.setattr(kv8, "_device", lambda *a: layers._dev)
+    monkeypatch.setattr(kv8, "_on", lambda dev, stream, body: body(0))
+    monkeypatch.setattr(kv8, "_call", lambda name, s, n, array, *a: seen.append((n, array)))
+    move = (i4(2, 4), i4(2), i4(2, 3), i4(2))
+
+    def laid_out():
+        pkg.kv8_compact(layers, *move)
+        n, array = seen.pop()
+        assert n == len(array) == 2
+        assert [c.k_pages for c in array] == [c.k_pages.data_ptr() for c in given[:2]]
+    laid_out()
+    given.append(cache())                              # (the caller's own list)
+    laid_out()
+    for change in (lambda: layers.caches.append(cache()), lambda: layers.caches.pop(), lambda: layers.caches.__setitem__(0, cache()),
+                   lambda: setattr(layers, "caches", given), lambda: setattr(layers, "_array", None), lambda: delattr(layers, "caches")):
+        with pytest.raises((AttributeError, pkg.DFlashError)):
+            change()
+        laid_out()
