@@ -151,10 +151,10 @@ class _LaidOut:
         raise _error(f"{type(self).__name__}: {name} cannot be taken away")
 
 
-class KV8Cache:
+class KV8Cache(_LaidOut):
     """An 8-bit paged cache: k_pages [n_pages, kv heads, 64, head dim] and v_pages [n_pages, kv heads,
     head dim, 64] float8_e4m3fn, k_scale / v_scale [n_pages, kv heads] fp32, powers of two. The tensors are
-    the caller's; `KV8Cache.empty` allocates them."""
+    the caller's, and stay those of the cache; `KV8Cache.empty` allocates them."""
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale):
         n, h, _, d = _tensor("k_pages", k_pages, _E4M3, (None, None, PAGE, None))
@@ -171,6 +171,7 @@ class KV8Cache:
                                 v_pages=v_pages.data_ptr(), k_scale=k_scale.data_ptr(), v_scale=v_scale.data_ptr())
         self._ref = ctypes.byref(self._c)
         self._dev = k_pages.get_device() if len({t.device for t in self._tensors()}) == 1 else None
+        self._sealed = True
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, head_dim, device="cuda"):

@@ -248,3 +248,18 @@ def test_layers_stay_as_they_were_laid_out(monkeypatch):
         with pytest.raises((AttributeError, pkg.DFlashError)):
             change()
         laid_out()
+
+
+def test_caches_stay_as_they_were_laid_out():
+    """A cache's tensors and sizes are what the library was given: another tensor in their place would leave the calls with
+    the addresses of the old one, whose memory may be another's by then."""
+    pkg, i4, e4, bf, cache = _things()
+    c = cache()
+    was = [t.data_ptr() for t in c._tensors()]
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale", "n_pages", "n_kv_heads", "head_dim"):
+        with pytest.raises(pkg.DFlashError, match=name):
+            setattr(c, name, getattr(cache(8), name))
+        with pytest.raises(pkg.DFlashError, match=name):
+            delattr(c, name)
+    assert [t.data_ptr() for t in c._tensors()] == was == [c._c.k_pages, c._c.v_pages, c._c.k_scale, c._c.v_scale]
+    assert c.n_pages == c._c.n_pages == 4
