@@ -402,7 +402,8 @@ def qk_norm_rope_backward(table, positions, q, k, q_weight, k_weight, grad_q_out
         if w is None:
             w = torch.empty((qk_norm_rope_workspace(),), dtype=torch.uint8, device=dev)
         qw = torch.empty((hd,), dtype=torch.float32, device=dev)
-        kw = None if k is None else torch.empty_like(qw)
+        # (the library leaves dk_weight alone where k has no heads: a sum over nothing)
+        kw = None if k is None else torch.empty_like(qw) if nk else torch.zeros_like(qw)
         x = _ffi.QKNormRopeGrad(rows, nq, nk, hd, _dt(q), eps, positions.data_ptr(), q_weight.data_ptr(), _ptr(k_weight),
                                 q.data_ptr(), _ptr(k), grad_q_out.data_ptr(), _ptr(grad_k_out), qs, ks, gqs, gks, a.data_ptr(),
                                 _ptr(b), a_s, b_s, qw.data_ptr(), _ptr(kw), w.data_ptr(), w.numel())

@@ -447,7 +447,7 @@ dflash_status dflash_rope_apply(void *stream, const dflash_rope *rope, int32_t r
  *   n = R^T y, g = n * weight, r = 1 / sqrt(mean(x^2) + eps):
  *   dx = r (g - x r^2 mean(g x)), dweight = sum over rows and heads of n x r.
  *   grad_q_out / grad_k_out, dq / dk: of dtype, rows of their own strides; dq / dk may be grad_q_out / grad_k_out (same stride).
- *   dq_weight, dk_weight [head_dim] fp32 (dk_weight untouched without k): overwritten, the same bits for the same inputs.
+ *   dq_weight, dk_weight [head_dim] fp32 (dk_weight untouched without k or with n_k_heads 0): overwritten, the same bits for the same inputs.
  *   workspace: dflash_qk_norm_rope_workspace() bytes, 256-byte aligned; calls that may overlap need one each. */
 dflash_status dflash_qk_norm_rope(void *stream, const dflash_rope *rope, int32_t rows, int32_t n_q_heads,
                                   int32_t n_k_heads, int32_t head_dim, dflash_dtype dtype, const int32_t *positions,

@@ -843,3 +843,23 @@ def test_two_calls_at_once_long():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(x, y) for r in got[i] for x, y in zip(r, sets[i][4]))
+
+
+# ---------------------------------------------------------------- further ends of the ranges
+@pytest.mark.parametrize("rows", [0, 5])
+def test_norm_gradient_of_no_key_heads(rows):
+    """k of no heads: its weight's gradient is a sum over nothing, zeros, in memory that held something else."""
+    from block_diffusion_speculative_inject_gb300 import Rope, qk_norm_rope, qk_norm_rope_backward
+    g = torch.Generator().manual_seed(2)
+    q, gq = (torch.randn((rows, 2, 64), generator=g).cuda() for _ in range(2))
+    none, w, pos = torch.empty((rows, 0, 64), device="cuda"), torch.ones(64, device="cuda"), _i4(list(range(rows)))
+    t = Rope(64)
+    out = qk_norm_rope(t, pos, q, none, w, w)
+    assert out[1].shape == (rows, 0, 64)
+    want = qk_norm_rope_backward(t, pos, q, None, w, None, gq, None)
+    for _ in range(4):
+        held = [torch.full((64,), 7.0, device="cuda") for _ in range(64)]            # what the next ones are made of
+        del held
+        dq, dk, dqw, dkw = qk_norm_rope_backward(t, pos, q, none, w, w, gq, none)
+        assert torch.equal(dq, want[0]) and torch.equal(dqw, want[2]) and dk.shape == (rows, 0, 64)
+        assert bool((dkw == 0).all())
