@@ -863,3 +863,97 @@ def test_norm_gradient_of_no_key_heads(rows):
         dq, dk, dqw, dkw = qk_norm_rope_backward(t, pos, q, none, w, w, gq, none)
         assert torch.equal(dq, want[0]) and torch.equal(dqw, want[2]) and dk.shape == (rows, 0, 64)
         assert bool((dkw == 0).all())
+
+
+def test_attention_blocks_whole_lists_in_tiles():
+    """Every block listed, in the kernel for many rows. With one tile of rows for a request and head, and without a causal mask,
+    the line is cut in the same places as over the whole context, so the bits are its bits. Of several tiles of causal rows a
+    listed item is as long for every tile, one over the whole context ends with its tile's last row, so the cuts differ."""
+    from block_diffusion_speculative_inject_gb300 import kv8_attention
+    for hd, group, n_q, mask, ctx in ((64, 4, [20, 20], "causal", [9000, 300]), (128, 8, [16, 9], "causal", [5000, 641]),
+                                      (128, 2, [64, 3], "causal", [64, 4000]), (64, 4, [150, 90], "none", [3000, 1100]),
+                                      (128, 8, [200, 40], "tree", [2000, 900]),
+                                      (64, 4, [150, 90], "causal", [3000, 1100])):
+        c, table, q, cu, tree = _attn_case(n_q[0] + hd, ctx, n_q, 2, hd, 2 * group, mask, torch.bfloat16)
+        whole = torch.full((2, 2, 150), -1, dtype=torch.int32)
+        for b in range(2):
+            whole[b, :, :R.pages_of(ctx[b])] = torch.arange(R.pages_of(ctx[b]), dtype=torch.int32)
+        gpu = _to_gpu(c)
+        out, lse = _check_blocks(c, table, q, cu, ctx, whole, mask, tree, torch.bfloat16, max(n_q), gpu=gpu)
+        full, flse = kv8_attention(gpu, q.cuda(), _i4(cu), _i4(ctx), table.cuda(), mask=mask, max_q=max(n_q), want_lse=True,
+                                   tree_mask=None if tree is None else tree.cuda())
+        if mask != "causal" or max(n_q) * group <= 128:
+            assert torch.equal(out, full.cpu()) and torch.equal(lse, flse.cpu())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_gradient_far_offsets(dtype):
+    """Rows so far apart that the last ones lie past 2^31 elements of q, k, their gradients and the outputs, each with a
+    stride of its own; the places between the rows stay as they are."""
+    from block_diffusion_speculative_inject_gb300 import Rope, qk_norm_rope, qk_norm_rope_backward
+    if torch.cuda.mem_get_info()[0] < 70 << 30:
+        pytest.skip("needs 70 GB")
+    rows, nq, nk, hd = 131, 3, 2, 64
+    table, freq, mag, pos, x = _norm_case(9, rows, nq, nk, hd, 32, False, "yarn", dtype)
+    eps = 1e-6
+
+    def far(values, stride):
+        assert (rows - 1) * stride > 2 ** 31
+        buf = torch.empty(rows * stride, dtype=dtype, device="cuda")
+        t = buf.view(rows, stride)
+        edge = values.shape[1] * hd
+        t[:, edge:edge + 8] = 5
+        v = t[:, :edge].unflatten(1, (values.shape[1], hd))
+        v.copy_(values)
+        return t[:, edge:edge + 8], v
+
+    step = (1 << 24) + (1 << 18)
+    edges, t = {}, {}
+    for i, name in enumerate(("q", "k", "dq", "dk")):
+        edges[name], t[name] = far(x[name], step + 64 * i)
+    w = [x[n].cuda() for n in ("wq", "wk")]
+    qo, ko = qk_norm_rope(table, pos.cuda(), t["q"], t["k"], *w, eps=eps)
+    args = (pos, 32, freq, mag, False, eps)
+    _check_norm(qo, x["q"], x["wq"], *args)
+    _check_norm(ko, x["k"], x["wk"], *args)
+    # a lane adds at most 131 rows' terms of a head, as if one CTA held them all; then 8 warps, 5 shuffles, 19 CTAs' and 5 more
+    chain = rows * max(nq, nk) + 8 + 5 + 19 + 5
+    _, _, dqw, dkw = qk_norm_rope_backward(table, pos.cuda(), t["q"], t["k"], *w, t["dq"], t["dk"], eps=eps, dq=t["dq"], dk=t["dk"])
+    _check_grad(t["dq"], dqw, x["q"], x["wq"], x["dq"], *args, chain)
+    _check_grad(t["dk"], dkw, x["k"], x["wk"], x["dk"], *args, chain)
+    assert torch.equal(t["q"].cpu(), x["q"]) and torch.equal(t["k"].cpu(), x["k"])
+    assert all(bool((e == 5).all()) for e in edges.values())
+    del t, edges
+    torch.cuda.empty_cache()
+
+
+def test_norm_gradient_long_sums():
+    """Several hundred thousand rows of small heads: the weights' gradients are sums of a million terms, in chains of a CTA's
+    share of the rows."""
+    from block_diffusion_speculative_inject_gb300 import Rope, qk_norm_rope_backward
+    rows, nq, nk, hd = 400003, 2, 1, 32
+    g = torch.Generator(device="cuda").manual_seed(12)
+    pos = torch.randint(0, 5000, (rows,), generator=g, dtype=torch.int32, device="cuda")
+    # (terms that do not cancel: the products of a dim have a mean)
+    q, k = (torch.randn((rows, h, hd), generator=g, device="cuda") + 0.5 for h in (nq, nk))
+    gq, gk = (torch.randn((rows, h, hd), generator=g, device="cuda") + 0.25 for h in (nq, nk))
+    w = torch.randn(hd, generator=g, device="cuda")
+    dq, dk, dqw, dkw = qk_norm_rope_backward(Rope(hd, rot_dim=16), pos, q, k, w, w, gq, gk)
+    freq, mag = R.rope_freq(16, 1e6)
+    args = (pos.cpu(), 16, freq, mag, False, 1e-6)
+    # 304 CTAs; a lane adds one head's terms of some of its CTA's rows, all of them at most; then warps, shuffles, CTAs
+    chain = -(-rows // 304) * nq + 8 + 5 + 10 + 5
+    _check_grad(dq, dqw, q.cpu(), w.cpu(), gq.cpu(), *args, chain)
+    _check_grad(dk, dkw, k.cpu(), w.cpu(), gk.cpu(), *args, chain)
+
+
+def test_compact_most_layers():
+    """128 layers in one call, the most: each as alone."""
+    from block_diffusion_speculative_inject_gb300 import KV8Layers, kv8_compact
+    base, counts = [70, 3], [9, 6]
+    caches, table, keep = _compact_case(21, base, 20, counts, 1, 64, layers=128)
+    gpus = [_to_gpu(c) for c in caches]
+    kv8_compact(KV8Layers(gpus), table.cuda(), _i4(base), keep.cuda(), _i4(counts))
+    for c, gpu in zip(caches, gpus):
+        L.compact(c, table, base, keep, counts)
+        _same_cache(gpu, c)
