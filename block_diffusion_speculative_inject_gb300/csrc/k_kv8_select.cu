@@ -190,7 +190,12 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
 // of a CTA's rows are loaded at once.
 constexpr int KS_THREADS = 256;
 constexpr int KS_TILE = KS_THREADS / 2;               // blocks of a CTA at once: 16 of a warp
-constexpr int KS_ROWS = 80;                           // rows of q staged at once: 40 KB
+// Rows of q staged at once: 16 rows of the most heads to a kv head, 8. More rows take another round, which reads the table
+// and converts the bounds again. 8 x 16 rows over 1024 .. 2049 blocks with 80, 96 and 128: 48.7, 49.2 and 43.4 us for 8
+// heads to a kv head, 46.0, 46.2 and 40.1 for 7, 33.3, 33.5 and 33.6 for 5; 16 single tokens over 513 blocks 14.9, 14.9 and 15.3.
+constexpr int KS_ROWS = 128;
+template <int HD>
+constexpr size_t KS_SMEM = (size_t)KS_ROWS / 8 * (HD / 16) * 32 * sizeof(uint4) + KS_ROWS * sizeof(float);
 
 struct SelectArgs {
   Kv8AttnArgs a;
@@ -231,8 +236,9 @@ struct Vec4<float> {
 template <typename T, int HD>
 __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x) {
   constexpr int KS = HD / 16, C = HD / 64;
-  __shared__ uint4 qf[KS_ROWS / 8][KS][32];            // fragments of q+ and of q-
-  __shared__ float unit[KS_ROWS];                      // 0: a row that has no say
+  extern __shared__ uint4 ks_smem[];
+  uint4(*qf)[KS][32] = (uint4(*)[KS][32])ks_smem;      // [KS_ROWS / 8]: fragments of q+ and of q-
+  float *unit = (float *)(qf + KS_ROWS / 8);           // [KS_ROWS], 0: a row that has no say
   const Kv8AttnArgs &a = x.a;
   pdl_trigger();
   pdl_wait();
@@ -489,16 +495,20 @@ bool choice_ok(const dflash_kv8_cache *c, const dflash_kv8_choice *x) {
   return (int64_t)x->n_req * c->n_kv_heads * x->n_select < (1ll << 31) &&
          x->q_stride >= (int64_t)x->n_q_heads * c->head_dim && x->q_stride % (16 / dtype_bytes(x->dtype)) == 0;
 }
+template <typename T, int HD>
+cudaError_t launch_scores(const SelectArgs &x, dim3 g, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(k_kv8_scores<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)KS_SMEM<HD>);
+  return e != cudaSuccess ? e : launch_pdl(k_kv8_scores<T, HD>, g, dim3(KS_THREADS), KS_SMEM<HD>, s, x);
+}
 template <typename T>
 cudaError_t launch_select(const SelectArgs &x, int hd, cudaStream_t s) {
   // CTAs of a (request, kv head), which take KS_TILE blocks at a time in turn: as many as are resident (64 items over
   // 1024 .. 2049 blocks with 2 each 43.5 us, 4 34.4, 5 36.2, 8 37.2, 17 40.8: each makes q's whole numbers for itself)
   const long items = (long)x.a.n_req * x.a.nkv, want = items < 304 ? 304 / items : 1;
   const long most = ((long)x.a.width + KS_TILE - 1) / KS_TILE;
-  const dim3 g((unsigned)(want < most ? want : most), x.a.nkv, x.a.n_req), t(KS_THREADS);
+  const dim3 g((unsigned)(want < most ? want : most), x.a.nkv, x.a.n_req);
   cudaError_t e = cudaSuccess;
-  if (x.a.width > x.n_select)
-    e = hd == 128 ? launch_pdl(k_kv8_scores<T, 128>, g, t, 0, s, x) : launch_pdl(k_kv8_scores<T, 64>, g, t, 0, s, x);
+  if (x.a.width > x.n_select) e = hd == 128 ? launch_scores<T, 128>(x, g, s) : launch_scores<T, 64>(x, g, s);
   if (e == cudaSuccess) e = launch_pdl(k_kv8_choose, dim3(x.a.nkv, x.a.n_req), dim3(KC_THREADS), 0, s, x);
   return e;
 }

@@ -957,3 +957,13 @@ def test_compact_most_layers():
     for c, gpu in zip(caches, gpus):
         L.compact(c, table, base, keep, counts)
         _same_cache(gpu, c)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n_q,group", [(16, 8), (17, 8), (19, 7), (32, 8), (33, 8), (26, 5)])
+def test_select_rows_about_a_round(hd, n_q, group):
+    """As many rows as are staged at once (128), a few more, and two rounds of them, for one request and for ragged ones."""
+    for ctx, n in (([2000], [n_q]), ([1500, 700, 900, 640], [n_q, 1, 0, n_q - 1])):
+        table, bound, scale, q, cu = _choice_case(n_q + hd, ctx, n, 2, hd, group, torch.bfloat16)
+        got = _choose(table, bound, scale, q, cu, ctx, 6, 1, 0).cpu()
+        assert torch.equal(got, L.select(q, cu, ctx, table, bound, scale, 6, 1, 0))
