@@ -21,8 +21,6 @@ struct BoundsArgs {
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *(const __half2 *)&x; }
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *(const __nv_bfloat162 *)&x; }
-// bytes 0x7f / 0xff of a word, as 0x80 in each
-__device__ __forceinline__ uint32_t nan_bytes_of(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 template <int HD>
 __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
@@ -125,7 +123,7 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
         most[j] = __hmax2(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
       }
       const uint32_t l = *(const uint32_t *)&least[j], m = *(const uint32_t *)&most[j];
-      nan |= nan_bytes_of(l) | nan_bytes_of(m);
+      nan |= nan_bytes(l) | nan_bytes(m);
       out[j] = up ? m : l;
     }
     if (__any_sync(0xffffffffu, (nan & 0x80008000u) != 0)) {
@@ -205,11 +203,6 @@ struct SelectArgs {
   int32_t *blocks;
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // four signed bytes as two f16 pairs: byte + 128 in the low bits of 1024 + .., less 1152
 __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
   const uint32_t u = w ^ 0x80808080u;
@@ -331,8 +324,8 @@ __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const uint4 q = qf[at[z]][k][lane];
-            mma_16816(up[z], hi[k], q.x, q.y);
-            mma_16816(dn[z], lo[k], q.z, q.w);
+            mma_f16(up[z], hi[k], q.x, q.y);
+            mma_f16(dn[z], lo[k], q.z, q.w);
           }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
