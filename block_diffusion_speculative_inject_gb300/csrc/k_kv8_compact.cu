@@ -3,9 +3,12 @@
 // A CTA per (request, kv head, layer, K or V) takes the pages that rows go to one after another, from the first: a row
 // goes to its own place or below, so a page's rows come from that page or later ones, and none that is still to
 // be read has been written. Per page: the rows' bytes go to shared memory with their pages' scales, the largest
-// value gives the page's scale as the append's does, and the bytes are written anew. It is all latency (lengths, the rows'
-// places, their pages, their bytes): 4.6 us for 8 rows of one layer of 8 x 128, 24 us for 8 paths of 1 .. 16 rows in 32 layers,
-// whose 4096 CTAs are not quite two waves (49 us with 256 threads a CTA that went over the whole page).
+// value gives the page's scale as the append's does, and the bytes are written anew. 8 rows of one layer of 8 x 128 take 4.6 us,
+// all latency: lengths, the rows' places, their pages, their bytes. 8 paths of 1 .. 16 rows in 32 layers take 24 us (49 with 256
+// threads a CTA that went over the whole page). A page of V keeps the 64 tokens of a dim together, so that a row's 128 values
+// lie in as many sectors of 32 bytes: the 67 rows are 9 MB to read and write, their sectors 58 MB (9 us at the copy
+// rate; 64 MB by the counters). The rest is that chain, which each of 4096 CTAs goes through for itself in 1.7 waves, though
+// its first links are the same for all layers, heads, K and V. 200 rows of each request take 235 us, 48 in one layer.
 #include "kv8.cuh"
 
 namespace dflash {

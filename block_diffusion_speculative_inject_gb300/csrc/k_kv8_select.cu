@@ -6,9 +6,11 @@ namespace dflash {
 
 // ---------------------------------------------------------------- bounds
 // A warp per (page, kv head): lanes read 16 bytes of a row each, several rows at a time, and keep the least and the
-// largest of their 16 dims. The read of the pages and the instructions (two minima and two maxima a word) bound it about
-// alike: 47 us for 8 prompts of 16384 .. 32768 tokens of 8 x 128 (201 MB of keys, 4.6 TB/s); 65 with a conversion of every
-// pair to f16, 56 with shifts and masks in its place.
+// largest of their 16 dims. 47 us for 8 prompts of 16384 .. 32768 tokens of 8 x 128 (208 MB of keys, 215 with the bounds
+// and the tables, 4.6 TB/s); 65 with a conversion of every pair to f16, 56 with shifts and masks in its place. What is left
+// is latency (45% of the issue slots, 58% of DRAM, and 12 of a warp's 16 cycles an instruction are the wait for its
+// rows): a page of a head is a chain of its own, table entry, rows, shuffles, store. More of them hide it better: 8 x 16384
+// tokens take 33 us, the next 8 x 16384 24.5 (5.6 TB/s).
 constexpr int KB_THREADS = 256;
 constexpr int KB_CTAS = 152 * 4;
 
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
     }
     __syncwarp();
     uint32_t nan = 0;
-    uint32_t out[8];                                   // the least (the largest) of dims 2 j and 2 j + 1 in the second (fourth) byte
+    uint32_t out[8];                                   // the least (the largest) of dims 4 (j / 2) + (j & 1) and two further, in the second and fourth byte
     const bool up = lane >= LPR;                       // the first row's lanes write the least, the second's the largest
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

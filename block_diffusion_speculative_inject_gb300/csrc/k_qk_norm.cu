@@ -12,8 +12,11 @@
 // of a row (219 us when every head read them from shared memory, four lanes to a bank), copies ahead through shared memory,
 // paired arithmetic and packed conversions (248 without these two), as many CTAs as are resident (146 with a third more), and
 // no more copies ahead than two (142 with one, 138 with four: the shared memory is the first-level cache's). The gradient
-// keeps both weights' sums, 128 registers for two CTAs per SM (110 us at 154 registers and one CTA; 105 with three copies
-// ahead, 101 with two, 98 with half as many groups to a row).
+// keeps both weights' sums, 128 registers for two CTAs per SM, with 36 bytes spilled (110 us at 154 registers and one CTA; 105
+// with three copies ahead, 101 with two, 98 with half as many groups to a row).
+// 16384 rows of 40 x 128 take 58 us in bf16, 114 in fp32 (its gradient 161). Where the rotated dims, a stride or an address do not
+// keep a 16-byte boundary, every access is of two elements or of one, in instances sized for heads of 256: with 20
+// dims of 128 turned 174 us, and 255 for the gradient.
 #include <cmath>
 
 #include "rope.cuh"
@@ -413,8 +416,8 @@ cudaError_t launch_norm(NormArgs &a, int width, int *ctas, cudaStream_t s) {
   a.by_pairs = ((1u << 20) + a.rot / 2 - 1) / (a.rot / 2);
   constexpr int most = GRAD ? QN_CTAS_GRAD : QN_CTAS;
   // Groups of lanes that share a row: 8, for more than one row's angles at a time, 4 in the gradient (forward and gradient
-  // above with 4 129 and 98 us, with 8 128 and 101); all of them where that leaves too few CTAs, and no more than there
-  // are heads.
+  // above with 4 129 and 98 us, with 8 128 and 101); all of them where that leaves too few CTAs, and no more than the
+  // power of two that holds the heads.
   a.step = 1;
   while (a.step < per && a.step < heads && (a.step < (GRAD ? 4 : 8) || (int64_t)a.rows * a.step < (int64_t)most * per)) a.step *= 2;
   const int tile = per / a.step;

@@ -24,7 +24,7 @@ Calls run on the device of their tensors, on `stream` (default: that device's cu
 allocate outputs that are not given from torch's allocator. Arguments that do not fit raise
 DFlashError before anything is launched. None of them records a gradient, so with grad mode on a floating-point
 tensor that requires one is refused (rope's gradient is rope with transpose=True, qk_norm_rope's is
-qk_norm_rope_backward, for a Function of the caller's).
+qk_norm_rope_backward, for a Function of the caller's), but by kv8_select, whose answer is whole numbers.
 """
 import ctypes
 import functools
@@ -452,7 +452,8 @@ def kv8_attention(cache, q, cu_q, ctx_len, block_table, mask="causal", tree_mask
     else; give it, for without it a batch of single tokens or short blocks goes to the kernel for many rows, which
     takes 1.1 to 3 times as long there. workspace: a uint8 tensor of kv8_workspace(...) bytes; allocated for the call if None.
     blocks: [n, kv heads, any] int32, the blocks of 64 tokens that each request and kv head reads, as kv8_select makes
-    them (dflash_kv8_attention_blocks); everything if None.
+    them (dflash_kv8_attention_blocks); everything if None. Of a list only the first entries count, as many as the context has
+    blocks, so those that name a block come first; a block is to be listed once.
     Returns out [rows, heads, head_dim], or (out, lse [rows, heads] fp32) with want_lse."""
     a = _attn_args(cache, q, cu_q, ctx_len, block_table, mask, tree_mask, scale, max_q, out, lse)
     _no_gradient("kv8_attention", q, out, lse)
@@ -507,8 +508,10 @@ def kv8_select(cache, bounds, q, cu_q, ctx_len, block_table, n_select, keep_firs
     """Chooses n_select blocks of 64 tokens of each request and kv head for kv8_attention(blocks=...)
     (dflash_kv8_select): the first keep_first, those of the request's own rows (the context's last) and keep_last before
     them, then by falling score, the largest product with a row of q that the key bounds allow (q rounded to 11 bits); ties
-    go to the lowest index. Arguments as kv8_attention's. Returns blocks [n, kv heads, n_select] int32, rising, -1 after the
-    last; out: a tensor for them. workspace: a uint8 tensor of kv8_select_workspace(...) bytes; allocated for the call if None."""
+    go to the lowest index. Where the first two kinds are more than n_select, the lowest are kept and the last rows do not see
+    themselves: keep_first + keep_last + (rows + 62) // 64 + 1 hold them all for a request of `rows` rows. Arguments as
+    kv8_attention's. Returns blocks [n, kv heads, n_select] int32, rising, -1 after the last; out: a tensor for them.
+    workspace: a uint8 tensor of kv8_select_workspace(...) bytes; allocated for the call if None."""
     a = _choice_args(cache, bounds, q, cu_q, ctx_len, block_table, n_select, keep_first, keep_last)
     shape = (a.n_req, cache.n_kv_heads, a.n_select)
     if out is not None:

@@ -967,3 +967,20 @@ def test_select_rows_about_a_round(hd, n_q, group):
         table, bound, scale, q, cu = _choice_case(n_q + hd, ctx, n, 2, hd, group, torch.bfloat16)
         got = _choose(table, bound, scale, q, cu, ctx, 6, 1, 0).cpu()
         assert torch.equal(got, L.select(q, cu, ctx, table, bound, scale, 6, 1, 0))
+
+
+def test_select_holds_a_requests_own_blocks():
+    """keep_first + keep_last + (rows + 62) // 64 + 1 blocks hold all that are kept in any case, wherever the rows begin in a
+    block; with one less there is a place where they do not fit, and the lowest stay."""
+    first, last = 1, 2
+    for rows in (1, 2, 63, 64, 65, 66, 129, 130):
+        ctx = [64 * 12 + rows + o for o in (0, 1, 62, 63)]
+        kept = [set(range(first)) | set(range((c - rows) // PAGE - last, R.pages_of(c))) for c in ctx]
+        most = first + last + (rows + 62) // PAGE + 1
+        assert max(len(x) for x in kept) == most
+        table, bound, scale, q, cu = _choice_case(rows, ctx, [rows] * 4, 1, 64, 2, torch.bfloat16)
+        for k in (most, most - 1):
+            got = _choose(table, bound, scale, q, cu, ctx, k, first, last).cpu()
+            for b in range(4):
+                have = sorted(kept[b])[:k]
+                assert set(have) <= set(got[b, 0].tolist()) and (len(kept[b]) <= k or got[b, 0].tolist() == have)
