@@ -484,7 +484,8 @@ extern "C" dflash_status dflash_qk_norm_rope(void *stream, const dflash_rope *ro
   const int n = nk ? 6 : 3;
   for (int i = 0; i < n; ++i)
     if (!f[i].p || !aligned(f[i].p, es)) return DFLASH_ERR_INVALID_ARG;
-  if ((q == q_out && q_stride != q_out_stride) || (nk && k == k_out && k_stride != k_out_stride))
+  if ((q == q_out && q_stride != q_out_stride) || (nk && k == k_out && k_stride != k_out_stride) ||
+      (nk && (q_out == k || q_out == k_out || k_out == q)))
     return DFLASH_ERR_INVALID_ARG;
   NormArgs a = norm_args(rope, rows, n_q_heads, nk, head_dim, eps, positions);
   a.qw = q_weight, a.kw = k_weight;
@@ -519,7 +520,9 @@ extern "C" dflash_status dflash_qk_norm_rope_backward(void *stream, const dflash
     if (!x->positions || !aligned(x->positions, 4)) return DFLASH_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i)
       if (!f[i].p || !aligned(f[i].p, es)) return DFLASH_ERR_INVALID_ARG;
-    if (x->dq == x->q || (nk && x->dk == x->k) || (x->dq == x->grad_q_out && x->dq_stride != x->grad_q_out_stride) ||
+    if (x->dq == x->q ||
+        (nk && (x->dk == x->k || x->dk == x->q || x->dk == x->grad_q_out || x->dq == x->k || x->dq == x->grad_k_out || x->dq == x->dk)) ||
+        (x->dq == x->grad_q_out && x->dq_stride != x->grad_q_out_stride) ||
         (nk && x->dk == x->grad_k_out && x->dk_stride != x->grad_k_out_stride))
       return DFLASH_ERR_INVALID_ARG;
   }

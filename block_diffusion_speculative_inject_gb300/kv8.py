@@ -342,14 +342,25 @@ def _like(name, t, ref, own):
     return stride
 
 
+def _not_over(name, t, **others):
+    """Refuses an output `t` in the place of another tensor of the call."""
+    if t is not None and t.numel():
+        for other, x in others.items():
+            if x is not None and x.data_ptr() == t.data_ptr():
+                raise _error(f"{name} must not be {other}")
+
+
 def qk_norm_rope(table, positions, q, k, q_weight, k_weight, eps=1e-6, q_out=None, k_out=None, stream=None):
     """Per-head RMSNorm and rotation in one pass (dflash_qk_norm_rope): every head of q [rows, heads, head_dim] and
     (unless None) k becomes the rotation of x / sqrt(mean(x^2) + eps) * weight by its row's position. q_weight, k_weight
     [head_dim] of q's type. Rows may be strided. q_out / k_out: new tensors if None; q / k themselves work in
-    place. Returns (q_out, k_out)."""
+    place, and no output may overlap anything else. Returns (q_out, k_out)."""
     rows, nq, qs, nk, ks, eps = _norm_args(table, positions, q, k, q_weight, k_weight, eps)
     hd = table.head_dim
     qos, kos = _like("q_out", q_out, q, q), _like("k_out", k_out, k, k)
+    if q_out is not None or k_out is not None:
+        _not_over("q_out", q_out, k=k, k_out=k_out)
+        _not_over("k_out", k_out, q=q)
     _no_gradient("qk_norm_rope", q, k, q_weight, k_weight, q_out, k_out)
     dev = _device(q, k, positions, q_weight, k_weight, q_out, k_out)
 
@@ -375,7 +386,7 @@ def qk_norm_rope_backward(table, positions, q, k, q_weight, k_weight, grad_q_out
                           workspace=None, stream=None):
     """The gradients of qk_norm_rope's q, k and weights from those of its outputs (dflash_qk_norm_rope_backward); q and
     k are its inputs as they were before it. dq / dk: new tensors if None; grad_q_out / grad_k_out themselves work in
-    place. workspace: a uint8 tensor of qk_norm_rope_workspace() bytes; allocated for the call if None.
+    place, and no output may overlap anything else. workspace: a uint8 tensor of qk_norm_rope_workspace() bytes; allocated for the call if None.
     Returns (dq, dk, dq_weight, dk_weight), the last two [head_dim] fp32 (dk and dk_weight None without k)."""
     rows, nq, qs, nk, ks, eps = _norm_args(table, positions, q, k, q_weight, k_weight, eps)
     hd = table.head_dim
@@ -383,10 +394,9 @@ def qk_norm_rope_backward(table, positions, q, k, q_weight, k_weight, grad_q_out
         raise _error("grad_q_out goes with q and grad_k_out with k")
     gqs, gks = _like("grad_q_out", grad_q_out, q, None), _like("grad_k_out", grad_k_out, k, None)
     dqs, dks = _like("dq", dq, q, grad_q_out), _like("dk", dk, k, grad_k_out)
-    if rows and (dq is not None or dk is not None):
-        for x, y, name in ((dq, q, "dq"), (dk, k, "dk")):
-            if x is not None and x.data_ptr() == y.data_ptr():
-                raise _error(f"{name} must not be {name[1:]}, which is read for the weight's gradient")
+    if dq is not None or dk is not None:               # (q and k are read for the weights' gradients)
+        _not_over("dq", dq, q=q, k=k, grad_k_out=grad_k_out, dk=dk)
+        _not_over("dk", dk, k=k, q=q, grad_q_out=grad_q_out)
     if workspace is not None:
         _tensor("workspace", workspace, _U1, (None,))
     _no_gradient("qk_norm_rope_backward", q, k, q_weight, k_weight, grad_q_out, grad_k_out, dq, dk)

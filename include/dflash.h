@@ -438,16 +438,18 @@ dflash_status dflash_rope_apply(void *stream, const dflash_rope *rope, int32_t r
 
 /* Per-head RMSNorm of queries and keys with the rotary positions in the same pass: every head x [head_dim] of q
  * and of k becomes the rotation of x / sqrt(mean(x^2) + eps) * weight by its row's position. Arguments as
- * dflash_rope_apply's (q_out / k_out may be q / k themselves, with the same stride; k may be NULL, and k_weight then is not
- * read), q_weight and k_weight [head_dim] of `dtype`, eps > 0. Computed in fp32 from the stored values, rounded
- * once; the squares of a head are to fit fp32.
+ * dflash_rope_apply's (q_out / k_out may be q / k themselves, with the same stride, and overlap nothing else; k may be
+ * NULL, and k_weight then is not read), q_weight and k_weight [head_dim] of `dtype`, eps > 0. Computed in fp32 from the
+ * stored values, rounded once; the squares of a head are to fit fp32.
  *
  * dflash_qk_norm_rope_backward: the gradients of q, k and of both weights from those of q_out and k_out. q, k are the
  * call's inputs before it (an in-place call has overwritten them). With y the gradient of a head's output, R its rotation,
  *   n = R^T y, g = n * weight, r = 1 / sqrt(mean(x^2) + eps):
  *   dx = r (g - x r^2 mean(g x)), dweight = sum over rows and heads of n x r.
- *   grad_q_out / grad_k_out, dq / dk: of dtype, rows of their own strides; dq / dk may be grad_q_out / grad_k_out (same stride).
- *   dq_weight, dk_weight [head_dim] fp32 (dk_weight untouched without k or with n_k_heads 0): overwritten, the same bits for the same inputs.
+ *   grad_q_out / grad_k_out, dq / dk: of dtype, rows of their own strides; dq / dk may be grad_q_out / grad_k_out (same
+ *   stride) and overlap nothing else.
+ *   dq_weight, dk_weight [head_dim] fp32 (dk_weight untouched without k or with n_k_heads 0): overwritten, the same
+ *   bits for the same inputs.
  *   workspace: dflash_qk_norm_rope_workspace() bytes, 256-byte aligned; calls that may overlap need one each. */
 dflash_status dflash_qk_norm_rope(void *stream, const dflash_rope *rope, int32_t rows, int32_t n_q_heads,
                                   int32_t n_k_heads, int32_t head_dim, dflash_dtype dtype, const int32_t *positions,

@@ -263,3 +263,34 @@ def test_caches_stay_as_they_were_laid_out():
             delattr(c, name)
     assert [t.data_ptr() for t in c._tensors()] == was == [c._c.k_pages, c._c.v_pages, c._c.k_scale, c._c.v_scale]
     assert c.n_pages == c._c.n_pages == 4
+
+
+def test_norm_refuses_outputs_over_other_inputs(lib):  # noqa: F811
+    """In place is the same tensor in and out. An output over another one that is still to be read, or two outputs over one
+    another, would be a race: refused, at the C entries and in the binding, where the heads are as many."""
+    from block_diffusion_speculative_inject_gb300 import _ffi
+    t = _table(lib)
+
+    def forward(qo, ko, q=B, k=C):
+        return lib.dflash_qk_norm_rope(None, ctypes.byref(t), 2, 2, 2, 64, 1, A, 1e-6, G, H, q, 128, k, 128, qo, 128, ko, 128)
+    for qo, ko in ((C, E), (C, C), (D, B), (C, B), (D, D)):
+        assert forward(qo, ko) == -1
+    p = [32768 + 4096 * i for i in range(11)]
+    pos, qw, kw, q, k, gq, gk, dq, dk, dqw, dkw = p
+
+    def backward(dq, dk):
+        x = _ffi.QKNormRopeGrad(2, 2, 2, 64, 1, 1e-6, pos, qw, kw, q, k, gq, gk, 128, 128, 128, 128, dq, dk, 128, 128, dqw, dkw, A, 1 << 30)
+        return lib.dflash_qk_norm_rope_backward(None, ctypes.byref(t), ctypes.byref(x))
+    for a, b in ((k, dk), (gk, dk), (dk, dk), (dq, q), (dq, gq), (gk, gq), (q, dk), (dq, k)):
+        assert backward(a, b) == -1
+    pkg, i4, e4, bf, cache = _things()
+    x = [bf(3, 2, 64) for _ in range(6)]
+    norm = lambda **kw: pkg.qk_norm_rope(pkg.Rope(64), i4(3), x[0], x[1], bf(64), bf(64), **kw)  # noqa: E731
+    grad = lambda **kw: pkg.qk_norm_rope_backward(pkg.Rope(64), i4(3), x[0], x[1], bf(64), bf(64), x[2], x[3], **kw)  # noqa: E731
+    for f, over in ((norm, dict(q_out=x[1])), (norm, dict(k_out=x[0])), (norm, dict(q_out=x[4], k_out=x[4])), (grad, dict(dq=x[1])),
+                    (grad, dict(dk=x[0])), (grad, dict(dq=x[3])), (grad, dict(dk=x[2])), (grad, dict(dq=x[4], dk=x[4]))):
+        with pytest.raises(pkg.DFlashError, match="must not be"):
+            f(**over)
+    for f, over in ((norm, dict(q_out=x[0], k_out=x[1])), (grad, dict(dq=x[2], dk=x[3])), (grad, dict(dq=x[4], dk=x[5]))):
+        with pytest.raises(pkg.DFlashError, match="CUDA device"):
+            f(**over)
