@@ -184,15 +184,16 @@ __global__ void __launch_bounds__(KB_THREADS) k_kv8_bounds(const BoundsArgs a) {
 // truncates) holds. Contraction indices are permuted as in the attention for few rows: a lane's 16 bytes are the dims of
 // four steps.
 //
-// The bounds are few bytes (26 MB for 8 x 16 rows of 40 heads over 1024 .. 2049 blocks, 4 us), and what takes 26 us there are
+// The bounds are few bytes (26 MB for 8 x 16 rows of 40 heads over 1024 .. 2049 blocks, 4 us), and what takes 25 us there are
 // the latencies of a round (table, bounds, the products' chains of sums) with 16 warps per SM, and the reads of q's
 // fragments from shared memory. Both halves of q are kept there (46 us when they were made at every use), and all
 // of a CTA's rows are loaded at once.
 constexpr int KS_THREADS = 256;
 constexpr int KS_TILE = KS_THREADS / 2;               // blocks of a CTA at once: 16 of a warp
 // Rows of q staged at once: 16 rows of the most heads to a kv head, 8. More rows take another round, which reads the table
-// and converts the bounds again. 8 x 16 rows over 1024 .. 2049 blocks with 80, 96 and 128: 48.7, 49.2 and 43.4 us for 8
-// heads to a kv head, 46.0, 46.2 and 40.1 for 7, 33.3, 33.5 and 33.6 for 5; 16 single tokens over 513 blocks 14.9, 14.9 and 15.3.
+// and converts the bounds again. 8 x 16 rows over 1024 .. 2049 blocks with 80, 96 and 128: 47.8, 48.1 and 41.8 us for 8
+// heads to a kv head, 44.9, 45.3 and 38.8 for 7, 32.6, 32.7 and 32.7 for 5; 16 single tokens over 513 blocks 14.9, 15.0 and
+// 15.1. (A 64-bit division a row instead of the product took 0.9 us of the first three.)
 constexpr int KS_ROWS = 128;
 template <int HD>
 constexpr size_t KS_SMEM = (size_t)KS_ROWS / 8 * (HD / 16) * 32 * sizeof(uint4) + KS_ROWS * sizeof(float);
@@ -243,19 +244,22 @@ __global__ void __launch_bounds__(KS_THREADS, 2) k_kv8_scores(const SelectArgs x
   if (r.n == 0 || blocks <= x.n_select || blockIdx.x * KS_TILE >= blocks) return;
   const long long rows = (long long)r.n * group;
   float *score = x.score + ((size_t)b * a.nkv + h) * a.width;
+  const uint32_t inv_group = 65536u / group + 1;       // (exact for the 135 rows and 8 heads at most that it is used for)
   for (long long r0 = 0; r0 < rows; r0 += KS_ROWS) {
     // q in whole numbers: HD / 4 lanes a row, four dims each
     constexpr int LPR = HD / 4, N = KS_ROWS * LPR / KS_THREADS;
     const int here = (int)min((long long)KS_ROWS, rows - r0), tiles = (here + 7) / 8;
     const int i0 = threadIdx.x / LPR, l = threadIdx.x % LPR;
     typedef Vec4<T> Q4;
+    const long long token0 = r0 / group;
+    const int rest = (int)(r0 - token0 * group);
+    const T *q0 = (const T *)a.q + (r.row0 + token0) * a.q_stride + (int64_t)h * group * HD + 4 * l;
     Q4 in[N];                                         // all loads first
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int i = i0 + n * (KS_THREADS / LPR);
-      const long long row = r0 + i;
-      in[n] = i < here ? *(const Q4 *)((const T *)a.q + (r.row0 + row / group) * a.q_stride + (int64_t)(h * group + row % group) * HD + 4 * l)
-                       : Q4{};
+      const int token = (int)((uint32_t)(rest + i) * inv_group >> 16);          // (rest + i) / group
+      in[n] = i < here ? *(const Q4 *)(q0 + token * a.q_stride + (rest + i - token * group) * HD) : Q4{};
     }
     __syncthreads();
 #pragma unroll
